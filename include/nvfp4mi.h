@@ -462,6 +462,160 @@ int nvfp4_quantlinear_forward(const uint16_t* x, int64_t tokens, int64_t k, int6
                               int64_t ldw, uint16_t* y, int64_t ldy, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * Products of packed 4-bit matrices, the MXFP4 quantizer that feeds one of
+ * them, and a mixture-of-experts layer over NVFP4 experts.
+ *
+ * Their status must be looked at: NVFP4_CHECKED makes a compiler warn where
+ * the value is dropped.
+ */
+#if defined(__GNUC__)
+#define NVFP4_CHECKED __attribute__((warn_unused_result))
+#else
+#define NVFP4_CHECKED
+#endif
+
+/*
+ * MXFP4 quantizer: E2M1 elements and one E8M0 scale 2^(code-127) per 32
+ * consecutive elements ("从MXFP4到NVFP4：Model Optimizer混合精度格式转换完全攻略"
+ * §1 describes the format; the scale rule is that of the OCP Microscaling
+ * specification v1.0 §6.3, the largest power of two at or below the block max
+ * over that of the element format).  Per block, with amax = max |x|:
+ *   code = max(floor(log2 amax) - 2 + 127, 0)     (0 for an all-zero block)
+ *   nib  = E2M1 code of x / 2^(code-127), nearest, ties to even, saturated
+ * A block that holds an infinity or NaN gets code 255 (NaN) and zero nibbles.
+ * The result is what mxfp4_to_nvfp4_cast takes.
+ *
+ * x       [rows][ldx] bf16, columns 0..k-1, k % 32 == 0; 16-byte aligned rows.
+ * packed  [rows][k/2] uint8 out, contiguous, 16-byte aligned.
+ * e8m0    [rows][k/32] uint8 out, contiguous, 16-byte aligned.
+ * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED, HIP.
+ */
+NVFP4_CHECKED int mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx,
+                                 uint8_t* packed, uint8_t* e8m0, void* stream);
+
+/*
+ * out[r][i] = RN_bf16(e2m1(nibble) * 2^(code-127)): exact but for magnitudes
+ * of 2^128 and more, which become infinite.  Code 255 gives NaN.
+ * packed [rows][k/2], e8m0 [rows][k/32] and out [rows][k] bf16: contiguous,
+ * 16-byte aligned; k % 32 == 0.
+ * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED, HIP.
+ */
+NVFP4_CHECKED int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows,
+                                int64_t k, uint16_t* out, void* stream);
+
+/*
+ * Product of two MXFP4 matrices (the weights as Linear [out][in]):
+ *   y[t][o] = RN_bf16( sum_k xh[t][k] wh[o][k] ),
+ * xh, wh the exact values e2m1 * 2^(code-127); products are exact and summed
+ * in fp32 on the scaled FP4 matrix instructions.  Code 255 (NaN) makes every
+ * output of its row or column NaN.
+ *
+ * x_packed [tokens][k/2], x_e8m0 [tokens][k/32], w_packed [out_features][k/2],
+ * w_e8m0 [out_features][k/32]: uint8, contiguous, 16-byte aligned;
+ * k % 32 == 0; tokens, out_features and k below 2^31.
+ * y          [tokens][ldy] bf16, columns 0..out_features-1; any ldy >=
+ *            out_features (other columns are left as they were).
+ * workspace  16-byte aligned, at least mxfp4_matmul_workspace_bytes(tokens,
+ *            out_features, k) bytes (the query returns 0 where none is needed;
+ *            workspace may then be NULL); scratch.  Results do not depend on
+ *            what it held, and are the same bits on every call.
+ * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED, WORKSPACE, HIP.
+ */
+NVFP4_CHECKED size_t mxfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k);
+NVFP4_CHECKED int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, int64_t tokens,
+                               int64_t k, const uint8_t* w_packed, const uint8_t* w_e8m0,
+                               int64_t out_features, uint16_t* y, int64_t ldy, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Products with an NVFP4 weight as nvfp4_scale_sweep, nvfp4_quantize_dynamic
+ * or mxfp4_to_nvfp4_cast leave it ("Coder390 NVFP4 校正（校准）方式" §3, the
+ * W4A16 and W4A4 tiers):
+ *   w4a16:  y[t][o] = RN_bf16( w_scale2 * sum_k x[t][k] v[o][k] ),  x in bf16
+ *   w4a4:   y[t][o] = RN_bf16( w_scale2 * x_scale2 * sum_k u[t][k] v[o][k] )
+ * with v = e2m1 * e4m3(code) of w, u the same of x: exact operands, summed in
+ * fp32.  (nvfp4_quantlinear_forward rounds its operands to bf16 after scale_2;
+ * these do not.)  Code 0x7F (NaN) makes the outputs it enters NaN.
+ *
+ * x          w4a16: [tokens][ldx] bf16, columns 0..k-1, 16-byte aligned rows.
+ * x_packed, x_codes  w4a4: [tokens][k/2], [tokens][k/16].
+ * w_packed, w_codes  [out_features][k/2], [out_features][k/16].  All packed
+ *            and code arrays: uint8, contiguous, 16-byte aligned; k % 16 == 0;
+ *            tokens, out_features and k below 2^31.
+ * x_scale2, w_scale2  device float[1].
+ * y, workspace: as for mxfp4_matmul, with nvfp4_matmul_workspace_bytes (one
+ *            size serves both).
+ * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED, WORKSPACE, HIP.
+ */
+NVFP4_CHECKED size_t nvfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k);
+NVFP4_CHECKED int nvfp4_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx,
+                                     const uint8_t* w_packed, const uint8_t* w_codes,
+                                     const float* w_scale2, int64_t out_features, uint16_t* y,
+                                     int64_t ldy, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+NVFP4_CHECKED int nvfp4_matmul_w4a4(const uint8_t* x_packed, const uint8_t* x_codes,
+                                    const float* x_scale2, int64_t tokens, int64_t k,
+                                    const uint8_t* w_packed, const uint8_t* w_codes,
+                                    const float* w_scale2, int64_t out_features, uint16_t* y,
+                                    int64_t ldy, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * Router of a mixture-of-experts layer: the top_k largest logits of each
+ * token, largest first, the lower expert first among equals, and their
+ * softmax weights in fp32:
+ *   weight_s = exp(l_s - l_max) / sum over the chosen   (normalize = 1)
+ *                                  or over all experts  (normalize = 0).
+ * An expert whose logit is -infinity or NaN is not chosen; where fewer than
+ * top_k are left, the remaining places get id -1 and weight 0.  +infinity
+ * counts as the largest finite float.
+ *
+ * logits  [tokens][ldl] float, columns 0..experts-1.
+ * ids     [tokens][top_k] int32 out;  weights [tokens][top_k] float out.
+ * experts 1 .. 1024, top_k 1 .. 16 and at most experts.
+ * Errors: NULL_ARG, BAD_SHAPE, BAD_INPUT (experts, top_k or normalize out of
+ *         range), MISALIGNED (4 bytes), HIP.
+ */
+NVFP4_CHECKED int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl,
+                                  int top_k, int normalize, int32_t* ids, float* weights,
+                                  void* stream);
+
+/*
+ * Mixture-of-experts layer for a few tokens over NVFP4 experts in the layout
+ * mxfp4_to_nvfp4_cast writes ("从MXFP4到NVFP4：Model Optimizer混合精度格式转换完全
+ * 攻略" §3: w1 and w3 of an expert share one scale_2):
+ *   y[t] = RN_bf16( sum_s weights[t][s] W2_e ( silu(W1_e x[t]) * (W3_e x[t]) ) ),
+ * e = ids[t][s], silu(a) = a / (1 + exp(-a)), every W the exact NVFP4 value.
+ * Sums are in fp32; the product silu * up enters the second product as two
+ * bf16 parts (16 significant bits).  Results are the same bits on every call.
+ * An id outside 0..experts-1 (a place the router left empty, an expert that
+ * lives elsewhere) adds nothing; a token without any gets zeros.  An expert
+ * that a token names twice counts with both weights.
+ *
+ * x          [tokens][ldx] bf16, columns 0..hidden-1, 16-byte aligned rows.
+ * ids        [tokens][top_k] int32;  weights [tokens][top_k] float.
+ * w13_packed [experts][2][inter][hidden/2], w13_codes [experts][2][inter]
+ *            [hidden/16], w13_scale2 float[experts]: w1, then w3.
+ * w2_packed  [experts][hidden][inter/2], w2_codes [experts][hidden][inter/16],
+ *            w2_scale2 float[experts].  Packed and code arrays 16-byte aligned.
+ * y          [tokens][ldy] bf16, columns 0..hidden-1; any ldy >= hidden.
+ * tokens     0 .. 64;  top_k 1 .. 16;  experts 1 .. 1024.
+ * hidden, inter: multiples of 16 below 2^31.
+ * workspace  16-byte aligned, at least nvfp4_moe_workspace_bytes(tokens, top_k,
+ *            inter) bytes; scratch.
+ * Errors: NULL_ARG, BAD_SHAPE, BAD_INPUT (tokens, top_k or experts out of
+ *         range), MISALIGNED, WORKSPACE, HIP.
+ */
+NVFP4_CHECKED size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter);
+NVFP4_CHECKED int nvfp4_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t ldx,
+                                    const int32_t* ids, const float* weights, int64_t top_k,
+                                    int64_t experts, int64_t inter, const uint8_t* w13_packed,
+                                    const uint8_t* w13_codes, const float* w13_scale2,
+                                    const uint8_t* w2_packed, const uint8_t* w2_codes,
+                                    const float* w2_scale2, uint16_t* y, int64_t ldy,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

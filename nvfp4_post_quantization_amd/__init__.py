@@ -12,6 +12,12 @@ Functions (names as in the C ABI):
   quantize_dynamic(x, scale2)               -> (packed u8, codes u8)
   dequant(packed, codes, scale2)            -> bf16
   mxfp4_to_nvfp4_cast(packed, e8m0, want_fallback=True) -> (codes, scale2, fallback)
+  mxfp4_quantize(x) -> (packed u8, e8m0 u8);  mxfp4_dequant(packed, e8m0) -> bf16
+  mxfp4_matmul(x_packed, x_e8m0, w_packed, w_e8m0) -> bf16 x w^T
+  matmul_w4a16(x, w_packed, w_codes, w_scale2) -> bf16 x w^T
+  matmul_w4a4(x_packed, x_codes, x_scale2, w_packed, w_codes, w_scale2) -> bf16 x w^T
+  moe_route(logits, top_k) -> (ids i32, weights f32)
+  moe_forward(x, ids, weights, w13_packed, w13_codes, w13_scale2, w2_packed, w2_codes, w2_scale2) -> bf16
 """
 from __future__ import annotations
 
@@ -26,6 +32,8 @@ __all__ = [
     "hessian_accum_fq_chunks", "scale_sweep", "quantize_dynamic", "dequant", "mxfp4_to_nvfp4_cast",
     "fp8_compute_scale", "fp8_quantize", "fp8_dequant", "block_hadamard", "hessian_hadamard",
     "fakequant", "quantlinear_workspace_bytes", "quantlinear_forward", "scale_sweep_stats",
+    "mxfp4_quantize", "mxfp4_dequant", "mxfp4_matmul_workspace_bytes", "mxfp4_matmul", "matmul_workspace_bytes",
+    "matmul_w4a16", "matmul_w4a4", "moe_route", "moe_workspace_bytes", "moe_forward",
 ]
 
 # NVFP4MI_LIB names another build of the same library (the host-sanitizer
@@ -74,6 +82,22 @@ _SIGS = {
     "nvfp4_quantlinear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_quantlinear_forward": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _i64, _i64,
                                                  _c_void_p, _i64, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "mxfp4_quantize": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "mxfp4_dequant": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
+    "mxfp4_matmul_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "mxfp4_matmul": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, _c_void_p, _i64,
+                                    _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "nvfp4_matmul_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "nvfp4_matmul_w4a16": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64,
+                                          _c_void_p, _i64, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "nvfp4_matmul_w4a4": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                         _i64, _c_void_p, _i64, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "nvfp4_moe_route": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p,
+                                       _c_void_p]),
+    "nvfp4_moe_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "nvfp4_moe_forward": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _i64, _i64, _i64,
+                                         _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                         _i64, _c_void_p, ctypes.c_size_t, _c_void_p]),
 }
 
 _lib = None
@@ -537,3 +561,218 @@ def scale_sweep_stats(w: torch.Tensor, H: torch.Tensor, scale2: torch.Tensor, st
         w.data_ptr(), rows, k, ldw, H.data_ptr(), scale2.data_ptr(), packed.data_ptr(), codes.data_ptr(),
         stats.data_ptr(), _stream(w)))
     return packed, codes, stats
+
+
+def _flat(t: torch.Tensor, dtype, shape, name: str, device=None) -> torch.Tensor:
+    """A contiguous GPU tensor of one dtype and shape, on `device` when given."""
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor (got {list(t.shape)})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _scalar(t: torch.Tensor, name: str, device) -> torch.Tensor:
+    _dev(t, torch.float32, name)
+    if t.numel() < 1 or t.device != device:
+        raise ValueError(f"{name} must hold one float32 on {device}")
+    return t
+
+
+def _rows_out(out: torch.Tensor | None, rows: int, cols: int, device) -> torch.Tensor:
+    """The bf16 [rows, cols] output: made here, or checked."""
+    if out is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    _dev(out, torch.bfloat16, "out", 2)
+    if tuple(out.shape) != (rows, cols) or out.device != device:
+        raise ValueError(f"out must be [{rows}, {cols}] on {device}")
+    return out
+
+
+def _scratch(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _dev(workspace, torch.uint8, "workspace")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace
+
+
+def mxfp4_quantize(x: torch.Tensor, out=None):
+    """MXFP4 form of bf16 x[rows, k] (k % 32 == 0): (packed u8 [rows, k/2],
+    e8m0 u8 [rows, k/32]); out=(packed, e8m0) reuses buffers."""
+    _dev(x, torch.bfloat16, "x", 2)
+    rows, k = x.shape
+    ldx = _row_major(x, "x")
+    if out is None:
+        packed = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
+        e8m0 = torch.empty((rows, k // 32), dtype=torch.uint8, device=x.device)
+    else:
+        packed = _flat(out[0], torch.uint8, (rows, k // 2), "packed", x.device)
+        e8m0 = _flat(out[1], torch.uint8, (rows, k // 32), "e8m0", x.device)
+    with torch.cuda.device(x.device):
+        _check("mxfp4_quantize", load().mxfp4_quantize(
+            x.data_ptr(), rows, k, ldx, packed.data_ptr(), e8m0.data_ptr(), _stream(x)))
+    return packed, e8m0
+
+
+def mxfp4_dequant(packed: torch.Tensor, e8m0: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 [rows, k] of MXFP4 (packed u8 [rows, k/2], e8m0 u8 [rows, k/32])."""
+    _dev(packed, torch.uint8, "packed", 2)
+    rows, k = packed.shape[0], packed.shape[1] * 2
+    _flat(packed, torch.uint8, (rows, k // 2), "packed")
+    _flat(e8m0, torch.uint8, (rows, k // 32), "e8m0", packed.device)
+    if out is None:
+        out = torch.empty((rows, k), dtype=torch.bfloat16, device=packed.device)
+    _flat(out, torch.bfloat16, (rows, k), "out", packed.device)
+    with torch.cuda.device(packed.device):
+        _check("mxfp4_dequant", load().mxfp4_dequant(packed.data_ptr(), e8m0.data_ptr(), rows, k, out.data_ptr(),
+                                                     _stream(packed)))
+    return out
+
+
+def mxfp4_matmul_workspace_bytes(tokens: int, out_features: int, k: int) -> int:
+    return int(load().mxfp4_matmul_workspace_bytes(tokens, out_features, k))
+
+
+def mxfp4_matmul(x_packed: torch.Tensor, x_e8m0: torch.Tensor, w_packed: torch.Tensor, w_e8m0: torch.Tensor,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [tokens, out_features] bf16 = x w^T of two MXFP4 matrices (exact
+    products, fp32 sums, one rounding).  out may have any row stride;
+    workspace: uint8, at least mxfp4_matmul_workspace_bytes(...) bytes."""
+    _dev(x_packed, torch.uint8, "x_packed", 2)
+    _dev(w_packed, torch.uint8, "w_packed", 2)
+    dev = x_packed.device
+    tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
+    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed")
+    _flat(x_e8m0, torch.uint8, (tokens, k // 32), "x_e8m0", dev)
+    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
+    _flat(w_e8m0, torch.uint8, (o, k // 32), "w_e8m0", dev)
+    y = _rows_out(out, tokens, o, dev)
+    ws = _scratch(workspace, mxfp4_matmul_workspace_bytes(tokens, o, k), dev)
+    with torch.cuda.device(dev):
+        _check("mxfp4_matmul", load().mxfp4_matmul(
+            x_packed.data_ptr(), x_e8m0.data_ptr(), tokens, k, w_packed.data_ptr(), w_e8m0.data_ptr(), o, y.data_ptr(),
+            _row_major(y, "out"), ws.data_ptr(), ws.numel(), _stream(x_packed)))
+    return y
+
+
+def matmul_workspace_bytes(tokens: int, out_features: int, k: int) -> int:
+    """Workspace of matmul_w4a16 and matmul_w4a4."""
+    return int(load().nvfp4_matmul_workspace_bytes(tokens, out_features, k))
+
+
+def matmul_w4a16(x: torch.Tensor, w_packed: torch.Tensor, w_codes: torch.Tensor, w_scale2: torch.Tensor,
+                 out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [tokens, out_features] bf16 = x w^T of bf16 x [tokens, k] and an NVFP4
+    weight (packed u8 [out_features, k/2], codes u8 [out_features, k/16],
+    scale2 f32[1]), the weight taken exactly.  out may have any row stride;
+    workspace: uint8, at least matmul_workspace_bytes(...) bytes."""
+    _dev(x, torch.bfloat16, "x", 2)
+    _dev(w_packed, torch.uint8, "w_packed", 2)
+    tokens, k = x.shape
+    o = w_packed.shape[0]
+    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", x.device)
+    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", x.device)
+    _scalar(w_scale2, "w_scale2", x.device)
+    y = _rows_out(out, tokens, o, x.device)
+    ws = _scratch(workspace, matmul_workspace_bytes(tokens, o, k), x.device)
+    with torch.cuda.device(x.device):
+        _check("nvfp4_matmul_w4a16", load().nvfp4_matmul_w4a16(
+            x.data_ptr(), tokens, k, _row_major(x, "x"), w_packed.data_ptr(), w_codes.data_ptr(), w_scale2.data_ptr(),
+            o, y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(), _stream(x)))
+    return y
+
+
+def matmul_w4a4(x_packed: torch.Tensor, x_codes: torch.Tensor, x_scale2: torch.Tensor, w_packed: torch.Tensor,
+                w_codes: torch.Tensor, w_scale2: torch.Tensor, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y [tokens, out_features] bf16 = x w^T of two NVFP4 matrices (packed,
+    codes, scale2 as quantize_dynamic and scale_sweep return them), both taken
+    exactly.  out may have any row stride; workspace as for matmul_w4a16."""
+    _dev(x_packed, torch.uint8, "x_packed", 2)
+    _dev(w_packed, torch.uint8, "w_packed", 2)
+    dev = x_packed.device
+    tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
+    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed")
+    _flat(x_codes, torch.uint8, (tokens, k // 16), "x_codes", dev)
+    _scalar(x_scale2, "x_scale2", dev)
+    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
+    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", dev)
+    _scalar(w_scale2, "w_scale2", dev)
+    y = _rows_out(out, tokens, o, dev)
+    ws = _scratch(workspace, matmul_workspace_bytes(tokens, o, k), dev)
+    with torch.cuda.device(dev):
+        _check("nvfp4_matmul_w4a4", load().nvfp4_matmul_w4a4(
+            x_packed.data_ptr(), x_codes.data_ptr(), x_scale2.data_ptr(), tokens, k, w_packed.data_ptr(),
+            w_codes.data_ptr(), w_scale2.data_ptr(), o, y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(),
+            _stream(x_packed)))
+    return y
+
+
+def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None):
+    """The top_k experts of each token and their softmax weights: (ids i32
+    [tokens, top_k], weights f32 [tokens, top_k]), largest first, the lower
+    expert first among equals.  normalize: softmax over the chosen, else over
+    all experts.  -inf and NaN logits are never chosen (id -1, weight 0 where
+    too few are left)."""
+    _dev(logits, torch.float32, "logits", 2)
+    tokens, experts = logits.shape
+    ldl = _row_major(logits, "logits")
+    if out is None:
+        ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+        wts = torch.empty((tokens, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    else:
+        ids = _flat(out[0], torch.int32, (tokens, top_k), "ids", logits.device)
+        wts = _flat(out[1], torch.float32, (tokens, top_k), "weights", logits.device)
+    with torch.cuda.device(logits.device):
+        _check("nvfp4_moe_route", load().nvfp4_moe_route(
+            logits.data_ptr(), tokens, experts, ldl, top_k, int(bool(normalize)), ids.data_ptr(), wts.data_ptr(),
+            _stream(logits)))
+    return ids, wts
+
+
+def moe_workspace_bytes(tokens: int, top_k: int, inter: int) -> int:
+    return int(load().nvfp4_moe_workspace_bytes(tokens, top_k, inter))
+
+
+def moe_forward(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_packed: torch.Tensor,
+                w13_codes: torch.Tensor, w13_scale2: torch.Tensor, w2_packed: torch.Tensor, w2_codes: torch.Tensor,
+                w2_scale2: torch.Tensor, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Mixture-of-experts layer for up to 64 tokens over NVFP4 experts in the
+    cast's layout: y [tokens, hidden] bf16 = sum over a token's experts of
+    weight * W2 (silu(W1 x) * (W3 x)).
+
+    x bf16 [tokens, hidden]; ids i32 and weights f32 [tokens, top_k] (moe_route;
+    ids outside the experts add nothing); w13_packed u8 [experts, 2, inter,
+    hidden/2] with w13_codes [.., hidden/16] and w13_scale2 f32[experts];
+    w2_packed u8 [experts, 1, hidden, inter/2] (or without the 1) with w2_codes
+    [.., inter/16] and w2_scale2 f32[experts].  workspace: uint8, at least
+    moe_workspace_bytes(tokens, top_k, inter) bytes."""
+    _dev(x, torch.bfloat16, "x", 2)
+    _dev(ids, torch.int32, "ids", 2)
+    _dev(w13_packed, torch.uint8, "w13_packed", 4)
+    dev = x.device
+    tokens, hidden = x.shape
+    top_k = ids.shape[1]
+    e, _, inter, _ = w13_packed.shape
+    _flat(ids, torch.int32, (tokens, top_k), "ids", dev)
+    _flat(weights, torch.float32, (tokens, top_k), "weights", dev)
+    _flat(w13_packed, torch.uint8, (e, 2, inter, hidden // 2), "w13_packed", dev)
+    _flat(w13_codes, torch.uint8, (e, 2, inter, hidden // 16), "w13_codes", dev)
+    _flat(w13_scale2, torch.float32, (e,), "w13_scale2", dev)
+    mid = (1,) if w2_packed.dim() == 4 else ()
+    _flat(w2_packed, torch.uint8, (e, *mid, hidden, inter // 2), "w2_packed", dev)
+    _flat(w2_codes, torch.uint8, (e, *mid, hidden, inter // 16), "w2_codes", dev)
+    _flat(w2_scale2, torch.float32, (e,), "w2_scale2", dev)
+    y = _rows_out(out, tokens, hidden, dev)
+    ws = _scratch(workspace, moe_workspace_bytes(tokens, top_k, inter), dev)
+    with torch.cuda.device(dev):
+        _check("nvfp4_moe_forward", load().nvfp4_moe_forward(
+            x.data_ptr(), tokens, hidden, _row_major(x, "x"), ids.data_ptr(), weights.data_ptr(), top_k, e, inter,
+            w13_packed.data_ptr(), w13_codes.data_ptr(), w13_scale2.data_ptr(), w2_packed.data_ptr(),
+            w2_codes.data_ptr(), w2_scale2.data_ptr(), y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(),
+            _stream(x)))
+    return y

@@ -380,4 +380,143 @@ int nvfp4_quantlinear_forward(const uint16_t* x, int64_t tokens, int64_t k, int6
                             as_stream(stream));
 }
 
+int mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, uint8_t* packed, uint8_t* e8m0,
+                   void* stream) {
+  int st = check_matrix(rows, k, ldx, 2);
+  if (st) return st;
+  if (k % 32) return NVFP4_ERR_BAD_SHAPE;
+  if ((!x || !packed || !e8m0) && rows > 0) return NVFP4_ERR_NULL_ARG;
+  if (rows == 0) return NVFP4_OK;
+  if ((st = check_bf16_rows(x, ldx))) return st;
+  if (!aligned16(packed) || !aligned16(e8m0)) return NVFP4_ERR_MISALIGNED;
+  return launch_mxfp4_quantize(x, rows, k, ldx, packed, e8m0, as_stream(stream));
+}
+
+int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int64_t k, uint16_t* out, void* stream) {
+  int st = check_matrix(rows, k, k, 2);
+  if (st) return st;
+  if (k % 32) return NVFP4_ERR_BAD_SHAPE;
+  if ((!packed || !e8m0 || !out) && rows > 0) return NVFP4_ERR_NULL_ARG;
+  if (rows == 0) return NVFP4_OK;
+  if (!aligned16(packed) || !aligned16(e8m0) || !aligned16(out)) return NVFP4_ERR_MISALIGNED;
+  return launch_mxfp4_dequant(packed, e8m0, rows, k, out, as_stream(stream));
+}
+
+// Sizes of a product: every extent below 2^31 (the kernels index rows and
+// columns with 32 bits and form byte offsets in 64).
+static int check_product(int64_t tokens, int64_t out, int64_t k, int64_t block, int64_t ldy) {
+  if (tokens < 0 || out <= 0 || k <= 0 || k % block || ldy < out) return NVFP4_ERR_BAD_SHAPE;
+  if (tokens > INT32_MAX || out > INT32_MAX || k > INT32_MAX) return NVFP4_ERR_BAD_SHAPE;
+  return check_matrix(tokens, out, ldy, 2);
+}
+
+static size_t matmul_workspace(int64_t tokens, int64_t out_features, int64_t k, int64_t block, bool mx) {
+  if (tokens <= 0 || check_product(tokens, out_features, k, block, out_features)) return 0;
+  return product_workspace_bytes(tokens, out_features, k, mx);
+}
+
+static int check_workspace(const void* workspace, size_t have, size_t need) {
+  if (have < need) return NVFP4_ERR_WORKSPACE;
+  if (need && !workspace) return NVFP4_ERR_NULL_ARG;
+  return need && !aligned16(workspace) ? NVFP4_ERR_MISALIGNED : NVFP4_OK;
+}
+
+size_t mxfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k) {
+  return matmul_workspace(tokens, out_features, k, 32, true);
+}
+
+int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, int64_t tokens, int64_t k, const uint8_t* w_packed,
+                 const uint8_t* w_e8m0, int64_t out_features, uint16_t* y, int64_t ldy, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  int st = check_product(tokens, out_features, k, 32, ldy);
+  if (st) return st;
+  if (!w_packed || !w_e8m0 || ((!x_packed || !x_e8m0 || !y) && tokens > 0)) return NVFP4_ERR_NULL_ARG;
+  if (tokens == 0) return NVFP4_OK;
+  if (!aligned16(x_packed) || !aligned16(x_e8m0) || !aligned16(w_packed) || !aligned16(w_e8m0) || !aligned2(y))
+    return NVFP4_ERR_MISALIGNED;
+  if ((st = check_workspace(workspace, workspace_bytes, product_workspace_bytes(tokens, out_features, k, true))))
+    return st;
+  return launch_mxfp4_matmul(x_packed, x_e8m0, tokens, k, w_packed, w_e8m0, out_features, y, ldy, workspace,
+                             as_stream(stream));
+}
+
+size_t nvfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k) {
+  return matmul_workspace(tokens, out_features, k, 16, false);
+}
+
+int nvfp4_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* w_packed,
+                       const uint8_t* w_codes, const float* w_scale2, int64_t out_features, uint16_t* y, int64_t ldy,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_product(tokens, out_features, k, 16, ldy);
+  if (st || (st = check_matrix(tokens, k, ldx, 2))) return st;
+  if (!w_packed || !w_codes || !w_scale2 || ((!x || !y) && tokens > 0)) return NVFP4_ERR_NULL_ARG;
+  if (tokens == 0) return NVFP4_OK;
+  if ((st = check_bf16_rows(x, ldx))) return st;
+  if (!aligned16(w_packed) || !aligned16(w_codes) || !aligned4(w_scale2) || !aligned2(y)) return NVFP4_ERR_MISALIGNED;
+  if ((st = check_workspace(workspace, workspace_bytes, product_workspace_bytes(tokens, out_features, k, false))))
+    return st;
+  return launch_matmul_w4a16(x, tokens, k, ldx, w_packed, w_codes, w_scale2, out_features, y, ldy, workspace,
+                             as_stream(stream));
+}
+
+int nvfp4_matmul_w4a4(const uint8_t* x_packed, const uint8_t* x_codes, const float* x_scale2, int64_t tokens, int64_t k,
+                      const uint8_t* w_packed, const uint8_t* w_codes, const float* w_scale2, int64_t out_features,
+                      uint16_t* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_product(tokens, out_features, k, 16, ldy);
+  if (st) return st;
+  if (!x_scale2 || !w_packed || !w_codes || !w_scale2 || ((!x_packed || !x_codes || !y) && tokens > 0))
+    return NVFP4_ERR_NULL_ARG;
+  if (tokens == 0) return NVFP4_OK;
+  if (!aligned16(x_packed) || !aligned16(x_codes) || !aligned4(x_scale2) || !aligned16(w_packed) ||
+      !aligned16(w_codes) || !aligned4(w_scale2) || !aligned2(y))
+    return NVFP4_ERR_MISALIGNED;
+  if ((st = check_workspace(workspace, workspace_bytes, product_workspace_bytes(tokens, out_features, k, false))))
+    return st;
+  return launch_matmul_w4a4(x_packed, x_codes, x_scale2, tokens, k, w_packed, w_codes, w_scale2, out_features, y, ldy,
+                            workspace, as_stream(stream));
+}
+
+int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
+                    int32_t* ids, float* weights, void* stream) {
+  const int st = check_matrix(tokens, experts, ldl, 4);
+  if (st) return st;
+  if (tokens > INT32_MAX) return NVFP4_ERR_BAD_SHAPE;
+  if (experts > kMoeMaxExperts || top_k < 1 || top_k > kMoeMaxTopK || top_k > experts) return NVFP4_ERR_BAD_INPUT;
+  if (normalize != 0 && normalize != 1) return NVFP4_ERR_BAD_INPUT;
+  if ((!logits || !ids || !weights) && tokens > 0) return NVFP4_ERR_NULL_ARG;
+  if (tokens == 0) return NVFP4_OK;
+  if (!aligned4(logits) || !aligned4(ids) || !aligned4(weights)) return NVFP4_ERR_MISALIGNED;
+  return launch_moe_route(logits, tokens, experts, ldl, top_k, normalize, ids, weights, as_stream(stream));
+}
+
+size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
+  if (tokens <= 0 || tokens > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK) return 0;
+  if (inter <= 0 || inter % 16 || inter > INT32_MAX) return 0;
+  return moe_workspace_bytes(tokens, top_k, inter);
+}
+
+int nvfp4_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t ldx, const int32_t* ids,
+                      const float* weights, int64_t top_k, int64_t experts, int64_t inter, const uint8_t* w13_packed,
+                      const uint8_t* w13_codes, const float* w13_scale2, const uint8_t* w2_packed,
+                      const uint8_t* w2_codes, const float* w2_scale2, uint16_t* y, int64_t ldy, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int st = check_matrix(tokens, hidden, ldx, 2);
+  if (st || (st = check_matrix(tokens, hidden, ldy, 2))) return st;
+  if (hidden % 16 || inter <= 0 || inter % 16 || hidden > INT32_MAX || inter > INT32_MAX) return NVFP4_ERR_BAD_SHAPE;
+  if (tokens > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || experts < 1 || experts > kMoeMaxExperts)
+    return NVFP4_ERR_BAD_INPUT;
+  if (!mul_fits(hidden, inter) || !mul_fits(hidden * inter, 2 * experts)) return NVFP4_ERR_BAD_SHAPE;
+  if (!w13_packed || !w13_codes || !w13_scale2 || !w2_packed || !w2_codes || !w2_scale2 ||
+      ((!x || !ids || !weights || !y) && tokens > 0))
+    return NVFP4_ERR_NULL_ARG;
+  if (tokens == 0) return NVFP4_OK;
+  if ((st = check_bf16_rows(x, ldx))) return st;
+  if (!aligned4(ids) || !aligned4(weights) || !aligned16(w13_packed) || !aligned16(w13_codes) ||
+      !aligned4(w13_scale2) || !aligned16(w2_packed) || !aligned16(w2_codes) || !aligned4(w2_scale2) || !aligned2(y))
+    return NVFP4_ERR_MISALIGNED;
+  if ((st = check_workspace(workspace, workspace_bytes, moe_workspace_bytes(tokens, top_k, inter)))) return st;
+  return launch_moe_forward(x, tokens, hidden, ldx, ids, weights, (int)top_k, experts, inter, w13_packed, w13_codes,
+                            w13_scale2, w2_packed, w2_codes, w2_scale2, y, ldy, workspace, as_stream(stream));
+}
+
 }  // extern "C"

@@ -23,6 +23,7 @@ inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Test hook read from the environment: NVFP4MI_FORCE_EXACT=1 disables the
@@ -86,5 +87,30 @@ int launch_probe_write(void* buf, size_t bytes, uint32_t value, int wgs, hipStre
 int launch_probe_copy(const void* src, void* dst, size_t bytes, int wgs, hipStream_t s);
 int launch_mx_cast(uint8_t* packed, const uint8_t* e8m0, int64_t groups, int64_t mats, int64_t rows, int64_t k,
                    uint8_t* codes, float* scale2, int64_t* fallback, hipStream_t s);
+// products of packed 4-bit matrices (tokens, out and k below 2^31)
+int launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t k, int64_t ldx, uint8_t* packed, uint8_t* e8m0,
+                          hipStream_t s);
+int launch_mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int64_t k, uint16_t* out,
+                         hipStream_t s);
+size_t product_workspace_bytes(int64_t tokens, int64_t out, int64_t k, bool mx);
+int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* wp, const uint8_t* wc,
+                        const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);
+int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens, int64_t k,
+                       const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y, int64_t ldy,
+                       void* workspace, hipStream_t s);
+int launch_mxfp4_matmul(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp,
+                        const uint8_t* we, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);
+// mixture-of-experts layer: limits of one call
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxTopK = 16;
+constexpr int kMoeMaxExperts = 1024;
+size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter);
+int launch_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
+                     int32_t* ids, float* weights, hipStream_t s);
+int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t ldx, const int32_t* ids,
+                       const float* weights, int top_k, int64_t experts, int64_t inter, const uint8_t* w13_packed,
+                       const uint8_t* w13_codes, const float* w13_scale2, const uint8_t* w2_packed,
+                       const uint8_t* w2_codes, const float* w2_scale2, uint16_t* y, int64_t ldy, void* workspace,
+                       hipStream_t s);
 
 }  // namespace nvfp4

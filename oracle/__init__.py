@@ -30,6 +30,10 @@ Sources (page title, section):
 * "FP4量化技术概述" §3.1 (MR-GPTQ): block Hadamard rotation fused into the
   weights, W' = W H, activations rotated online (rotate.py).
 
+* Packed products and the expert layer (product.py): the W4A16 and W4A4 tiers
+  of "Coder390 NVFP4 校正（校准）方式" §3, the MXFP4 format of the ModelOpt
+  guide §1, the shared gate/up scale of its §3.
+
 Readings where the pages are silent are marked "reading:" in the docstrings.
 
 Readings no worked example on the pages can confirm (every function is
@@ -56,6 +60,7 @@ from .nvfp4 import (
 from .mxcast import mxfp4_to_nvfp4, mxfp4_dequant
 from .fp8 import fp8_tensor_scale, fp8_quantize, fp8_dequant
 from .rotate import hadamard16, rotate_blocks, rotate_hessian
+from .product import mxfp4_quantize, nvfp4_values, matmul, moe_route, moe_forward
 
 __all__ = [
     "E2M1_MAGNITUDES", "E4M3_VALUES", "e2m1_decode", "e2m1_encode", "e4m3_value",
@@ -67,4 +72,5 @@ __all__ = [
     "mxfp4_to_nvfp4", "mxfp4_dequant",
     "fp8_tensor_scale", "fp8_quantize", "fp8_dequant",
     "hadamard16", "rotate_blocks", "rotate_hessian",
+    "mxfp4_quantize", "nvfp4_values", "matmul", "moe_route", "moe_forward",
 ]
