@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4mi.so")
 SOURCES = ["api.hip", "quant.hip", "hessian.hip", "sweep.hip", "cast.hip", "fp8.hip", "rotate.hip", "linear.hip",
-           "probe.hip", "sweep_stats.hip", "mxfp4.hip", "matmul.hip", "moe.hip"]
+           "probe.hip", "sweep_stats.hip", "mxfp4.hip", "matmul.hip", "matmul_tile.hip", "moe.hip"]
 ARCH = os.environ.get("NVFP4MI_ARCH", "gfx950")
 
 FLAGS = [

@@ -102,14 +102,21 @@ int run(const ProductArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// Tokens up to which the streaming kernel is used.
+constexpr int64_t kFewTokens = 64;
+
+static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
+  return tokens > kFewTokens && tile_product_fits(tokens, out, k, mx, ldx_bytes);
+}
+
 size_t product_workspace_bytes(int64_t tokens, int64_t out, int64_t k, bool mx) {
-  (void)tokens; (void)out; (void)k; (void)mx;
-  return 0;
+  return use_tiles(tokens, out, k, mx, mx ? k / 2 : k * 2) ? tile_product_workspace(tokens, out, k, mx) : 0;
 }
 
 int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* wp, const uint8_t* wc,
                         const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s) {
-  (void)workspace;
+  if (use_tiles(tokens, out, k, false, ldx * 2))
+    return launch_tile_nv(x, ldx, nullptr, nullptr, nullptr, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s);
   const ProductArgs a{reinterpret_cast<const uint8_t*>(x), nullptr, nullptr, wp, wc, ws2, ldx * 2, ldy, y, (int)tokens,
                       (int)out, (int)k};
   return (k % 32) ? run<kW4A16, false>(a, s) : run<kW4A16, true>(a, s);
@@ -118,14 +125,16 @@ int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ld
 int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens, int64_t k,
                        const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y, int64_t ldy,
                        void* workspace, hipStream_t s) {
-  (void)workspace;
+  if (use_tiles(tokens, out, k, false, k * 2))
+    return launch_tile_nv(nullptr, 0, xp, xc, xs2, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s);
   const ProductArgs a{xp, xc, xs2, wp, wc, ws2, k / 2, ldy, y, (int)tokens, (int)out, (int)k};
   return (k % 32) ? run<kW4A4, false>(a, s) : run<kW4A4, true>(a, s);
 }
 
 int launch_mxfp4_matmul(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp,
                         const uint8_t* we, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s) {
-  (void)workspace;
+  if (use_tiles(tokens, out, k, true, k / 2))
+    return launch_tile_mx(xp, xe, tokens, k, wp, we, out, y, ldy, workspace, s);
   const ProductArgs a{xp, xe, nullptr, wp, we, nullptr, k / 2, ldy, y, (int)tokens, (int)out, (int)k};
   return run<kMX, true>(a, s);
 }

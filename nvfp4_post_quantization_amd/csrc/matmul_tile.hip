@@ -1,0 +1,667 @@
+// Products of packed 4-bit matrices for more tokens than the streaming
+// kernels of matmul.hip take: tiles of tokens x output rows on the matrix
+// cores, fed through LDS.
+//
+//   MXFP4       32x32x64 scaled FP4 instructions on the packed operands
+//   16 x NVFP4  32x32x16 bf16 / fp16 instructions; the weights stay packed in
+//               LDS and are expanded (exactly) in registers by the one wave
+//               column that multiplies them; W4A4's activations are expanded
+//               to fp16 once, into the workspace
+//
+// The weights are the instruction's M side, the tokens its N side, so that a
+// lane's results are runs of four neighbouring outputs of one token.
+//
+// Stages of the channel axis (128 channels of MXFP4, 64 of 16-bit
+// activations) go from HBM / L2 straight to LDS (buffer loads to LDS, 16 bytes
+// a lane), several stages ahead; waves wait for their own loads by count and
+// meet at one barrier per stage, in the middle of it, so that the first
+// operands of the next stage are read while the second half is multiplied.
+// LDS addresses are the lanes' in order, so the swizzle that keeps the operand
+// reads free of bank conflicts permutes the 16-byte pieces of a row on the
+// global side.  Pieces beyond k are given an offset beyond the buffer, which
+// reads as zero; rows beyond the matrix repeat its last row and are not
+// stored.
+//
+// Block scales lie a row apart in memory, one short run per row and stage; a
+// small launch first writes them as one word per (stage, row), rows adjacent,
+// padded with zeros, so that a stage's scales are one contiguous load.
+#include <atomic>
+
+#include "common.hpp"
+#include "product_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+
+// 16 (4) bytes a lane from the buffer to LDS at dst + 16 (4) lane; dst is
+// uniform over the wave.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t b, uint8_t* dst, uint32_t offset, int base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)dst, 16, (int)offset, base, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, uint32_t offset, int base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)dst, 4, (int)offset, base, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+constexpr uint32_t kBeyond = 0x80000000u;           // past any buffer here (below 2^31 bytes): reads as zero
+
+// Piece swizzles of LDS rows of 64, 128 and 32 bytes: any 8 or 16 rows in a
+// row spread one 16-byte column over all banks.
+__device__ __forceinline__ int swizzle64(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
+__device__ __forceinline__ int swizzle128(int row) { return row & 7; }
+__device__ __forceinline__ int swizzle32(int row) { return ((row >> 2) ^ (row >> 3)) & 1; }
+
+struct TileArgs {
+  const uint8_t* x;           // packed MXFP4 rows, or 16-bit rows
+  const uint8_t* w;           // packed rows
+  const uint32_t* xs;         // [steps][tokens_pad] scale words (MXFP4)
+  const uint32_t* ws;         // [steps][out_pad]
+  const float* s0;            // tensor scales, or NULL
+  const float* s1;
+  uint16_t* y;
+  float* partial;             // [splits][tokens][ldp] when splits > 1
+  int64_t ldx, ldw, ldy;      // bytes, bytes, elements
+  int64_t ldp;
+  int tokens, out, k;
+  int tokens_pad, out_pad;    // multiples of 256
+  int tiles_m, tiles_n, splits, steps;
+};
+
+// Which tile a workgroup takes.  Consecutive workgroups go to the 8 XCDs in
+// turn; each XCD gets a contiguous run of tiles, walked in columns of up to 8
+// token tiles, so that what its CUs read at one time shares its L2.
+struct TilePos { int m, n, split; };
+__device__ __forceinline__ TilePos tile_of(const TileArgs& a) {
+  const int total = a.tiles_m * a.tiles_n * a.splits;
+  const int id = blockIdx.x, xcd = id & 7, i = id >> 3;
+  const int q = total >> 3, r = total & 7;
+  int t = xcd * q + min(xcd, r) + i;
+  const int per = a.tiles_m * a.tiles_n;
+  TilePos p;
+  p.split = t / per;
+  t -= p.split * per;
+  const int band = t / (8 * a.tiles_n);
+  const int rows = min(8, a.tiles_m - band * 8);
+  t -= band * 8 * a.tiles_n;
+  p.n = t / rows;
+  p.m = band * 8 + t % rows;
+  return p;
+}
+
+// Results of a wave: tile (n, m) covers outputs o0 + 32 n + .., tokens
+// t0 + 32 m + (lane & 31).  Register 4 g + e of a lane is output
+// 8 g + 4 (lane >> 5) + e of the tile.
+template <int TN, int TM>
+__device__ __forceinline__ void store_tiles(const TileArgs& a, const f32x16 (&acc)[TN][TM], int o0, int t0, int split) {
+  const int lane = threadIdx.x & 63, sub = 4 * (lane >> 5);
+  float s0 = 1.0f, s1 = 1.0f;
+  if (a.s0) s0 = *a.s0;
+  if (a.s1) s1 = *a.s1;
+  const bool wide = (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int t = t0 + 32 * m + (lane & 31);
+    if (t >= a.tokens) continue;
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int o = o0 + 32 * n + 8 * g + sub;
+        if (o >= a.out) continue;
+        if (a.splits > 1) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[n][m][4 * g + e];
+          *reinterpret_cast<f32x4*>(a.partial + ((int64_t)split * a.tokens + t) * a.ldp + o) = v;
+          continue;
+        }
+        uint16_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = to_bf16(acc[n][m][4 * g + e] * s0 * s1);
+        uint16_t* dst = a.y + (int64_t)t * a.ldy + o;
+        if (wide && o + 3 < a.out) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (o + e < a.out) dst[e] = v[e];
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ f32x16 mfma32_mx(uint4 a, uint32_t sa, uint4 b, uint32_t sb, f32x16 c, int sel) {
+  const i32x8 va = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i32x8 vb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  if (sel == 0) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, 2, (int)sa, 2, (int)sb);
+}
+
+// MXFP4: WM x WN waves of 32 TM tokens x 32 TN outputs, four stages of 128
+// channels in LDS, three of them on their way.
+template <int TM, int TN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void mx_tile_kernel(TileArgs a) {
+  constexpr int NW = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN, NBUF = 4;
+  constexpr int XB = BM * 64, WB = BN * 64, XSB = BM * 4, WSB = BN * 4, STAGE = XB + WB + XSB + WSB;
+  constexpr int XL = BM / 16 / NW, WL = BN / 16 / NW, SL = (BM + BN) / 64 / NW;     // loads of a wave per stage
+  constexpr int LOADS = XL + WL + SL;
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && (BM + BN) % (64 * NW) == 0 && BM % 64 == 0, "tile split");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TilePos pos = tile_of(a);
+  const int t0 = pos.m * BM, o0 = pos.n * BN;
+  const int s_begin = (int)((int64_t)a.steps * pos.split / a.splits);
+  const int s_end = (int)((int64_t)a.steps * (pos.split + 1) / a.splits);
+
+  const int rows_x = min(BM, a.tokens - t0), rows_w = min(BN, a.out - o0);
+  const auto bx = make_buffer(a.x + (int64_t)t0 * a.ldx, (uint32_t)((int64_t)rows_x * a.ldx));
+  const auto bw = make_buffer(a.w + (int64_t)o0 * a.ldw, (uint32_t)((int64_t)rows_w * a.ldw));
+  const auto bxs = make_buffer(a.xs, (uint32_t)((int64_t)a.steps * a.tokens_pad * 4));
+  const auto bws = make_buffer(a.ws, (uint32_t)((int64_t)a.steps * a.out_pad * 4));
+  // this lane's part of the loads: 4 lanes per 64-byte row
+  uint32_t xo[XL], wo[WL];
+  const int piece = (lane & 3) ^ swizzle64(wave * 16 + (lane >> 2));
+#pragma unroll
+  for (int i = 0; i < XL; ++i)
+    xo[i] = (uint32_t)(min((wave + i * NW) * 16 + (lane >> 2), rows_x - 1) * a.ldx + piece * 16);
+#pragma unroll
+  for (int i = 0; i < WL; ++i)
+    wo[i] = (uint32_t)(min((wave + i * NW) * 16 + (lane >> 2), rows_w - 1) * a.ldw + piece * 16);
+
+  auto load_stage = [&](int s) {
+    uint8_t* dst = lds + (s & (NBUF - 1)) * STAGE;
+    const bool cut = (s + 1) * 128 > a.k && s * 128 + piece * 32 >= a.k;      // this lane's piece lies beyond k
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      load_lds16(bx, dst + (wave + i * NW) * 1024, cut ? kBeyond : xo[i], s * 64);
+#pragma unroll
+    for (int i = 0; i < WL; ++i)
+      load_lds16(bw, dst + XB + (wave + i * NW) * 1024, cut ? kBeyond : wo[i], s * 64);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int c = wave + i * NW;                                            // 64 rows of scale words
+      if (c < BM / 64)
+        load_lds4(bxs, dst + XB + WB + c * 256, lane * 4, (s * a.tokens_pad + t0 + c * 64) * 4);
+      else
+        load_lds4(bws, dst + XB + WB + c * 256, lane * 4, (s * a.out_pad + o0 + c * 64 - BM) * 4);
+    }
+  };
+
+  const int wm = wave % WM, wn = wave / WM, half = lane >> 5, l32 = lane & 31;
+  const int frag = l32 * 64 + ((half ^ swizzle64(l32)) << 4);                 // piece `half`; ^ 32 gives piece 2 + half
+  const int xf = wm * TM * 32 * 64 + frag, wf = XB + wn * TN * 32 * 64 + frag;
+  const int xsf = XB + WB + (wm * TM * 32 + l32) * 4, wsf = XB + WB + XSB + (wn * TN * 32 + l32) * 4;
+  uint4 xr[2][TM], wr[2][TN];
+  uint32_t xsr[2][TM], wsr[2][TN];
+  auto read_scales = [&](int set, int s) {
+    const uint8_t* b = lds + (s & (NBUF - 1)) * STAGE;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xsr[set][i] = *reinterpret_cast<const uint32_t*>(b + xsf + i * 128) >> (8 * half);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wsr[set][i] = *reinterpret_cast<const uint32_t*>(b + wsf + i * 128) >> (8 * half);
+  };
+  auto read_frags = [&](int set, int s) {
+    const uint8_t* b = lds + (s & (NBUF - 1)) * STAGE;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xr[set][i] = *reinterpret_cast<const uint4*>(b + ((xf + i * 2048) ^ (set * 32)));
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wr[set][i] = *reinterpret_cast<const uint4*>(b + ((wf + i * 2048) ^ (set * 32)));
+  };
+
+  f32x16 acc[TN][TM];
+#pragma unroll
+  for (int n = 0; n < TN; ++n)
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
+
+  if (s_begin < s_end) {
+#pragma unroll
+    for (int i = 0; i < NBUF - 1; ++i)
+      if (s_begin + i < s_end) load_stage(s_begin + i);
+    if (s_begin + 2 < s_end) wait_loads<2 * LOADS>();
+    else if (s_begin + 1 < s_end) wait_loads<LOADS>();
+    else wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    read_scales(0, s_begin);
+    read_frags(0, s_begin);
+    for (int s = s_begin; s < s_end; ++s) {
+      read_frags(1, s);
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_mx(wr[0][n], wsr[0][n], xr[0][m], xsr[0][m], acc[n][m], 0);
+      if (s + 1 < s_end) {
+        if (s + 2 < s_end) wait_loads<LOADS>();
+        else wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        if (s + 3 < s_end) load_stage(s + 3);
+        read_scales(1, s + 1);
+        read_frags(0, s + 1);
+      }
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_mx(wr[1][n], wsr[0][n], xr[1][m], xsr[0][m], acc[n][m], 1);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) xsr[0][i] = xsr[1][i];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) wsr[0][i] = wsr[1][i];
+    }
+  }
+  store_tiles<TN, TM>(a, acc, o0 + wn * TN * 32, t0 + wm * TM * 32, pos.split);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x16 mfma32_16(uint4 a, uint4 b, f32x16 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+// 16-bit activations x NVFP4 weights: WM x WN waves of 32 TM tokens x 32 TN
+// outputs, three stages of 64 channels in LDS, two of them on their way.
+// Lane half h of an instruction takes channels 32 h + 8 j .. + 7 of the stage
+// at step j, so that a lane's weights of a stage are one 16-byte piece.
+template <bool F16, int TM, int TN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) {
+  constexpr int NW = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
+  constexpr int XB = BM * 128, WB = BN * 32, WSB = BN * 4, STAGE = XB + WB + WSB;
+  constexpr int XL = BM / 8 / NW, WL = BN / 32 / NW;
+  constexpr int SL = (BN / 64 + NW - 1) / NW;
+  constexpr int LOADS = XL + WL + SL;
+  static_assert(BM % (8 * NW) == 0 && BN % (32 * NW) == 0, "tile split");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TilePos pos = tile_of(a);
+  const int t0 = pos.m * BM, o0 = pos.n * BN;
+  const int s_begin = (int)((int64_t)a.steps * pos.split / a.splits);
+  const int s_end = (int)((int64_t)a.steps * (pos.split + 1) / a.splits);
+
+  const int rows_x = min(BM, a.tokens - t0), rows_w = min(BN, a.out - o0);
+  // the last row ends with its k channels, not with its stride
+  const auto bx = make_buffer(a.x + (int64_t)t0 * a.ldx, (uint32_t)((int64_t)(rows_x - 1) * a.ldx + (int64_t)a.k * 2));
+  const auto bw = make_buffer(a.w + (int64_t)o0 * a.ldw, (uint32_t)((int64_t)rows_w * a.ldw));
+  const auto bws = make_buffer(a.ws, (uint32_t)((int64_t)a.steps * a.out_pad * 4));
+  uint32_t xo[XL], wo[WL];
+  const int xpiece = (lane & 7) ^ swizzle128(lane >> 3);
+  const int wpiece = (lane & 1) ^ swizzle32(lane >> 1);
+#pragma unroll
+  for (int i = 0; i < XL; ++i)
+    xo[i] = (uint32_t)(min((wave + i * NW) * 8 + (lane >> 3), rows_x - 1) * a.ldx + xpiece * 16);
+#pragma unroll
+  for (int i = 0; i < WL; ++i)
+    wo[i] = (uint32_t)(min((wave + i * NW) * 32 + (lane >> 1), rows_w - 1) * a.ldw + wpiece * 16);
+
+  auto load_stage = [&](int s, int buf) {
+    uint8_t* dst = lds + buf * STAGE;
+    const bool last = (s + 1) * 64 > a.k;
+    const bool xcut = last && s * 64 + xpiece * 8 >= a.k, wcut = last && s * 64 + wpiece * 32 >= a.k;
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      load_lds16(bx, dst + (wave + i * NW) * 1024, xcut ? kBeyond : xo[i], s * 128);
+#pragma unroll
+    for (int i = 0; i < WL; ++i)
+      load_lds16(bw, dst + XB + (wave + i * NW) * 1024, wcut ? kBeyond : wo[i], s * 32);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      // fewer runs of 64 rows than waves: the rest load the first runs again
+      const int c = (wave + i * NW) % (BN / 64);
+      load_lds4(bws, dst + XB + WB + c * 256, lane * 4, (s * a.out_pad + o0 + c * 64) * 4);
+    }
+  };
+
+  const int wm = wave % WM, wn = wave / WM, half = lane >> 5, l32 = lane & 31;
+  const int xrow = (wm * TM * 32 + l32) * 128;
+  const int wf = XB + (wn * TN * 32 + l32) * 32 + ((half ^ swizzle32(l32)) << 4);
+  const int wsf = XB + WB + (wn * TN * 32 + l32) * 4;
+  uint4 xr[2][TM], wr[TN];
+  uint32_t wsr[TN];
+  auto read_x = [&](int set, int j, int buf) {
+    const uint8_t* b = lds + buf * STAGE + xrow + (((4 * half + j) ^ swizzle128(l32)) << 4);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xr[set][i] = *reinterpret_cast<const uint4*>(b + i * 4096);
+  };
+  uint4 wr_next[TN];
+  uint32_t wsr_next[TN];
+  auto read_w = [&](int buf) {
+    const uint8_t* b = lds + buf * STAGE;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      wr_next[i] = *reinterpret_cast<const uint4*>(b + wf + i * 1024);
+      wsr_next[i] = *reinterpret_cast<const uint32_t*>(b + wsf + i * 128) >> (16 * half);
+    }
+  };
+  auto expand = [&](int n, int j) {
+    const uint32_t q = j == 0 ? wr[n].x : j == 1 ? wr[n].y : j == 2 ? wr[n].z : wr[n].w;
+    const float s = j < 2 ? e4m3_f32<0>(wsr[n]) : e4m3_f32<1>(wsr[n]);
+    return F16 ? fp4x8_f16(q, splat_f16(s)) : fp4x8_bf16(q, s);
+  };
+
+  f32x16 acc[TN][TM];
+#pragma unroll
+  for (int n = 0; n < TN; ++n)
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
+
+  if (s_begin < s_end) {
+    load_stage(s_begin, 0);
+    if (s_begin + 1 < s_end) {
+      load_stage(s_begin + 1, 1);
+      wait_loads<LOADS>();
+    } else {
+      wait_loads<0>();
+    }
+    __builtin_amdgcn_s_barrier();
+    int buf = 0;
+    read_w(0);
+    read_x(0, 0, 0);
+    for (int s = s_begin; s < s_end; ++s) {
+      const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
+#pragma unroll
+      for (int n = 0; n < TN; ++n) { wr[n] = wr_next[n]; wsr[n] = wsr_next[n]; }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < 3) {
+          read_x((j + 1) & 1, j + 1, buf);
+        } else if (s + 1 < s_end) {
+          wait_loads<0>();
+          __builtin_amdgcn_s_barrier();
+          if (s + 2 < s_end) load_stage(s + 2, after);
+          read_w(next);
+          read_x(0, 0, next);
+        }
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+          const uint4 w = expand(n, j);
+#pragma unroll
+          for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_16<F16>(w, xr[j & 1][m], acc[n][m]);
+        }
+      }
+      buf = next;
+    }
+  }
+  store_tiles<TN, TM>(a, acc, o0 + wn * TN * 32, t0 + wm * TM * 32, pos.split);
+}
+
+// Scale bytes [rows][nb] to words [steps][rows_pad], four bytes of a row each,
+// zero beyond nb and rows.  One thread per word, rows fastest.
+__device__ __forceinline__ void scale_words(const uint8_t* src, int rows, int nb, uint32_t* dst, int rows_pad,
+                                            int64_t i) {
+  const int step = (int)(i / rows_pad), row = (int)(i % rows_pad);
+  uint32_t v = 0;
+  if (row < rows) {
+    const uint8_t* p = src + (int64_t)row * nb + step * 4;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (step * 4 + b < nb) v |= (uint32_t)p[b] << (8 * b);
+  }
+  dst[i] = v;
+}
+
+struct PrepArgs {
+  const uint8_t* ws;          // weight scale bytes [out][nb]
+  uint32_t* wdst;
+  const uint8_t* xs;          // MXFP4: token scale bytes [tokens][nb]
+  uint32_t* xdst;
+  const uint8_t* xp;          // W4A4: packed tokens, expanded to fp16 [tokens][k] at xh
+  const uint8_t* xc;
+  uint16_t* xh;
+  int tokens, out, nb, tokens_pad, out_pad, steps, k;
+};
+
+__global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
+  const int64_t nw = (int64_t)a.steps * a.out_pad, nx = a.xs ? (int64_t)a.steps * a.tokens_pad : 0;
+  const int64_t nh = a.xh ? (int64_t)a.tokens * (a.k >> 4) : 0;              // 16-channel blocks
+  const int64_t total = nw + nx + nh, stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
+    if (i < nw) {
+      scale_words(a.ws, a.out, a.nb, a.wdst, a.out_pad, i);
+    } else if (i < nw + nx) {
+      scale_words(a.xs, a.tokens, a.nb, a.xdst, a.tokens_pad, i - nw);
+    } else {
+      const int64_t b = i - nw - nx;
+      const uint2 q = *reinterpret_cast<const uint2*>(a.xp + b * 8);
+      const f16x2 s = splat_f16(e4m3_f32<0>(a.xc[b]));
+      uint4* dst = reinterpret_cast<uint4*>(a.xh + b * 16);
+      dst[0] = fp4x8_f16(q.x, s);
+      dst[1] = fp4x8_f16(q.y, s);
+    }
+  }
+}
+
+// y = RN_bf16(s0 s1 sum over splits), in split order.
+__global__ __launch_bounds__(256) void join_kernel(TileArgs a) {
+  const int64_t quads = a.ldp >> 2, total = a.tokens * quads;
+  float s0 = 1.0f, s1 = 1.0f;
+  if (a.s0) s0 = *a.s0;
+  if (a.s1) s1 = *a.s1;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / quads;
+    const int o = (int)(i % quads) * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(a.partial + t * a.ldp + o);
+    for (int s = 1; s < a.splits; ++s)
+      v += *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)s * a.tokens + t) * a.ldp + o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (o + e < a.out) a.y[t * a.ldy + o + e] = to_bf16(v[e] * s0 * s1);
+  }
+}
+
+constexpr int kCus = 256;
+
+// How a product is cut.  Large tiles where they fill the card, else tiles of
+// 128 x 128 with the channels split until they do.
+struct Plan {
+  bool large;
+  int tiles_m, tiles_n, splits, steps;
+  int tokens_pad, out_pad;
+  size_t xs, ws, xh, partial, bytes;     // workspace offsets
+};
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+Plan plan_product(int64_t tokens, int64_t out, int64_t k, bool mx) {
+  Plan p{};
+  p.steps = (int)((k + (mx ? 127 : 63)) / (mx ? 128 : 64));
+  p.tokens_pad = (int)((tokens + 255) / 256 * 256);
+  p.out_pad = (int)((out + 255) / 256 * 256);
+  const int64_t big = (int64_t)(p.tokens_pad / 256) * (p.out_pad / 256);
+  p.large = big >= kCus * 3 / 4;
+  const int side = p.large ? 256 : 128;
+  p.tiles_m = (int)((tokens + side - 1) / side);
+  p.tiles_n = (int)((out + side - 1) / side);
+  p.splits = 1;
+  if (!p.large) {
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    while (tiles * p.splits < kCus && p.splits * 2 * 8 <= p.steps) p.splits *= 2;
+  }
+  size_t at = 0;
+  p.ws = at;
+  at = align256(at + (size_t)p.steps * p.out_pad * 4);
+  p.xs = at;
+  if (mx) at = align256(at + (size_t)p.steps * p.tokens_pad * 4);
+  p.xh = at;
+  if (!mx) at = align256(at + (size_t)tokens * k * 2);                        // used by W4A4 only
+  p.partial = at;
+  if (p.splits > 1) at = align256(at + (size_t)p.splits * tokens * ((out + 3) / 4 * 4) * 4);
+  p.bytes = at;
+  return p;
+}
+
+typedef void (*TileKernel)(TileArgs);
+
+// Raises the kernel's dynamic LDS limit, once per kernel (`slot`) and device.
+int allow_lds(TileKernel kernel, int slot, size_t lds) {
+  static std::atomic<uint64_t> done[8];
+  int dev = 0;
+  const hipError_t g = hipGetDevice(&dev);
+  if (g != hipSuccess) return hip_status(g, "hipGetDevice");
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done[slot].load(std::memory_order_acquire) & bit) return NVFP4_OK;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return hip_status(e, "hipFuncSetAttribute");
+  done[slot].fetch_or(bit, std::memory_order_release);
+  return NVFP4_OK;
+}
+
+// The launch that follows a tile kernel: joins the channel splits.
+int join(const TileArgs& a, hipStream_t s) {
+  int st = launch_status("tile kernel");
+  if (st || a.splits == 1) return st;
+  const int64_t quads = (int64_t)a.tokens * (a.ldp >> 2);
+  const int64_t want = (quads + 255) / 256;
+  join_kernel<<<(unsigned)(want < 4096 ? want : 4096), 256, 0, s>>>(a);
+  return launch_status("join_kernel");
+}
+
+unsigned tile_grid(const TileArgs& a) { return (unsigned)(a.tiles_m * a.tiles_n * a.splits); }
+
+template <int TM, int TN, int WM, int WN, int OCC>
+int run_mx(int slot, const TileArgs& a, hipStream_t s) {
+  constexpr size_t lds = 4 * (size_t)32 * (TM * WM + TN * WN) * 68;
+  const int st = allow_lds(mx_tile_kernel<TM, TN, WM, WN, OCC>, slot, lds);
+  if (st) return st;
+  mx_tile_kernel<TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, lds, s>>>(a);
+  return join(a, s);
+}
+
+template <bool F16, int TM, int TN, int WM, int WN, int OCC>
+int run_nv(int slot, const TileArgs& a, hipStream_t s) {
+  constexpr size_t lds = 3 * (size_t)32 * (TM * WM * 128 + TN * WN * 36);
+  const int st = allow_lds(nv_tile_kernel<F16, TM, TN, WM, WN, OCC>, slot, lds);
+  if (st) return st;
+  nv_tile_kernel<F16, TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, lds, s>>>(a);
+  return join(a, s);
+}
+
+int launch_prep(const PrepArgs& a, hipStream_t s) {
+  const int64_t total = (int64_t)a.steps * a.out_pad + (a.xs ? (int64_t)a.steps * a.tokens_pad : 0) +
+                        (a.xh ? (int64_t)a.tokens * (a.k >> 4) : 0);
+  const int64_t want = (total + 255) / 256;
+  prep_kernel<<<(unsigned)(want < 8192 ? want : 8192), 256, 0, s>>>(a);
+  return launch_status("prep_kernel");
+}
+
+}  // namespace
+
+// Byte offsets inside a tile's rows and inside the scale words stay below 2^31.
+bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
+  const int64_t lim = INT64_C(1) << 31;
+  const int64_t steps = (k + (mx ? 127 : 63)) / (mx ? 128 : 64);
+  return 256 * ldx_bytes < lim && 256 * k < lim && steps * (out + 255) * 4 < lim && steps * (tokens + 255) * 4 < lim &&
+         (out + 127) / 128 * ((tokens + 127) / 128) < lim / 64;
+}
+
+size_t tile_product_workspace(int64_t tokens, int64_t out, int64_t k, bool mx) {
+  return plan_product(tokens, out, k, mx).bytes;
+}
+
+int launch_tile_mx(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp, const uint8_t* we,
+                   int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s) {
+  const Plan p = plan_product(tokens, out, k, true);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  PrepArgs q{};
+  q.ws = we;
+  q.wdst = reinterpret_cast<uint32_t*>(base + p.ws);
+  q.xs = xe;
+  q.xdst = reinterpret_cast<uint32_t*>(base + p.xs);
+  q.tokens = (int)tokens;
+  q.out = (int)out;
+  q.nb = (int)(k / 32);
+  q.tokens_pad = p.tokens_pad;
+  q.out_pad = p.out_pad;
+  q.steps = p.steps;
+  q.k = (int)k;
+  int st = launch_prep(q, s);
+  if (st) return st;
+  TileArgs a{};
+  a.x = xp;
+  a.w = wp;
+  a.xs = q.xdst;
+  a.ws = q.wdst;
+  a.y = y;
+  a.partial = reinterpret_cast<float*>(base + p.partial);
+  a.ldx = a.ldw = k / 2;
+  a.ldy = ldy;
+  a.ldp = (out + 3) / 4 * 4;
+  a.tokens = (int)tokens;
+  a.out = (int)out;
+  a.k = (int)k;
+  a.tokens_pad = p.tokens_pad;
+  a.out_pad = p.out_pad;
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  a.splits = p.splits;
+  a.steps = p.steps;
+  if (p.large) return run_mx<4, 4, 2, 2, 1>(0, a, s);
+  return run_mx<2, 2, 2, 2, 2>(1, a, s);
+}
+
+int launch_tile_nv(const uint16_t* x, int64_t ldx, const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens,
+                   int64_t k, const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y,
+                   int64_t ldy, void* workspace, hipStream_t s) {
+  const Plan p = plan_product(tokens, out, k, false);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const bool f16 = xp != nullptr;
+  PrepArgs q{};
+  q.ws = wc;
+  q.wdst = reinterpret_cast<uint32_t*>(base + p.ws);
+  q.xp = xp;
+  q.xc = xc;
+  q.xh = f16 ? reinterpret_cast<uint16_t*>(base + p.xh) : nullptr;
+  q.tokens = (int)tokens;
+  q.out = (int)out;
+  q.nb = (int)(k / 16);
+  q.tokens_pad = p.tokens_pad;
+  q.out_pad = p.out_pad;
+  q.steps = p.steps;
+  q.k = (int)k;
+  int st = launch_prep(q, s);
+  if (st) return st;
+  TileArgs a{};
+  a.x = reinterpret_cast<const uint8_t*>(f16 ? q.xh : x);
+  a.w = wp;
+  a.ws = q.wdst;
+  a.s0 = ws2;
+  a.s1 = xs2;
+  a.y = y;
+  a.partial = reinterpret_cast<float*>(base + p.partial);
+  a.ldx = (f16 ? k : ldx) * 2;
+  a.ldw = k / 2;
+  a.ldy = ldy;
+  a.ldp = (out + 3) / 4 * 4;
+  a.tokens = (int)tokens;
+  a.out = (int)out;
+  a.k = (int)k;
+  a.tokens_pad = p.tokens_pad;
+  a.out_pad = p.out_pad;
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  a.splits = p.splits;
+  a.steps = p.steps;
+  if (f16) {
+    if (p.large) return run_nv<true, 8, 2, 1, 4, 1>(2, a, s);
+    return run_nv<true, 2, 2, 2, 2, 2>(3, a, s);
+  }
+  if (p.large) return run_nv<false, 8, 2, 1, 4, 1>(4, a, s);
+  return run_nv<false, 4, 1, 1, 4, 2>(5, a, s);
+}
+
+}  // namespace nvfp4
