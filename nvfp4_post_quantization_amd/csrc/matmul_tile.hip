@@ -25,7 +25,7 @@
 // Block scales lie a row apart in memory, one short run per row and stage; a
 // small launch first writes them as one word per (stage, row), rows adjacent,
 // padded with zeros, so that a stage's scales are one contiguous load.
-#include <atomic>
+#include <type_traits>
 
 #include "common.hpp"
 #include "product_device.hpp"
@@ -34,19 +34,26 @@ namespace nvfp4 {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_buffer(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+// A raw buffer resource: loads past `bytes` return zero.
+__device__ __forceinline__ i32x4 make_buffer(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), (int)bytes, 0x00020000};
 }
 
 // 16 (4) bytes a lane from the buffer to LDS at dst + 16 (4) lane; dst is
-// uniform over the wave.
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t b, uint8_t* dst, uint32_t offset, int base) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)dst, 16, (int)offset, base, 0, 0);
+// uniform over the wave.  In assembly because the compiler, which cannot tell
+// the stages apart, waits for every load in flight before the next read of
+// LDS; these write no register, and the kernels wait for them by count.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
-__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t b, uint8_t* dst, uint32_t offset, int base) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)dst, 4, (int)offset, base, 0, 0);
+__device__ __forceinline__ void load_lds16(i32x4 b, uint32_t dst, uint32_t offset, int base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"s"(dst), "v"(offset), "s"(b), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(i32x4 b, uint32_t dst, uint32_t offset, int base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               ::"s"(dst), "v"(offset), "s"(b), "s"(base) : "memory", "m0");
 }
 
 template <int N>
@@ -156,8 +163,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx_tile_kernel(TileArgs a) 
   constexpr int XL = BM / 16 / NW, WL = BN / 16 / NW, SL = (BM + BN) / 64 / NW;     // loads of a wave per stage
   constexpr int LOADS = XL + WL + SL;
   static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0 && (BM + BN) % (64 * NW) == 0 && BM % 64 == 0, "tile split");
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NBUF * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds_base = lds_address(lds);
   const TilePos pos = tile_of(a);
   const int t0 = pos.m * BM, o0 = pos.n * BN;
   const int s_begin = (int)((int64_t)a.steps * pos.split / a.splits);
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx_tile_kernel(TileArgs a) 
     wo[i] = (uint32_t)(min((wave + i * NW) * 16 + (lane >> 2), rows_w - 1) * a.ldw + piece * 16);
 
   auto load_stage = [&](int s) {
-    uint8_t* dst = lds + (s & (NBUF - 1)) * STAGE;
+    const uint32_t dst = lds_base + (s & (NBUF - 1)) * STAGE;
     const bool cut = (s + 1) * 128 > a.k && s * 128 + piece * 32 >= a.k;      // this lane's piece lies beyond k
 #pragma unroll
     for (int i = 0; i < XL; ++i)
@@ -226,6 +234,16 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx_tile_kernel(TileArgs a) 
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
 
+  auto multiply = [&](int set) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+        acc[n][m] = mfma32_mx(wr[set][n], wsr[0][n], xr[set][m], xsr[0][m], acc[n][m], set);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
   if (s_begin < s_end) {
 #pragma unroll
     for (int i = 0; i < NBUF - 1; ++i)
@@ -236,29 +254,29 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx_tile_kernel(TileArgs a) 
     __builtin_amdgcn_s_barrier();
     read_scales(0, s_begin);
     read_frags(0, s_begin);
-    for (int s = s_begin; s < s_end; ++s) {
+    // one stage; AHEAD: how many more stages follow, 3 standing for more
+    auto step = [&](int s, auto ahead_c) {
+      constexpr int AHEAD = decltype(ahead_c)::value;
       read_frags(1, s);
-#pragma unroll
-      for (int n = 0; n < TN; ++n)
-#pragma unroll
-        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_mx(wr[0][n], wsr[0][n], xr[0][m], xsr[0][m], acc[n][m], 0);
-      if (s + 1 < s_end) {
-        if (s + 2 < s_end) wait_loads<LOADS>();
-        else wait_loads<0>();
+      multiply(0);
+      if constexpr (AHEAD > 0) {
+        wait_loads<AHEAD >= 2 ? LOADS : 0>();
         __builtin_amdgcn_s_barrier();
-        if (s + 3 < s_end) load_stage(s + 3);
+        if constexpr (AHEAD >= 3) load_stage(s + 3);
         read_scales(1, s + 1);
         read_frags(0, s + 1);
       }
-#pragma unroll
-      for (int n = 0; n < TN; ++n)
-#pragma unroll
-        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_mx(wr[1][n], wsr[0][n], xr[1][m], xsr[0][m], acc[n][m], 1);
+      multiply(1);
 #pragma unroll
       for (int i = 0; i < TM; ++i) xsr[0][i] = xsr[1][i];
 #pragma unroll
       for (int i = 0; i < TN; ++i) wsr[0][i] = wsr[1][i];
-    }
+    };
+    int s = s_begin;
+    for (; s + 3 < s_end; ++s) step(s, std::integral_constant<int, 3>{});
+    if (s + 2 < s_end) step(s++, std::integral_constant<int, 2>{});
+    if (s + 1 < s_end) step(s++, std::integral_constant<int, 1>{});
+    step(s, std::integral_constant<int, 0>{});
   }
   store_tiles<TN, TM>(a, acc, o0 + wn * TN * 32, t0 + wm * TM * 32, pos.split);
 }
@@ -284,8 +302,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) 
   constexpr int SL = (BN / 64 + NW - 1) / NW;
   constexpr int LOADS = XL + WL + SL;
   static_assert(BM % (8 * NW) == 0 && BN % (32 * NW) == 0, "tile split");
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds_base = lds_address(lds);
   const TilePos pos = tile_of(a);
   const int t0 = pos.m * BM, o0 = pos.n * BN;
   const int s_begin = (int)((int64_t)a.steps * pos.split / a.splits);
@@ -307,7 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) 
     wo[i] = (uint32_t)(min((wave + i * NW) * 32 + (lane >> 1), rows_w - 1) * a.ldw + wpiece * 16);
 
   auto load_stage = [&](int s, int buf) {
-    uint8_t* dst = lds + buf * STAGE;
+    const uint32_t dst = lds_base + buf * STAGE;
     const bool last = (s + 1) * 64 > a.k;
     const bool xcut = last && s * 64 + xpiece * 8 >= a.k, wcut = last && s * 64 + wpiece * 32 >= a.k;
 #pragma unroll
@@ -371,7 +390,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) 
     int buf = 0;
     read_w(0);
     read_x(0, 0, 0);
-    for (int s = s_begin; s < s_end; ++s) {
+    // one stage; AHEAD: how many more stages follow, 2 standing for more
+    auto step = [&](int s, auto ahead_c) {
+      constexpr int AHEAD = decltype(ahead_c)::value;
       const int next = buf == 2 ? 0 : buf + 1, after = next == 2 ? 0 : next + 1;
 #pragma unroll
       for (int n = 0; n < TN; ++n) { wr[n] = wr_next[n]; wsr[n] = wsr_next[n]; }
@@ -379,10 +400,10 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) 
       for (int j = 0; j < 4; ++j) {
         if (j < 3) {
           read_x((j + 1) & 1, j + 1, buf);
-        } else if (s + 1 < s_end) {
+        } else if constexpr (AHEAD > 0) {
           wait_loads<0>();
           __builtin_amdgcn_s_barrier();
-          if (s + 2 < s_end) load_stage(s + 2, after);
+          if constexpr (AHEAD >= 2) load_stage(s + 2, after);
           read_w(next);
           read_x(0, 0, next);
         }
@@ -394,7 +415,11 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void nv_tile_kernel(TileArgs a) 
         }
       }
       buf = next;
-    }
+    };
+    int s = s_begin;
+    for (; s + 2 < s_end; ++s) step(s, std::integral_constant<int, 2>{});
+    if (s + 1 < s_end) step(s++, std::integral_constant<int, 1>{});
+    step(s, std::integral_constant<int, 0>{});
   }
   store_tiles<TN, TM>(a, acc, o0 + wn * TN * 32, t0 + wm * TM * 32, pos.split);
 }
@@ -504,23 +529,6 @@ Plan plan_product(int64_t tokens, int64_t out, int64_t k, bool mx) {
   return p;
 }
 
-typedef void (*TileKernel)(TileArgs);
-
-// Raises the kernel's dynamic LDS limit, once per kernel (`slot`) and device.
-int allow_lds(TileKernel kernel, int slot, size_t lds) {
-  static std::atomic<uint64_t> done[8];
-  int dev = 0;
-  const hipError_t g = hipGetDevice(&dev);
-  if (g != hipSuccess) return hip_status(g, "hipGetDevice");
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done[slot].load(std::memory_order_acquire) & bit) return NVFP4_OK;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return hip_status(e, "hipFuncSetAttribute");
-  done[slot].fetch_or(bit, std::memory_order_release);
-  return NVFP4_OK;
-}
-
 // The launch that follows a tile kernel: joins the channel splits.
 int join(const TileArgs& a, hipStream_t s) {
   int st = launch_status("tile kernel");
@@ -534,20 +542,14 @@ int join(const TileArgs& a, hipStream_t s) {
 unsigned tile_grid(const TileArgs& a) { return (unsigned)(a.tiles_m * a.tiles_n * a.splits); }
 
 template <int TM, int TN, int WM, int WN, int OCC>
-int run_mx(int slot, const TileArgs& a, hipStream_t s) {
-  constexpr size_t lds = 4 * (size_t)32 * (TM * WM + TN * WN) * 68;
-  const int st = allow_lds(mx_tile_kernel<TM, TN, WM, WN, OCC>, slot, lds);
-  if (st) return st;
-  mx_tile_kernel<TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, lds, s>>>(a);
+int run_mx(const TileArgs& a, hipStream_t s) {
+  mx_tile_kernel<TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, 0, s>>>(a);
   return join(a, s);
 }
 
 template <bool F16, int TM, int TN, int WM, int WN, int OCC>
-int run_nv(int slot, const TileArgs& a, hipStream_t s) {
-  constexpr size_t lds = 3 * (size_t)32 * (TM * WM * 128 + TN * WN * 36);
-  const int st = allow_lds(nv_tile_kernel<F16, TM, TN, WM, WN, OCC>, slot, lds);
-  if (st) return st;
-  nv_tile_kernel<F16, TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, lds, s>>>(a);
+int run_nv(const TileArgs& a, hipStream_t s) {
+  nv_tile_kernel<F16, TM, TN, WM, WN, OCC><<<tile_grid(a), 64 * WM * WN, 0, s>>>(a);
   return join(a, s);
 }
 
@@ -610,8 +612,8 @@ int launch_tile_mx(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t
   a.tiles_n = p.tiles_n;
   a.splits = p.splits;
   a.steps = p.steps;
-  if (p.large) return run_mx<4, 4, 2, 2, 1>(0, a, s);
-  return run_mx<2, 2, 2, 2, 2>(1, a, s);
+  if (p.large) return run_mx<4, 4, 2, 2, 1>(a, s);
+  return run_mx<2, 2, 2, 2, 2>(a, s);
 }
 
 int launch_tile_nv(const uint16_t* x, int64_t ldx, const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens,
@@ -657,11 +659,11 @@ int launch_tile_nv(const uint16_t* x, int64_t ldx, const uint8_t* xp, const uint
   a.splits = p.splits;
   a.steps = p.steps;
   if (f16) {
-    if (p.large) return run_nv<true, 8, 2, 1, 4, 1>(2, a, s);
-    return run_nv<true, 2, 2, 2, 2, 2>(3, a, s);
+    if (p.large) return run_nv<true, 8, 2, 1, 4, 1>(a, s);
+    return run_nv<true, 2, 2, 2, 2, 2>(a, s);
   }
-  if (p.large) return run_nv<false, 8, 2, 1, 4, 1>(4, a, s);
-  return run_nv<false, 4, 1, 1, 4, 2>(5, a, s);
+  if (p.large) return run_nv<false, 8, 2, 1, 4, 1>(a, s);
+  return run_nv<false, 4, 1, 1, 4, 2>(a, s);
 }
 
 }  // namespace nvfp4

@@ -235,7 +235,7 @@ def test_product_nan_scales_stay_in_their_row(kind, tokens):
 def test_product_full_size_sampled(kind):
     """Gate projection over a prompt batch and down projection over a short
     ragged one, sampled rows against the oracle."""
-    for tokens, out, k in ((2048, 12288, 4096), (333, 4096, 12288)):
+    for tokens, out, k in ((2048, 12288, 4096), (333, 4096, 12288), (2049, 6200, 160), (3333, 4100, 608)):
         note(f"{kind} tokens={tokens} out={out} k={k}")
         c = Case(kind, np.random.default_rng(k), tokens, out, k)
         y = c.fn(*c.args, workspace=c.workspace(0xFF))
