@@ -513,7 +513,7 @@ NVFP4_CHECKED int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int6
  *
  * x_packed [tokens][k/2], x_e8m0 [tokens][k/32], w_packed [out_features][k/2],
  * w_e8m0 [out_features][k/32]: uint8, contiguous, 16-byte aligned;
- * k % 32 == 0; tokens, out_features and k below 2^31.
+ * k % 32 == 0, k at most 2^26; tokens and out_features below 2^31 - 15.
  * y          [tokens][ldy] bf16, columns 0..out_features-1; any ldy >=
  *            out_features (other columns are left as they were).
  * workspace  16-byte aligned, at least mxfp4_matmul_workspace_bytes(tokens,
@@ -541,8 +541,8 @@ NVFP4_CHECKED int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, i
  * x          w4a16: [tokens][ldx] bf16, columns 0..k-1, 16-byte aligned rows.
  * x_packed, x_codes  w4a4: [tokens][k/2], [tokens][k/16].
  * w_packed, w_codes  [out_features][k/2], [out_features][k/16].  All packed
- *            and code arrays: uint8, contiguous, 16-byte aligned; k % 16 == 0;
- *            tokens, out_features and k below 2^31.
+ *            and code arrays: uint8, contiguous, 16-byte aligned; k % 16 == 0,
+ *            k at most 2^26; tokens and out_features below 2^31 - 15.
  * x_scale2, w_scale2  device float[1].
  * y, workspace: as for mxfp4_matmul, with nvfp4_matmul_workspace_bytes (one
  *            size serves both).
@@ -601,7 +601,7 @@ NVFP4_CHECKED int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t e
  *            w2_scale2 float[experts].  Packed and code arrays 16-byte aligned.
  * y          [tokens][ldy] bf16, columns 0..hidden-1; any ldy >= hidden.
  * tokens     0 .. 64;  top_k 1 .. 16;  experts 1 .. 1024.
- * hidden, inter: multiples of 16 below 2^31.
+ * hidden, inter: multiples of 16, at most 2^26, their product below 2^31.
  * workspace  16-byte aligned, at least nvfp4_moe_workspace_bytes(tokens, top_k,
  *            inter) bytes; scratch.
  * Errors: NULL_ARG, BAD_SHAPE, BAD_INPUT (tokens, top_k or experts out of

@@ -402,11 +402,12 @@ int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int6
   return launch_mxfp4_dequant(packed, e8m0, rows, k, out, as_stream(stream));
 }
 
-// Sizes of a product: every extent below 2^31 (the kernels index rows and
-// columns with 32 bits and form byte offsets in 64).
+// Sizes of a product: rows and columns are indexed with 32 bits, and 16 rows of
+// packed channels have 32-bit offsets.
+constexpr int64_t kMaxChannels = INT64_C(1) << 26;
 static int check_product(int64_t tokens, int64_t out, int64_t k, int64_t block, int64_t ldy) {
   if (tokens < 0 || out <= 0 || k <= 0 || k % block || ldy < out) return NVFP4_ERR_BAD_SHAPE;
-  if (tokens > INT32_MAX || out > INT32_MAX || k > INT32_MAX) return NVFP4_ERR_BAD_SHAPE;
+  if (tokens > INT32_MAX || out > INT32_MAX - 15 || k > kMaxChannels) return NVFP4_ERR_BAD_SHAPE;
   return check_matrix(tokens, out, ldy, 2);
 }
 
@@ -491,7 +492,7 @@ int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_
 
 size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
   if (tokens <= 0 || tokens > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK) return 0;
-  if (inter <= 0 || inter % 16 || inter > INT32_MAX) return 0;
+  if (inter <= 0 || inter % 16 || inter > kMaxChannels) return 0;
   return moe_workspace_bytes(tokens, top_k, inter);
 }
 
@@ -502,10 +503,10 @@ int nvfp4_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
                       size_t workspace_bytes, void* stream) {
   int st = check_matrix(tokens, hidden, ldx, 2);
   if (st || (st = check_matrix(tokens, hidden, ldy, 2))) return st;
-  if (hidden % 16 || inter <= 0 || inter % 16 || hidden > INT32_MAX || inter > INT32_MAX) return NVFP4_ERR_BAD_SHAPE;
+  if (hidden % 16 || inter <= 0 || inter % 16 || hidden > kMaxChannels || inter > kMaxChannels) return NVFP4_ERR_BAD_SHAPE;
+  if (hidden * inter >= INT64_C(1) << 31) return NVFP4_ERR_BAD_SHAPE;          // 32-bit offsets within an expert
   if (tokens > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || experts < 1 || experts > kMoeMaxExperts)
     return NVFP4_ERR_BAD_INPUT;
-  if (!mul_fits(hidden, inter) || !mul_fits(hidden * inter, 2 * experts)) return NVFP4_ERR_BAD_SHAPE;
   if (!w13_packed || !w13_codes || !w13_scale2 || !w2_packed || !w2_codes || !w2_scale2 ||
       ((!x || !ids || !weights || !y) && tokens > 0))
     return NVFP4_ERR_NULL_ARG;

@@ -3,11 +3,12 @@
 // W4A4 tiers) and for MXFP4 on both sides.
 //
 // Few tokens: the weights are read once and bound the call.  A workgroup
-// takes 16 RT output rows and splits the channels over its waves; each wave
-// streams its share of the rows straight from HBM into registers, expands it
-// there, and multiplies it by up to 16 NT tokens on the matrix cores (the
-// rows are the instruction's M side, the tokens its N side).  The waves'
-// partial tiles meet in LDS and are added in wave order.
+// takes a run of 16-row tiles, as many workgroups as there are CUs; its eight
+// waves split the channels, hold their part of the tokens in registers and
+// stream the rows' packed weights past them from HBM, expanding them in
+// registers for the matrix cores (the rows are the instruction's M side, the
+// tokens its N side).  The waves' partial tiles meet in LDS and are added in
+// wave order.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -28,10 +29,6 @@ struct ProductArgs {
   int tokens, out, k;
 };
 
-// Bytes of a row's block scales.
-template <int KIND>
-__device__ __forceinline__ int64_t scale_row(int k) { return KIND == kMX ? k >> 5 : k >> 4; }
-
 template <int KIND>
 __device__ __forceinline__ float tensor_scaled(float v, const ProductArgs& a) {
   if constexpr (KIND == kW4A16) return v * *a.ws2;
@@ -39,71 +36,70 @@ __device__ __forceinline__ float tensor_scaled(float v, const ProductArgs& a) {
   else return v;
 }
 
-template <int KIND, int RT, int NT, int NW, bool K32>
-__global__ __launch_bounds__(64 * NW) void few_tokens_kernel(ProductArgs a) {
-  __shared__ f32x4 part[NW][RT * NT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row0 = blockIdx.x * 16 * RT;
+template <int KIND, int NT, int QW>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void few_tokens_kernel(ProductArgs a) {
+  constexpr int RT = 2 / QW, TB = 4 / RT / NT;
+  __shared__ f32x4 part[kStreamWaves * TB * RT * NT * 64];
+  const int lane = threadIdx.x & 63, r16 = lane & 15;
+  const int tiles = (a.out + 15) >> 4;
+  const int begin = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
   const int tok0 = blockIdx.y * 16 * NT;
-  ProductRows<RT, NT> p;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int64_t row = min(row0 + 16 * r + (lane & 15), a.out - 1);      // rows past the end are not stored
-    p.wp[r] = a.wp + row * (a.k >> 1);
-    p.wc[r] = a.wc + row * scale_row<KIND>(a.k);
-  }
+  const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> (KIND == kMX ? 5 : 4);
+  TokenRows tokens[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int64_t t = min(tok0 + 16 * n + (lane & 15), a.tokens - 1);
-    p.xp[n] = a.xp + t * a.ldx;
-    p.xc[n] = a.xc + t * scale_row<KIND>(a.k);
-  }
-  f32x4 acc[RT][NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int units = (a.k + 127) >> 7;
-  const int per = (units + NW - 1) / NW;
-  product_units<KIND, RT, NT, K32, false, (NT > 1 ? 1 : 2)>(acc, p, min(wave * per, units), min((wave + 1) * per, units),
-                                                           lane >> 4, a.k, 0);
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) part[wave][r * NT + n][lane] = acc[r][n];
-  __syncthreads();
-  for (int i = threadIdx.x; i < RT * NT * 64; i += 64 * NW) {
-    const int tile = i >> 6, l = i & 63;
-    f32x4 s = part[0][tile][l];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) s += part[w][tile][l];
-    const int row = row0 + 16 * (tile / NT) + 4 * (l >> 4);
-    const int t = tok0 + 16 * (tile % NT) + (l & 15);
-    if (t < a.tokens) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (row + e < a.out) a.y[t * a.ldy + row + e] = to_bf16(tensor_scaled<KIND>(s[e], a));
+    const int t0 = min(tok0 + 16 * n, a.tokens - 1);             // tokens past the end are not stored
+    const int t = min(r16, a.tokens - 1 - t0);
+    if constexpr (KIND == kW4A16) {
+      tokens[n].x = a.xp + (int64_t)(t0 + t) * a.ldx;
+    } else {
+      const uint32_t rows = min(16, a.tokens - t0);
+      tokens[n].packed = PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds};
+      tokens[n].row_w = t * ldw;
+      tokens[n].row_s = t * lds;
     }
   }
+  auto rows_of = [&](int t) {
+    const int row = t * 16;
+    const uint32_t rows = min(min(16 * RT, (end - t) * 16), a.out - row);
+    return PackedRows{a.wp + (int64_t)row * ldw, a.wc + (int64_t)row * lds, rows * ldw, rows * lds};
+  };
+  auto done = [&](int t, int n, int l, auto sum) {
+    const int row = t * 16 + 4 * (l >> 4), tok = tok0 + 16 * n + (l & 15);
+    if (tok >= a.tokens || row >= a.out) return;
+    const f32x4 v = sum(l);
+    uint16_t* dst = a.y + (int64_t)tok * a.ldy + row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row + e < a.out) dst[e] = to_bf16(tensor_scaled<KIND>(v[e], a));
+  };
+  stream_tiles<KIND, NT, QW, TB>(begin, end, a.k, r16 * ldw, r16 * lds, 16 * ldw, 16 * lds, tokens, part, rows_of, done);
 }
 
-template <int KIND, int RT, int NT, int NW, bool K32>
-void run_few(const ProductArgs& a, hipStream_t s) {
-  const dim3 grid((a.out + 16 * RT - 1) / (16 * RT), (a.tokens + 16 * NT - 1) / (16 * NT));
-  few_tokens_kernel<KIND, RT, NT, NW, K32><<<grid, 64 * NW, 0, s>>>(a);
-}
+constexpr int kCus = 256;
 
-template <int KIND, bool K32>
-int run(const ProductArgs& a, hipStream_t s) {
-  if (a.tokens <= 16) run_few<KIND, 1, 1, 8, K32>(a, s);
-  else run_few<KIND, 2, 2, 8, K32>(a, s);
+template <int KIND, int NT, int QW>
+int run_few(const ProductArgs& a, hipStream_t s) {
+  const int tiles = (a.out + 15) / 16;
+  const dim3 grid(tiles < kCus ? tiles : kCus, (a.tokens + 16 * NT - 1) / (16 * NT));
+  few_tokens_kernel<KIND, NT, QW><<<grid, 64 * kStreamWaves, 0, s>>>(a);
   return launch_status("few_tokens_kernel");
+}
+
+// One quad of the tokens a wave and two row tiles at a time where that covers
+// the channels, else two quads and one row tile.
+template <int KIND>
+int run(const ProductArgs& a, hipStream_t s) {
+  const bool one = a.k <= 512 * kStreamWaves;
+  if (a.tokens <= 16) return one ? run_few<KIND, 1, 1>(a, s) : run_few<KIND, 1, 2>(a, s);
+  return run_few<KIND, 2, 1>(a, s);
 }
 
 }  // namespace
 
 // Tokens up to which the streaming kernel is used.
-constexpr int64_t kFewTokens = 64;
+constexpr int64_t kFewTokens = 32;
 
 static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
   return tokens > kFewTokens && tile_product_fits(tokens, out, k, mx, ldx_bytes);
@@ -119,7 +115,7 @@ int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ld
     return launch_tile_nv(x, ldx, nullptr, nullptr, nullptr, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s);
   const ProductArgs a{reinterpret_cast<const uint8_t*>(x), nullptr, nullptr, wp, wc, ws2, ldx * 2, ldy, y, (int)tokens,
                       (int)out, (int)k};
-  return (k % 32) ? run<kW4A16, false>(a, s) : run<kW4A16, true>(a, s);
+  return run<kW4A16>(a, s);
 }
 
 int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens, int64_t k,
@@ -128,7 +124,7 @@ int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, i
   if (use_tiles(tokens, out, k, false, k * 2))
     return launch_tile_nv(nullptr, 0, xp, xc, xs2, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s);
   const ProductArgs a{xp, xc, xs2, wp, wc, ws2, k / 2, ldy, y, (int)tokens, (int)out, (int)k};
-  return (k % 32) ? run<kW4A4, false>(a, s) : run<kW4A4, true>(a, s);
+  return run<kW4A4>(a, s);
 }
 
 int launch_mxfp4_matmul(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp,
@@ -136,7 +132,7 @@ int launch_mxfp4_matmul(const uint8_t* xp, const uint8_t* xe, int64_t tokens, in
   if (use_tiles(tokens, out, k, true, k / 2))
     return launch_tile_mx(xp, xe, tokens, k, wp, we, out, y, ldy, workspace, s);
   const ProductArgs a{xp, xe, nullptr, wp, we, nullptr, k / 2, ldy, y, (int)tokens, (int)out, (int)k};
-  return run<kMX, true>(a, s);
+  return run<kMX>(a, s);
 }
 
 }  // namespace nvfp4

@@ -59,8 +59,6 @@ __device__ __forceinline__ void load_lds4(i32x4 b, uint32_t dst, uint32_t offset
 template <int N>
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
-constexpr uint32_t kBeyond = 0x80000000u;           // past any buffer here (below 2^31 bytes): reads as zero
-
 // Piece swizzles of LDS rows of 64, 128 and 32 bytes: piece p of a row lies at
 // place p ^ swizzle.  A 16-byte read of a wave is served in four groups of 16
 // lanes (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; the same + 32) over 64 banks;

@@ -6,11 +6,12 @@
 //          weight(t, e) * W2_e ( silu(W1_e x[t]) * (W3_e x[t]) )
 //
 // The experts' weights, read once each, bound the layer.  Two launches: the
-// first makes h = weight * s2 * silu(gate) * up for every (token, expert)
-// pair, the second adds W2_e h over the experts of each token inside the
-// matrix accumulators, in a fixed order, so the result is reproducible.
-// Who goes where is worked out again from the ids by every workgroup (at
-// most 1024 of them), which costs less than a launch that writes it down.
+// first makes h = weight * s2 * silu(gate) * up for every (expert, token)
+// pair, the second adds W2_e h over the experts of each token, in a fixed
+// order, so the result is reproducible.  Who goes where is worked out again
+// from the ids by every workgroup (at most 1024 of them), which costs less
+// than a launch that writes it down: a 64-bit token mask per expert, and the
+// list of the jobs to do.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -18,9 +19,8 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kMaxIds = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kUpWaves = 8;
-constexpr int kDownWaves = 8;
+constexpr int kCus = 256;
+constexpr int kMaxJobs = kMoeMaxTokens * kMoeMaxTopK;
 
 struct MoeArgs {
   const uint8_t* x;               // bf16 rows
@@ -31,220 +31,269 @@ struct MoeArgs {
   const float *s13, *s2;
   uint16_t* y;
   int64_t ldy;
-  uint16_t* h;                    // [tokens * top_k][inter] bf16, then the same for the low parts
+  uint16_t* h;                    // [pairs][ldh] bf16, then the same for the low parts
+  int64_t ldh;                    // inter rounded up to whole quads, zero past inter
   int64_t lo;                     // bytes from a value's high part to its low part
   int tokens, hidden, inter, experts, top_k;
 };
 
+// A job is a chosen expert with up to 16 of its tokens.
 struct Routing {
-  int32_t ids[kMaxIds];
-  uint32_t bits[kMoeMaxExperts / 32];
-  uint16_t active[kMoeMaxExperts];        // the chosen experts in ascending order
-  int count;
+  uint32_t mask[kMoeMaxExperts][2];       // tokens of an expert
+  uint16_t expert[kMaxJobs];              // by job: its expert, experts in ascending order,
+  uint16_t base[kMaxJobs];                // its first pair (rows of h),
+  uint8_t first[kMaxJobs];                // its first token's place among the expert's
+  uint32_t part[16];                      // per wave: jobs and pairs (upper half)
+  int jobs;
 };
 
-// Fill r from the ids (all threads; syncs).
+__device__ __forceinline__ uint64_t tokens_of(const Routing& r, int e) {
+  return (uint64_t)r.mask[e][1] << 32 | r.mask[e][0];
+}
+
+// Fill r from the ids (all threads, THREADS of them; syncs).
+template <int THREADS>
 __device__ __forceinline__ void read_routing(Routing& r, const MoeArgs& a) {
-  const int n = a.tokens * a.top_k;
-  for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += blockDim.x) r.bits[i] = 0;
+  constexpr int PER = kMoeMaxExperts / THREADS;
+  const int n = a.tokens * a.top_k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < 2 * a.experts; i += THREADS) (&r.mask[0][0])[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = a.ids[i];
-    const bool ok = e >= 0 && e < a.experts;
-    r.ids[i] = ok ? e : -1;
-    if (ok) atomicOr(&r.bits[e >> 5], 1u << (e & 31));
+  for (int i = tid; i < n; i += THREADS) {
+    const int e = a.ids[i], t = i / a.top_k;
+    if (e >= 0 && e < a.experts) atomicOr(&r.mask[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
-  if (threadIdx.x < kMoeMaxExperts / 32) {
-    int base = 0;
-    for (int i = 0; i < (int)threadIdx.x; ++i) base += __popc(r.bits[i]);
-    uint32_t b = r.bits[threadIdx.x];
-    while (b) {
-      r.active[base++] = (uint16_t)(threadIdx.x * 32 + __ffs(b) - 1);
-      b &= b - 1;
+  // prefix sums over the experts, PER of them a thread: jobs in the lower half
+  // of the word, pairs (at most 1024) in the upper
+  uint32_t own[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    const uint32_t c = e < a.experts ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0;
+    own[i] = (c + 15) >> 4 | c << 16;
+    sum += own[i];
+  }
+  uint32_t scan = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_up(scan, d);
+    if (lane >= d) scan += o;
+  }
+  if (lane == 63) r.part[wave] = scan;
+  __syncthreads();
+  uint32_t before = scan - sum;
+  uint32_t all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) before += r.part[w];
+    all += r.part[w];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    for (int q = 0; q < (int)(own[i] & 0xFFFF); ++q) {
+      const int job = (before & 0xFFFF) + q;
+      r.expert[job] = (uint16_t)(tid * PER + i);
+      r.base[job] = (uint16_t)((before >> 16) + 16 * q);
+      r.first[job] = (uint8_t)(16 * q);
     }
-    if (threadIdx.x == kMoeMaxExperts / 32 - 1) r.count = base;
+    before += own[i];
   }
+  if (tid == 0) r.jobs = (int)(all & 0xFFFF);
   __syncthreads();
 }
 
-// First place s of expert e among token t's choices, or -1; *weight adds up
-// all of them (an expert named twice counts once, with both weights).
-__device__ __forceinline__ int find_choice(const Routing& r, const MoeArgs& a, int t, int e, float* weight) {
-  int first = -1;
+// The place-th set bit of a nonzero mask, for place = first + lane % 16 (the
+// last one for places beyond).
+__device__ __forceinline__ int token_of_column(uint64_t mask, int first) {
+  const int lane = threadIdx.x & 63;
+  const int n = __popcll(mask);
+  const int rank = __popcll(mask & ((1ull << lane) - 1));
+  // lane t sends t to lane rank(t); lanes whose bit is clear send to a lane of
+  // their own past the set bits
+  const int to = (mask >> lane) & 1 ? rank : n + lane - rank;
+  const int t = __builtin_amdgcn_ds_permute(to * 4, lane);
+  return __shfl(t, min(first + (lane & 15), n - 1));
+}
+
+// What a token gives an expert (all places that name it).
+__device__ __forceinline__ float weight_of(const MoeArgs& a, int t, int e) {
   float w = 0.f;
-  for (int s = a.top_k - 1; s >= 0; --s) {
-    if (r.ids[t * a.top_k + s] == e) {
-      first = s;
-      if (weight) w += a.weights[t * a.top_k + s];
-    }
-  }
-  if (weight) *weight = w;
-  return first;
+  for (int s = 0; s < a.top_k; ++s)
+    if (a.ids[t * a.top_k + s] == e) w += a.weights[t * a.top_k + s];
+  return w;
 }
 
-// h of 16 channels of one expert for its tokens, 16 NT at a time.
-template <int NT, bool K32>
-__device__ __forceinline__ void up_tile(const MoeArgs& a, int e, int row0, int first, int count, const uint8_t* tok,
-                                        const uint16_t* slot, const float* wt, f32x4* part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  ProductRows<2, NT> p;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {                                  // gate row and up row
-    const int64_t row = ((int64_t)e * 2 + r) * a.inter + min(row0 + (lane & 15), a.inter - 1);
-    p.wp[r] = a.p13 + row * (a.hidden >> 1);
-    p.wc[r] = a.c13 + row * (a.hidden >> 4);
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    p.xp[n] = a.x + tok[min(first + 16 * n + (lane & 15), count - 1)] * a.ldx;
-    p.xc[n] = nullptr;
-  }
-  f32x4 acc[2][NT];
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int units = (a.hidden + 127) >> 7, per = (units + kUpWaves - 1) / kUpWaves;
-  product_units<kW4A16, 2, NT, K32, false, (NT > 1 ? 1 : 2)>(acc, p, min(wave * per, units), min((wave + 1) * per, units),
-                                                            lane >> 4, a.hidden, 0);
-  __syncthreads();                                               // the last tile's sums are done with
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) part[(wave * 2 * NT + r * NT + n) * 64 + lane] = acc[r][n];
-  __syncthreads();
-  const float s13 = a.s13[e], s2 = a.s2[e];
-  for (int i = threadIdx.x; i < NT * 64; i += 64 * kUpWaves) {
-    const int n = i >> 6, l = i & 63;
-    f32x4 g = part[n * 64 + l], u = part[(NT + n) * 64 + l];
-#pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) {
-      g += part[(w * 2 * NT + n) * 64 + l];
-      u += part[(w * 2 * NT + NT + n) * 64 + l];
-    }
-    const int c = first + 16 * n + (l & 15), row = row0 + 4 * (l >> 4);
-    if (c < count) {
-      const float scale = wt[c] * s2;
-      uint16_t* dst = a.h + (int64_t)slot[c] * a.inter + row;
+// Where channel c of a row of h is kept: within each unit of 128 channels in
+// the order in which the second launch's lanes read them, piece j (8 channels)
+// of the four chunks of 32 next to each other.
+__device__ __forceinline__ int place_of(int c) {
+  return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
+}
+
+// h of a run of (job, 8 channels) tiles, as many runs as there are workgroups.
+// A row tile holds the gate rows of the channels in rows 0-7 and their up rows
+// in 8-15, so that one pass over the tokens serves both.
+template <int QW>
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void moe_up_kernel(MoeArgs a) {
+  constexpr int RT = 2 / QW, TB = 4 / RT;
+  __shared__ Routing r;
+  __shared__ f32x4 part[kStreamWaves * TB * RT * 64];
+  __shared__ float wt[16];
+  read_routing<64 * kStreamWaves>(r, a);
+  const int lane = threadIdx.x & 63, r16 = lane & 15;
+  const int tiles = a.inter >> 3;
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(r.jobs) * tiles;
+  int64_t begin = total * blockIdx.x / gridDim.x;
+  const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t ldw = (uint32_t)a.hidden >> 1, lds = (uint32_t)a.hidden >> 4;
+  const uint32_t row = (r16 >> 3) * (uint32_t)a.inter + (r16 & 7);
+  while (begin < end) {                              // one job after another
+    const int job = __builtin_amdgcn_readfirstlane((int)(begin / tiles));
+    const int t0 = __builtin_amdgcn_readfirstlane((int)(begin - (int64_t)job * tiles));
+    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)tiles, t0 + end - begin));
+    begin += t1 - t0;
+    const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job], base = r.base[job];
+    const uint64_t mask = tokens_of(r, e);
+    const int count = min(16, __popcll(mask) - first);
+    const int tok = token_of_column(mask, first);
+    if (threadIdx.x < 16) wt[threadIdx.x] = weight_of(a, tok, e) * a.s2[e];
+    const float s13 = a.s13[e];
+    const uint8_t* w = a.p13 + (int64_t)e * 2 * a.inter * ldw;
+    const uint8_t* c = a.c13 + (int64_t)e * 2 * a.inter * lds;
+    TokenRows tokens[1];
+    tokens[0].x = a.x + tok * a.ldx;
+    auto rows_of = [&](int t) {
+      const uint32_t rows = a.inter + min(8 * RT, (t1 - t) * 8);      // to the end of the step's up rows
+      return PackedRows{w + (int64_t)t * 8 * ldw, c + (int64_t)t * 8 * lds, rows * ldw, rows * lds};
+    };
+    auto done = [&](int t, int, int l, auto sum) {
+      if (l >= 32 || (l & 15) >= count) return;
+      const f32x4 gate = sum(l), up = sum(l + 32);
+      const float scale = wt[l & 15];
+      uint32_t hi[4], lo[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (row + q < a.inter) {
-          const float gate = g[q] * s13, up = u[q] * s13;
-          const float h = gate / (1.0f + expf(-gate)) * up * scale;
-          // two bf16 parts keep 16 significant bits of h
-          const uint16_t hi = to_bf16(h);
-          dst[q] = hi;
-          *reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(dst + q) + a.lo) = to_bf16(h - bf16_to_f32(hi));
+        const float v = gate[q] * s13;
+        const float h = v / (1.0f + expf(-v)) * (up[q] * s13) * scale;
+        hi[q] = to_bf16(h);                          // two bf16 parts keep 16 significant bits of h
+        lo[q] = to_bf16(h - bf16_to_f32(hi[q]));
+      }
+      uint16_t* row_h = a.h + (int64_t)(base + (l & 15)) * a.ldh;
+      auto put = [&](int c, uint2 high, uint2 low) {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(row_h + place_of(c));
+        *reinterpret_cast<uint2*>(dst) = high;
+        *reinterpret_cast<uint2*>(dst + a.lo) = low;
+      };
+      put(t * 8 + 4 * (l >> 4), make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
+          make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
+      if (t == tiles - 1)                            // the rest of the row's last quad
+        for (int c = a.inter + 4 * (l >> 4); c < a.ldh; c += 8) put(c, make_uint2(0, 0), make_uint2(0, 0));
+    };
+    stream_tiles<kW4A16, 1, QW, TB>(t0, t1, a.hidden, row * ldw, row * lds, 8 * ldw, 8 * lds, tokens, part, rows_of,
+                                    done);
+  }
+}
+
+// 32 output channels for all tokens.  The (job, quad of its channels) steps are
+// dealt to the waves, and a wave loads the next step's weights and h into the
+// registers of the current one's as it uses them.  A product has a column for
+// each token of the job, added to the token's sums in the wave's own part of
+// LDS, step after step.  The waves are added at the end.
+constexpr int kDownRows = 2;              // row tiles of 16
+
+__global__ __launch_bounds__(64 * kStreamWaves, 2) void moe_down_kernel(MoeArgs a) {
+  __shared__ Routing r;
+  __shared__ __attribute__((aligned(16))) float sums[kStreamWaves * kMoeMaxTokens * 16 * kDownRows];   // [wave][tokens][32]
+  const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int each = a.tokens * 16 * kDownRows;
+  for (int i = threadIdx.x; i < kStreamWaves * each; i += 64 * kStreamWaves) sums[i] = 0.f;
+  read_routing<64 * kStreamWaves>(r, a);
+  const int row0 = blockIdx.x * 16 * kDownRows;
+  const int quads = (a.inter + 511) >> 9;
+  const int steps = __builtin_amdgcn_readfirstlane(r.jobs) * quads;
+  const uint32_t ldw = (uint32_t)a.inter >> 1, lds = (uint32_t)a.inter >> 4;
+  const uint32_t rows = min(16 * kDownRows, a.hidden - row0);
+  float* mine = sums + wave * each;
+
+  Quad<kW4A16> w[kDownRows];
+  uint4 h[2][4][4];                       // high and low parts, [unit][8 channels]
+  PackedRows next{};
+  const uint8_t* next_h = nullptr;
+  int next_q = 0;
+  auto aim = [&](int i) {                 // at step i, or at nothing past the last one
+    const bool there = i < steps;
+    i = min(i, steps - 1);
+    const int job = i / quads;
+    next_q = i - job * quads;
+    const int e = __builtin_amdgcn_readfirstlane(r.expert[job]);
+    const int count = min(16, __popcll(tokens_of(r, e)) - r.first[job]);
+    const int64_t row = (int64_t)e * a.hidden + row0;
+    next = PackedRows{a.p2 + row * ldw, a.c2 + row * lds, there ? rows * ldw : 0, there ? rows * lds : 0};
+    next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)(r.base[job] + min(r16, count - 1)) * a.ldh * 2 +
+             next_q * 1024 + g * 16;
+  };
+  auto load_scales = [&](int t) { w[t].load_scales(next, (16 * t + r16) * lds, next_q, g, a.inter); };
+  auto load_unit = [&](int u) {
+#pragma unroll
+    for (int t = 0; t < kDownRows; ++t) w[t].load_weights(u, next, (16 * t + r16) * ldw, next_q, g);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[p][u][j] = global_load16(next_h + (p ? a.lo : 0) + u * 256 + j * 64);
+  };
+  if (wave < steps) {
+    aim(wave);
+#pragma unroll
+    for (int t = 0; t < kDownRows; ++t) load_scales(t);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_unit(u);
+    for (int i = wave; i < steps; i += kStreamWaves) {
+      const int job = i / quads;
+      aim(i + kStreamWaves);
+      u32x2 ws[kDownRows];
+      f32x4 acc[kDownRows][2];
+#pragma unroll
+      for (int t = 0; t < kDownRows; ++t) {
+        ws[t] = w[t].scales(g);
+        load_scales(t);
+        acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int t = 0; t < kDownRows; ++t) {
+          float s0, s1;
+          Quad<kW4A16>::codes(ws[t], u, s0, s1);
+          const uint32_t wv[4] = {w[t].w[u].x, w[t].w[u].y, w[t].w[u].z, w[t].w[u].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = fp4x8_bf16(wv[j], j < 2 ? s0 : s1);
+            acc[t][0] = mfma_bf16(v, h[0][u][j], acc[t][0]);
+            acc[t][1] = mfma_bf16(v, h[1][u][j], acc[t][1]);
+          }
         }
+        load_unit(u);
+        __builtin_amdgcn_sched_barrier(0);         // the loads go out here, not where their values are near
+      }
+      const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job];
+      const uint64_t mask = tokens_of(r, e);
+      const int tok = token_of_column(mask, first);
+      if (r16 < min(16, __popcll(mask) - first)) {
+#pragma unroll
+        for (int t = 0; t < kDownRows; ++t)
+          *reinterpret_cast<f32x4*>(mine + (tok * kDownRows + t) * 16 + 4 * g) += acc[t][0] + acc[t][1];
       }
     }
   }
-}
-
-template <bool K32>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeArgs a) {
-  __shared__ Routing r;
-  __shared__ uint8_t tok[kMoeMaxTokens];
-  __shared__ uint16_t slot[kMoeMaxTokens];
-  __shared__ float wt[kMoeMaxTokens];
-  __shared__ int count;
-  __shared__ f32x4 part[kUpWaves * 2 * 2 * 64];
-  read_routing(r, a);
-  const int row0 = blockIdx.x * 16;
-  if ((int)blockIdx.y >= r.count) return;
-  const int e = r.active[blockIdx.y];
-  if (threadIdx.x < 64) {
-    const int t = threadIdx.x;
-    float w = 0.f;
-    const int s = t < a.tokens ? find_choice(r, a, t, e, &w) : -1;
-    const uint64_t mask = __ballot(s >= 0);
-    if (s >= 0) {
-      const int at = __popcll(mask & ((1ull << t) - 1));
-      tok[at] = (uint8_t)t;
-      slot[at] = (uint16_t)(t * a.top_k + s);
-      wt[at] = w;
-    }
-    if (t == 0) count = __popcll(mask);
-  }
   __syncthreads();
-  const int n = count;
-  if (n <= 16) {
-    up_tile<1, K32>(a, e, row0, 0, n, tok, slot, wt, part);
-  } else {
-    for (int first = 0; first < n; first += 32) up_tile<2, K32>(a, e, row0, first, n, tok, slot, wt, part);
+  for (int i = threadIdx.x; i < each; i += 64 * kStreamWaves) {
+    const int t = i / (16 * kDownRows), o = row0 + i % (16 * kDownRows);
+    float v = sums[i];
+#pragma unroll
+    for (int z = 1; z < kStreamWaves; ++z) v += sums[z * each + i];
+    if (o < a.hidden) a.y[t * a.ldy + o] = to_bf16(v);
   }
-}
-
-// 16 output channels for all tokens.  The workgroup's waves share out
-// (expert, channel part) items.  An item's product has a column for every
-// token; each wave adds the columns of the tokens that the expert serves to
-// its own sums, item after item, and drops the rest (so a NaN in an expert's
-// scales reaches its own tokens only).  The waves are added at the end.
-template <int NT, bool K32>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeArgs a) {
-  __shared__ Routing r;
-  __shared__ f32x4 part[kDownWaves][NT][64];
-  read_routing(r, a);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row0 = blockIdx.x * 16;
-  const int units = (a.inter + 127) >> 7;
-  int parts = 1;
-  while (parts < units && r.count * parts < 4 * kDownWaves) parts *= 2;
-  const int per = (units + parts - 1) / parts;
-  const int64_t row = min(row0 + (lane & 15), a.hidden - 1);
-  const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h);
-  f32x4 sum[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) sum[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int i = wave; i < r.count * parts; i += kDownWaves) {
-    const int e = r.active[i / parts], part_i = i % parts;
-    const int s = lane < a.tokens ? find_choice(r, a, lane, e, nullptr) : -1;
-    const uint64_t mask = __ballot(s >= 0);
-    // other tokens' lanes read the first served token's row, whatever comes of it
-    const int any = __shfl(lane * a.top_k + s, __ffsll((unsigned long long)mask) - 1);
-    const int slot = s >= 0 ? lane * a.top_k + s : any;
-    ProductRows<1, NT> p;
-    const int64_t er = (int64_t)e * a.hidden + row;
-    p.wp[0] = a.p2 + er * (a.inter >> 1);
-    p.wc[0] = a.c2 + er * (a.inter >> 4);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      p.xp[n] = h + (int64_t)__shfl(slot, 16 * n + (lane & 15)) * a.inter * 2;
-      p.xc[n] = nullptr;
-    }
-    f32x4 acc[1][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[0][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    product_units<kW4A16, 1, NT, K32, true, 1>(acc, p, min(part_i * per, units), min((part_i + 1) * per, units),
-                                               lane >> 4, a.inter, a.lo);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if ((mask >> (16 * n + (lane & 15))) & 1) sum[n] += acc[0][n];
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) part[wave][n][lane] = sum[n];
-  __syncthreads();
-  for (int i = threadIdx.x; i < NT * 64; i += 64 * kDownWaves) {
-    const int n = i >> 6, l = i & 63;
-    f32x4 v = part[0][n][l];
-#pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) v += part[w][n][l];
-    const int t = 16 * n + (l & 15), o = row0 + 4 * (l >> 4);
-    if (t < a.tokens) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (o + q < a.hidden) a.y[t * a.ldy + o + q] = to_bf16(v[q]);
-    }
-  }
-}
-
-template <bool K32>
-void run_down(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid((a.hidden + 15) / 16);
-  if (a.tokens <= 16) moe_down_kernel<1, K32><<<grid, 64 * kDownWaves, 0, s>>>(a);
-  else if (a.tokens <= 32) moe_down_kernel<2, K32><<<grid, 64 * kDownWaves, 0, s>>>(a);
-  else moe_down_kernel<4, K32><<<grid, 64 * kDownWaves, 0, s>>>(a);
 }
 
 // One wave per token.  Lane l holds the logits of experts l, l + 64, ...;
@@ -305,9 +354,10 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const float* __restrict_
 
 }  // namespace
 
+static int64_t moe_ldh(int64_t inter) { return (inter + 511) / 512 * 512; }
+
 size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
-  const size_t plane = ((size_t)(tokens * top_k) * (size_t)inter * 2 + 255) & ~(size_t)255;
-  return 2 * plane;
+  return 2 * ((size_t)(tokens * top_k) * (size_t)moe_ldh(inter) * 2);
 }
 
 int launch_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
@@ -340,6 +390,7 @@ int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_
   a.y = y;
   a.ldy = ldy;
   a.h = reinterpret_cast<uint16_t*>(workspace);
+  a.ldh = moe_ldh(inter);
   a.lo = (int64_t)(moe_workspace_bytes(tokens, top_k, inter) / 2);
   a.tokens = (int)tokens;
   a.hidden = (int)hidden;
@@ -347,13 +398,15 @@ int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_
   a.experts = (int)experts;
   a.top_k = top_k;
   const int64_t pairs = tokens * top_k;
-  const dim3 grid((unsigned)((inter + 15) / 16), (unsigned)(pairs < experts ? pairs : experts));
-  if (hidden % 32) moe_up_kernel<false><<<grid, 64 * kUpWaves, 0, s>>>(a);
-  else moe_up_kernel<true><<<grid, 64 * kUpWaves, 0, s>>>(a);
+  const int64_t most = pairs < experts ? pairs : experts;        // experts reached, at least one job each
+  const int64_t want = most * (inter / 8);
+  const unsigned grid = (unsigned)(want < kCus ? want : kCus);
+  if (hidden <= 512 * kStreamWaves) moe_up_kernel<1><<<grid, 64 * kStreamWaves, 0, s>>>(a);
+  else moe_up_kernel<2><<<grid, 64 * kStreamWaves, 0, s>>>(a);
   const int st = launch_status("moe_up_kernel");
   if (st) return st;
-  if (inter % 32) run_down<false>(a, s);
-  else run_down<true>(a, s);
+  const unsigned rows = (unsigned)((hidden + 16 * kDownRows - 1) / (16 * kDownRows));
+  moe_down_kernel<<<rows, 64 * kStreamWaves, 0, s>>>(a);
   return launch_status("moe_down_kernel");
 }
 
