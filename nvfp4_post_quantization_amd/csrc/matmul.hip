@@ -3,12 +3,9 @@
 // W4A4 tiers) and for MXFP4 on both sides.
 //
 // Few tokens: the weights are read once and bound the call.  A workgroup
-// takes a run of 16-row tiles, as many workgroups as there are CUs; its eight
-// waves split the channels, hold their part of the tokens in registers and
-// stream the rows' packed weights past them from HBM, expanding them in
-// registers for the matrix cores (the rows are the instruction's M side, the
-// tokens its N side).  The waves' partial tiles meet in LDS and are added in
-// wave order.
+// takes a run of row tiles; its waves split the channels, hold their part of
+// the tokens in registers and stream the rows' packed weights past them from
+// HBM.  The waves' partial sums meet in LDS and are added in wave order.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -36,64 +33,140 @@ __device__ __forceinline__ float tensor_scaled(float v, const ProductArgs& a) {
   else return v;
 }
 
-template <int KIND, int NT, int QW>
-__global__ __launch_bounds__(64 * kStreamWaves, 2) void few_tokens_kernel(ProductArgs a) {
-  constexpr int RT = 2 / QW, TB = 4 / RT / NT;
-  __shared__ f32x4 part[kStreamWaves * TB * RT * NT * 64];
-  const int lane = threadIdx.x & 63, r16 = lane & 15;
-  const int tiles = (a.out + 15) >> 4;
-  const int begin = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
-  const int end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+constexpr int kCus = 256;
+
+// Workgroups: enough to give every CU its waves.
+unsigned few_grid(int tiles, int waves, int cu_waves) {
+  const int most = kCus * (cu_waves / waves);
+  return (unsigned)(tiles < most ? tiles : most);
+}
+
+__device__ __forceinline__ void tile_run(int tiles, int& begin, int& end) {
+  begin = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+  end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+}
+
+template <int KIND>
+__device__ __forceinline__ void store_rows(const ProductArgs& a, int row, int tok, f32x4 v) {
+  uint16_t* dst = a.y + (int64_t)tok * a.ldy + row;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (row + e < a.out) dst[e] = to_bf16(tensor_scaled<KIND>(v[e], a));
+}
+
+// 4 NG tokens (the y coordinate's) against NVFP4 rows.  CU: waves that share a
+// CU, MW: waves of a workgroup, both at most.
+template <int KIND, bool ODD, int NG, int QW, int RT, int CU, int MW>
+__global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a) {
+  constexpr int TB = 4;
+  __shared__ f32x4 part[MW * TB * NG * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[KIND == kW4A16 ? MW * 4096 : 16];
+  const int lane = threadIdx.x & 63, j = lane & 3;
+  const int wave = threadIdx.x >> 6;
+  const int tok0 = blockIdx.y * 4 * NG;
+  const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 4;
+  int begin, end;
+  tile_run((a.out + 15) >> 4, begin, end);
+  const uint32_t group_row[4] = {0, 4, 8, 12};
+  Chunk x[QW][1][NG];
+  auto rows_of = [&](int t) {
+    const int row = t * 16;
+    const uint32_t rows = min(min(16 * RT, (end - t) * 16), a.out - row);
+    return PackedRows{a.wp + (int64_t)row * ldw, a.wc + (int64_t)row * lds, rows * ldw, rows * lds};
+  };
+  auto load_tokens = [&](int q) {
+#pragma unroll
+    for (int z = 0; z < QW; ++z)
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const int t0 = min(tok0 + 4 * n, a.tokens - 1), t = min(j, a.tokens - 1 - t0);      // others are not stored
+        if constexpr (KIND == kW4A16) {
+          load_pieces(x[z][0][n], a.xp + (int64_t)(t0 + t) * a.ldx, q + z, a.k);
+        } else {
+          const uint32_t rows = (q + z) * 512 < a.k ? min(4, a.tokens - t0) : 0;
+          load_chunk<ODD>(x[z][0][n], PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds}, t,
+                     q + z, a.k);
+        }
+      }
+    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
+    if constexpr (KIND == kW4A16) {
+#pragma unroll
+      for (int z = 0; z < QW; ++z)
+#pragma unroll
+        for (int n = 0; n < NG; ++n) pieces_to_chunk(x[z][0][n], stage + wave * 4096);
+    }
+  };
+  auto done = [&](int t, int n, int q, int tj, f32x4 v) {
+    const int row = t * 16 + q * 4, tok = tok0 + 4 * n + tj;
+    if (tok < a.tokens && row < a.out) store_rows<KIND>(a, row, tok, v);
+  };
+  stream_rows<ODD, NG, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), 16, group_row, x, part, rows_of, load_tokens, done);
+}
+
+// 16 NT tokens against MXFP4 rows.
+template <int NT, int QW, int RT, int CU, int MW>
+__global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductArgs a) {
+  constexpr int TB = 4 / NT;
+  __shared__ f32x4 part[MW * TB * NT * 64];
+  const int r16 = threadIdx.x & 15;
   const int tok0 = blockIdx.y * 16 * NT;
-  const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> (KIND == kMX ? 5 : 4);
-  TokenRows tokens[NT];
+  const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 5;
+  int begin, end;
+  tile_run((a.out + 15) >> 4, begin, end);
+  PackedRows tokens[NT];
+  uint32_t token_row[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int t0 = min(tok0 + 16 * n, a.tokens - 1);             // tokens past the end are not stored
-    const int t = min(r16, a.tokens - 1 - t0);
-    if constexpr (KIND == kW4A16) {
-      tokens[n].x = a.xp + (int64_t)(t0 + t) * a.ldx;
-    } else {
-      const uint32_t rows = min(16, a.tokens - t0);
-      tokens[n].packed = PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds};
-      tokens[n].row_w = t * ldw;
-      tokens[n].row_s = t * lds;
-    }
+    const int t0 = min(tok0 + 16 * n, a.tokens - 1);
+    const uint32_t rows = min(16, a.tokens - t0);
+    tokens[n] = PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds};
+    token_row[n] = min(r16, a.tokens - 1 - t0);                                  // others are not stored
   }
   auto rows_of = [&](int t) {
     const int row = t * 16;
     const uint32_t rows = min(min(16 * RT, (end - t) * 16), a.out - row);
     return PackedRows{a.wp + (int64_t)row * ldw, a.wc + (int64_t)row * lds, rows * ldw, rows * lds};
   };
-  auto done = [&](int t, int n, int l, auto sum) {
+  auto done = [&](int t, int n, int l, f32x4 v) {
     const int row = t * 16 + 4 * (l >> 4), tok = tok0 + 16 * n + (l & 15);
-    if (tok >= a.tokens || row >= a.out) return;
-    const f32x4 v = sum(l);
-    uint16_t* dst = a.y + (int64_t)tok * a.ldy + row;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (row + e < a.out) dst[e] = to_bf16(tensor_scaled<KIND>(v[e], a));
+    if (tok < a.tokens && row < a.out) store_rows<kMX>(a, row, tok, v);
   };
-  stream_tiles<KIND, NT, QW, TB>(begin, end, a.k, r16 * ldw, r16 * lds, 16 * ldw, 16 * lds, tokens, part, rows_of, done);
+  stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, part, rows_of, done);
 }
 
-constexpr int kCus = 256;
-
-template <int KIND, int NT, int QW>
+template <int KIND, bool ODD, int NG, int QW, int RT, int CU>
 int run_few(const ProductArgs& a, hipStream_t s) {
-  const int tiles = (a.out + 15) / 16;
-  const dim3 grid(tiles < kCus ? tiles : kCus, (a.tokens + 16 * NT - 1) / (16 * NT));
-  few_tokens_kernel<KIND, NT, QW><<<grid, 64 * kStreamWaves, 0, s>>>(a);
+  const int waves = quad_plan<QW>(a.k, CU).waves;
+  const dim3 grid(few_grid((a.out + 15) / 16, waves, CU), (a.tokens + 4 * NG - 1) / (4 * NG));
+  if (waves <= 4) few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, 4><<<grid, 64 * waves, 0, s>>>(a);
+  else if (CU == 8 || waves <= 8) few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, 8><<<grid, 64 * waves, 0, s>>>(a);
+  else few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, CU><<<grid, 64 * waves, 0, s>>>(a);
   return launch_status("few_tokens_kernel");
 }
 
-// One quad of the tokens a wave and two row tiles at a time where that covers
-// the channels, else two quads and one row tile.
+template <int NT, int QW, int RT, int CU>
+int run_few_mx(const ProductArgs& a, hipStream_t s) {
+  const int waves = quad_plan<QW>(a.k, CU).waves;
+  const dim3 grid(few_grid((a.out + 15) / 16, waves, CU), (a.tokens + 16 * NT - 1) / (16 * NT));
+  if (waves <= 4) few_mx_tokens_kernel<NT, QW, RT, CU, 4><<<grid, 64 * waves, 0, s>>>(a);
+  else if (CU == 8 || waves <= 8) few_mx_tokens_kernel<NT, QW, RT, CU, 8><<<grid, 64 * waves, 0, s>>>(a);
+  else few_mx_tokens_kernel<NT, QW, RT, CU, CU><<<grid, 64 * waves, 0, s>>>(a);
+  return launch_status("few_mx_tokens_kernel");
+}
+
 template <int KIND>
 int run(const ProductArgs& a, hipStream_t s) {
-  const bool one = a.k <= 512 * kStreamWaves;
-  if (a.tokens <= 16) return one ? run_few<KIND, 1, 1>(a, s) : run_few<KIND, 1, 2>(a, s);
-  return run_few<KIND, 2, 1>(a, s);
+  if constexpr (KIND == kMX) {
+    const bool narrow = a.k <= 4096;
+    if (a.tokens <= 16) return narrow ? run_few_mx<1, 1, 2, 8>(a, s) : run_few_mx<1, 2, 1, 12>(a, s);
+    return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
+  } else {
+    const bool narrow = a.k <= 8192;
+    if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 1, 1, 16>(a, s) : run_few<KIND, true, 4, 1, 2, 8>(a, s);
+    if (a.tokens <= 4) return narrow ? run_few<KIND, false, 1, 1, 1, 16>(a, s) : run_few<KIND, false, 1, 2, 1, 16>(a, s);
+    if (a.tokens <= 8) return narrow ? run_few<KIND, false, 2, 1, 1, 16>(a, s) : run_few<KIND, false, 2, 2, 1, 12>(a, s);
+    return run_few<KIND, false, 4, 1, 2, 8>(a, s);
+  }
 }
 
 }  // namespace

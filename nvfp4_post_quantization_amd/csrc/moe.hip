@@ -37,7 +37,7 @@ struct MoeArgs {
   int tokens, hidden, inter, experts, top_k;
 };
 
-// A job is a chosen expert with up to 16 of its tokens.
+// A job is a chosen expert with up to JOB of its tokens.
 struct Routing {
   uint32_t mask[kMoeMaxExperts][2];       // tokens of an expert
   uint16_t expert[kMaxJobs];              // by job: its expert, experts in ascending order,
@@ -51,28 +51,27 @@ __device__ __forceinline__ uint64_t tokens_of(const Routing& r, int e) {
   return (uint64_t)r.mask[e][1] << 32 | r.mask[e][0];
 }
 
-// Fill r from the ids (all threads, THREADS of them; syncs).
-template <int THREADS>
+// Fill r from the ids (all threads, a whole number of waves; syncs).
+template <int JOB>
 __device__ __forceinline__ void read_routing(Routing& r, const MoeArgs& a) {
-  constexpr int PER = kMoeMaxExperts / THREADS;
+  const int threads = blockDim.x, per = (kMoeMaxExperts + threads - 1) / threads;
   const int n = a.tokens * a.top_k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < 2 * a.experts; i += THREADS) (&r.mask[0][0])[i] = 0;
+  for (int i = tid; i < 2 * a.experts; i += threads) (&r.mask[0][0])[i] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += THREADS) {
+  for (int i = tid; i < n; i += threads) {
     const int e = a.ids[i], t = i / a.top_k;
     if (e >= 0 && e < a.experts) atomicOr(&r.mask[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
-  // prefix sums over the experts, PER of them a thread: jobs in the lower half
+  // prefix sums over the experts, `per` of them a thread: jobs in the lower half
   // of the word, pairs (at most 1024) in the upper
-  uint32_t own[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
+  auto own = [&](int i) {
+    const int e = tid * per + i;
     const uint32_t c = e < a.experts ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0;
-    own[i] = (c + 15) >> 4 | c << 16;
-    sum += own[i];
-  }
+    return (c + JOB - 1) / JOB | c << 16;
+  };
+  uint32_t sum = 0;
+  for (int i = 0; i < per; ++i) sum += own(i);
   uint32_t scan = sum;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
@@ -83,28 +82,27 @@ __device__ __forceinline__ void read_routing(Routing& r, const MoeArgs& a) {
   __syncthreads();
   uint32_t before = scan - sum;
   uint32_t all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
+  for (int w = 0; w < threads / 64; ++w) {
     if (w < wave) before += r.part[w];
     all += r.part[w];
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    for (int q = 0; q < (int)(own[i] & 0xFFFF); ++q) {
+  for (int i = 0; i < per; ++i) {
+    const uint32_t mine = own(i);
+    for (int q = 0; q < (int)(mine & 0xFFFF); ++q) {
       const int job = (before & 0xFFFF) + q;
-      r.expert[job] = (uint16_t)(tid * PER + i);
-      r.base[job] = (uint16_t)((before >> 16) + 16 * q);
-      r.first[job] = (uint8_t)(16 * q);
+      r.expert[job] = (uint16_t)(tid * per + i);
+      r.base[job] = (uint16_t)((before >> 16) + JOB * q);
+      r.first[job] = (uint8_t)(JOB * q);
     }
-    before += own[i];
+    before += mine;
   }
   if (tid == 0) r.jobs = (int)(all & 0xFFFF);
   __syncthreads();
 }
 
-// The place-th set bit of a nonzero mask, for place = first + lane % 16 (the
-// last one for places beyond).
-__device__ __forceinline__ int token_of_column(uint64_t mask, int first) {
+// The place-th set bit of a nonzero mask (the last one for places beyond); all
+// lanes take part.
+__device__ __forceinline__ int token_of_place(uint64_t mask, int place) {
   const int lane = threadIdx.x & 63;
   const int n = __popcll(mask);
   const int rank = __popcll(mask & ((1ull << lane) - 1));
@@ -112,7 +110,7 @@ __device__ __forceinline__ int token_of_column(uint64_t mask, int first) {
   // their own past the set bits
   const int to = (mask >> lane) & 1 ? rank : n + lane - rank;
   const int t = __builtin_amdgcn_ds_permute(to * 4, lane);
-  return __shfl(t, min(first + (lane & 15), n - 1));
+  return __shfl(t, min(place, n - 1));
 }
 
 // What a token gives an expert (all places that name it).
@@ -123,101 +121,131 @@ __device__ __forceinline__ float weight_of(const MoeArgs& a, int t, int e) {
   return w;
 }
 
-// Where channel c of a row of h is kept: within each unit of 128 channels in
-// the order in which the second launch's lanes read them, piece j (8 channels)
-// of the four chunks of 32 next to each other.
+// Where channel c of a row of h is kept: within each quad (512 channels) in the
+// order in which the second launch's lanes read them, piece m (8 channels) of
+// the 16 chunks of 32 next to each other.
 __device__ __forceinline__ int place_of(int c) {
-  return (c & ~127) | ((c >> 3) & 3) << 5 | ((c >> 5) & 3) << 3 | (c & 7);
+  return (c & ~511) | ((c >> 3) & 3) << 7 | ((c >> 5) & 15) << 3 | (c & 7);
 }
 
-// h of a run of (job, 8 channels) tiles, as many runs as there are workgroups.
-// A row tile holds the gate rows of the channels in rows 0-7 and their up rows
-// in 8-15, so that one pass over the tokens serves both.
-template <int QW>
-__global__ __launch_bounds__(64 * kStreamWaves, 2) void moe_up_kernel(MoeArgs a) {
-  constexpr int RT = 2 / QW, TB = 4 / RT;
+// h of 4 NG tokens (tok: the lane's of each four) of a job, for row tiles
+// t0 .. t1 - 1.  A tile's first two row groups are the gate rows of 8 channels,
+// the others their up rows, so that one pass over the tokens serves both.
+template <bool ODD, int NG>
+__device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, int e, int base, int count, int first_tok,
+                                        uint64_t mask, int t0, int t1, const float* wt, f32x4* part, uint8_t* stage) {
+  constexpr int CH = 8;                              // channels of a tile
+  const int wave = threadIdx.x >> 6, j = threadIdx.x & 3;
+  const uint32_t ldw = (uint32_t)a.hidden >> 1, lds = (uint32_t)a.hidden >> 4;
+  const uint8_t* w = a.p13 + (int64_t)e * 2 * a.inter * ldw;
+  const uint8_t* c = a.c13 + (int64_t)e * 2 * a.inter * lds;
+  const float s13 = a.s13[e];
+  const uint32_t group_row[4] = {0, 4, (uint32_t)a.inter, (uint32_t)a.inter + 4};
+  Chunk x[1][1][NG];
+  auto rows_of = [&](int t) {
+    const uint32_t rows = a.inter + CH;              // to the end of the tile's up rows
+    return PackedRows{w + (int64_t)t * CH * ldw, c + (int64_t)t * CH * lds, rows * ldw, rows * lds};
+  };
+  auto load_tokens = [&](int q) {
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const int tok = token_of_place(mask, first_tok + min(4 * n + j, count - 1));
+      load_pieces(x[0][0][n], a.x + tok * a.ldx, q, a.hidden);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
+#pragma unroll
+    for (int n = 0; n < NG; ++n) pieces_to_chunk(x[0][0][n], stage + wave * 4096);
+  };
+  // done is called for the up rows by the lanes 8 after those of the gate rows
+  auto done = [&](int t, int n, int q, int tj, f32x4 v) {
+    f32x4 up;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) up[z] = __shfl_down(v[z], 8);
+    const int col = 4 * n + tj;
+    if (q >= 2 || col >= count) return;
+    const float scale = wt[col];
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const float gate = v[z] * s13;
+      const float h = gate / (1.0f + expf(-gate)) * (up[z] * s13) * scale;
+      hi[z] = to_bf16(h);                            // two bf16 parts keep 16 significant bits of h
+      lo[z] = to_bf16(h - bf16_to_f32(hi[z]));
+    }
+    uint16_t* row_h = a.h + (int64_t)(base + col) * a.ldh;
+    auto put = [&](int ch, uint2 high, uint2 low) {
+      uint8_t* dst = reinterpret_cast<uint8_t*>(row_h + place_of(ch));
+      *reinterpret_cast<uint2*>(dst) = high;
+      *reinterpret_cast<uint2*>(dst + a.lo) = low;
+    };
+    put(t * CH + 4 * q, make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
+        make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
+    if ((t + 1) * CH == a.inter && q == 0)           // the rest of the row's last quad
+      for (int ch = a.inter; ch < a.ldh; ch += 4) put(ch, make_uint2(0, 0), make_uint2(0, 0));
+  };
+  stream_rows<ODD, NG, 1, 1, 4>(t0, t1, a.hidden, plan, CH, group_row, x, part, rows_of, load_tokens, done);
+}
+
+// h of a run of (job, 8 channels) pieces of work, as many runs as there are
+// workgroups.
+template <bool ODD, int MW>
+__global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
   __shared__ Routing r;
-  __shared__ f32x4 part[kStreamWaves * TB * RT * 64];
-  __shared__ float wt[16];
-  read_routing<64 * kStreamWaves>(r, a);
-  const int lane = threadIdx.x & 63, r16 = lane & 15;
+  __shared__ f32x4 part[MW * 4 * 2 * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[MW * 4096];
+  __shared__ float wt[8];
+  read_routing<8>(r, a);
+  const int lane = threadIdx.x & 63;
+  const QuadPlan plan = quad_plan<1>(a.hidden, kCuWaves);
   const int tiles = a.inter >> 3;
   const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(r.jobs) * tiles;
-  int64_t begin = total * blockIdx.x / gridDim.x;
-  const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
-  const uint32_t ldw = (uint32_t)a.hidden >> 1, lds = (uint32_t)a.hidden >> 4;
-  const uint32_t row = (r16 >> 3) * (uint32_t)a.inter + (r16 & 7);
-  while (begin < end) {                              // one job after another
-    const int job = __builtin_amdgcn_readfirstlane((int)(begin / tiles));
-    const int t0 = __builtin_amdgcn_readfirstlane((int)(begin - (int64_t)job * tiles));
-    const int t1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)tiles, t0 + end - begin));
-    begin += t1 - t0;
-    const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job], base = r.base[job];
+  const int64_t begin = total * blockIdx.x / gridDim.x;
+  int left = __builtin_amdgcn_readfirstlane((int)(total * (blockIdx.x + 1) / gridDim.x - begin));
+  int job = __builtin_amdgcn_readfirstlane((int)(begin / tiles));
+  int t0 = __builtin_amdgcn_readfirstlane((int)(begin - (int64_t)job * tiles));
+  for (; left > 0; ++job, t0 = 0) {                  // one job after another
+    const int t1 = min(tiles, t0 + left);
+    left -= t1 - t0;
+    const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), base = __builtin_amdgcn_readfirstlane(r.base[job]);
+    const int first = __builtin_amdgcn_readfirstlane(r.first[job]);
     const uint64_t mask = tokens_of(r, e);
-    const int count = min(16, __popcll(mask) - first);
-    const int tok = token_of_column(mask, first);
-    if (threadIdx.x < 16) wt[threadIdx.x] = weight_of(a, tok, e) * a.s2[e];
-    const float s13 = a.s13[e];
-    const uint8_t* w = a.p13 + (int64_t)e * 2 * a.inter * ldw;
-    const uint8_t* c = a.c13 + (int64_t)e * 2 * a.inter * lds;
-    TokenRows tokens[1];
-    tokens[0].x = a.x + tok * a.ldx;
-    auto rows_of = [&](int t) {
-      const uint32_t rows = a.inter + min(8 * RT, (t1 - t) * 8);      // to the end of the step's up rows
-      return PackedRows{w + (int64_t)t * 8 * ldw, c + (int64_t)t * 8 * lds, rows * ldw, rows * lds};
-    };
-    auto done = [&](int t, int, int l, auto sum) {
-      if (l >= 32 || (l & 15) >= count) return;
-      const f32x4 gate = sum(l), up = sum(l + 32);
-      const float scale = wt[l & 15];
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v = gate[q] * s13;
-        const float h = v / (1.0f + expf(-v)) * (up[q] * s13) * scale;
-        hi[q] = to_bf16(h);                          // two bf16 parts keep 16 significant bits of h
-        lo[q] = to_bf16(h - bf16_to_f32(hi[q]));
-      }
-      uint16_t* row_h = a.h + (int64_t)(base + (l & 15)) * a.ldh;
-      auto put = [&](int c, uint2 high, uint2 low) {
-        uint8_t* dst = reinterpret_cast<uint8_t*>(row_h + place_of(c));
-        *reinterpret_cast<uint2*>(dst) = high;
-        *reinterpret_cast<uint2*>(dst + a.lo) = low;
-      };
-      put(t * 8 + 4 * (l >> 4), make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
-          make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
-      if (t == tiles - 1)                            // the rest of the row's last quad
-        for (int c = a.inter + 4 * (l >> 4); c < a.ldh; c += 8) put(c, make_uint2(0, 0), make_uint2(0, 0));
-    };
-    stream_tiles<kW4A16, 1, QW, TB>(t0, t1, a.hidden, row * ldw, row * lds, 8 * ldw, 8 * lds, tokens, part, rows_of,
-                                    done);
+    const int count = __builtin_amdgcn_readfirstlane(min(8, __popcll(mask) - first));
+    if (threadIdx.x < 64) {                          // (what reads wt comes after a barrier)
+      const int tok = token_of_place(mask, first + lane);
+      if (lane < 8) wt[lane] = weight_of(a, tok, e) * a.s2[e];
+    }
+    if (count <= 4) up_rows<ODD, 1>(a, plan, e, base, count, first, mask, t0, t1, wt, part, stage);
+    else up_rows<ODD, 2>(a, plan, e, base, count, first, mask, t0, t1, wt, part, stage);
   }
 }
 
-// 32 output channels for all tokens.  The (job, quad of its channels) steps are
-// dealt to the waves, and a wave loads the next step's weights and h into the
-// registers of the current one's as it uses them.  A product has a column for
-// each token of the job, added to the token's sums in the wave's own part of
-// LDS, step after step.  The waves are added at the end.
-constexpr int kDownRows = 2;              // row tiles of 16
+// 32 output channels for all tokens.  The (job, quad of its channels) steps, a
+// job being up to four tokens of an expert, are dealt to the waves, and a wave
+// loads the next step's weights and h as it uses the current one's.  A product
+// has a column for each token of the job, added to the token's sums in the
+// wave's own part of LDS, step after step.  The waves are added at the end.
+constexpr int kDownGroups = 8;            // row groups of 4
+constexpr int kDownWaves = 8;
 
-__global__ __launch_bounds__(64 * kStreamWaves, 2) void moe_down_kernel(MoeArgs a) {
+template <bool ODD>
+__global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a) {
+  constexpr int ROWS = 4 * kDownGroups;
   __shared__ Routing r;
-  __shared__ __attribute__((aligned(16))) float sums[kStreamWaves * kMoeMaxTokens * 16 * kDownRows];   // [wave][tokens][32]
-  const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+  __shared__ __attribute__((aligned(16))) float sums[kDownWaves * kMoeMaxTokens * ROWS];   // [wave][tokens][32]
+  const int lane = threadIdx.x & 63, b = lane >> 2, j = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int each = a.tokens * 16 * kDownRows;
-  for (int i = threadIdx.x; i < kStreamWaves * each; i += 64 * kStreamWaves) sums[i] = 0.f;
-  read_routing<64 * kStreamWaves>(r, a);
-  const int row0 = blockIdx.x * 16 * kDownRows;
+  const int each = a.tokens * ROWS;
+  for (int i = threadIdx.x; i < kDownWaves * each; i += 64 * kDownWaves) sums[i] = 0.f;
+  read_routing<4>(r, a);
+  const int row0 = blockIdx.x * ROWS;
   const int quads = (a.inter + 511) >> 9;
   const int steps = __builtin_amdgcn_readfirstlane(r.jobs) * quads;
   const uint32_t ldw = (uint32_t)a.inter >> 1, lds = (uint32_t)a.inter >> 4;
-  const uint32_t rows = min(16 * kDownRows, a.hidden - row0);
+  const uint32_t rows = min(ROWS, a.hidden - row0);
   float* mine = sums + wave * each;
 
-  Quad<kW4A16> w[kDownRows];
-  uint4 h[2][4][4];                       // high and low parts, [unit][8 channels]
+  RowGroup w[kDownGroups];
+  Chunk h[2][1], h_next[2][1];            // high and low parts
   PackedRows next{};
   const uint8_t* next_h = nullptr;
   int next_q = 0;
@@ -227,73 +255,73 @@ __global__ __launch_bounds__(64 * kStreamWaves, 2) void moe_down_kernel(MoeArgs 
     const int job = i / quads;
     next_q = i - job * quads;
     const int e = __builtin_amdgcn_readfirstlane(r.expert[job]);
-    const int count = min(16, __popcll(tokens_of(r, e)) - r.first[job]);
+    const int count = min(4, __popcll(tokens_of(r, e)) - r.first[job]);
     const int64_t row = (int64_t)e * a.hidden + row0;
-    next = PackedRows{a.p2 + row * ldw, a.c2 + row * lds, there ? rows * ldw : 0, there ? rows * lds : 0};
-    next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)(r.base[job] + min(r16, count - 1)) * a.ldh * 2 +
-             next_q * 1024 + g * 16;
+    next = uniform(PackedRows{a.p2 + row * ldw, a.c2 + row * lds, there ? rows * ldw : 0, there ? rows * lds : 0});
+    next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)(r.base[job] + min(j, count - 1)) * a.ldh * 2 +
+             next_q * 1024 + b * 16;
   };
-  auto load_scales = [&](int t) { w[t].load_scales(next, (16 * t + r16) * lds, next_q, g, a.inter); };
-  auto load_unit = [&](int u) {
-#pragma unroll
-    for (int t = 0; t < kDownRows; ++t) w[t].load_weights(u, next, (16 * t + r16) * ldw, next_q, g);
+  auto load_h = [&](Chunk (&d)[2][1]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[p][u][j] = global_load16(next_h + (p ? a.lo : 0) + u * 256 + j * 64);
+      for (int m = 0; m < 4; ++m) {
+        const uint4 v = global_load16(next_h + (p ? a.lo : 0) + m * 256);
+        d[p][0][4 * m] = v.x;
+        d[p][0][4 * m + 1] = v.y;
+        d[p][0][4 * m + 2] = v.z;
+        d[p][0][4 * m + 3] = v.w;
+      }
+  };
+  auto load_w = [&](int q) { w[q].load(next, 4 * q, next_q, LaneAt<ODD>(j, next_q, b, a.inter), a.inter); };
+  auto step = [&](int i, const Chunk (&x)[2][1], Chunk (&x_next)[2][1]) {
+    const int job = i / quads;
+    aim(i + kDownWaves);
+    load_h(x_next);
+    f32x4 acc[kDownGroups][1];
+#pragma unroll
+    for (int q = 0; q < kDownGroups; ++q) {
+      acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+      multiply_group<1, 2>(w[q], x, acc[q]);
+      load_w(q);
+      __builtin_amdgcn_sched_barrier(0);             // the load goes out here, not where its value is near
+    }
+    const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job];
+    const uint64_t mask = tokens_of(r, e);
+    const int tok = token_of_place(mask, first + j);
+    const f32x4 v0 = sum_chunks_rest(sum_chunks_pair(acc[0][0], acc[2][0]), sum_chunks_pair(acc[1][0], acc[3][0]));
+    const f32x4 v1 = sum_chunks_rest(sum_chunks_pair(acc[4][0], acc[6][0]), sum_chunks_pair(acc[5][0], acc[7][0]));
+    if ((lane & 12) == 0 && j < __popcll(mask) - first) {
+      f32x4* dst = reinterpret_cast<f32x4*>(mine + tok * ROWS + 4 * (lane >> 4));
+      dst[0] += v0;
+      dst[4] += v1;
+    }
   };
   if (wave < steps) {
     aim(wave);
+    load_h(h);
 #pragma unroll
-    for (int t = 0; t < kDownRows; ++t) load_scales(t);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) load_unit(u);
-    for (int i = wave; i < steps; i += kStreamWaves) {
-      const int job = i / quads;
-      aim(i + kStreamWaves);
-      u32x2 ws[kDownRows];
-      f32x4 acc[kDownRows][2];
-#pragma unroll
-      for (int t = 0; t < kDownRows; ++t) {
-        ws[t] = w[t].scales(g);
-        load_scales(t);
-        acc[t][0] = acc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-#pragma unroll
-        for (int t = 0; t < kDownRows; ++t) {
-          float s0, s1;
-          Quad<kW4A16>::codes(ws[t], u, s0, s1);
-          const uint32_t wv[4] = {w[t].w[u].x, w[t].w[u].y, w[t].w[u].z, w[t].w[u].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 v = fp4x8_bf16(wv[j], j < 2 ? s0 : s1);
-            acc[t][0] = mfma_bf16(v, h[0][u][j], acc[t][0]);
-            acc[t][1] = mfma_bf16(v, h[1][u][j], acc[t][1]);
-          }
-        }
-        load_unit(u);
-        __builtin_amdgcn_sched_barrier(0);         // the loads go out here, not where their values are near
-      }
-      const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job];
-      const uint64_t mask = tokens_of(r, e);
-      const int tok = token_of_column(mask, first);
-      if (r16 < min(16, __popcll(mask) - first)) {
-#pragma unroll
-        for (int t = 0; t < kDownRows; ++t)
-          *reinterpret_cast<f32x4*>(mine + (tok * kDownRows + t) * 16 + 4 * g) += acc[t][0] + acc[t][1];
-      }
+    for (int q = 0; q < kDownGroups; ++q) load_w(q);
+    for (int i = wave; i < steps; i += 2 * kDownWaves) {
+      step(i, h, h_next);
+      if (i + kDownWaves < steps) step(i + kDownWaves, h_next, h);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < each; i += 64 * kStreamWaves) {
-    const int t = i / (16 * kDownRows), o = row0 + i % (16 * kDownRows);
+  for (int i = threadIdx.x; i < each; i += 64 * kDownWaves) {
+    const int t = i / ROWS, o = row0 + i % ROWS;
     float v = sums[i];
 #pragma unroll
-    for (int z = 1; z < kStreamWaves; ++z) v += sums[z * each + i];
+    for (int z = 1; z < kDownWaves; ++z) v += sums[z * each + i];
     if (o < a.hidden) a.y[t * a.ldy + o] = to_bf16(v);
   }
+}
+
+template <bool ODD>
+void launch_up(const MoeArgs& a, unsigned grid, int waves, hipStream_t s) {
+  if (waves <= 4) moe_up_kernel<ODD, 4><<<grid, 64 * waves, 0, s>>>(a);
+  else if (waves <= 8) moe_up_kernel<ODD, 8><<<grid, 64 * waves, 0, s>>>(a);
+  else moe_up_kernel<ODD, 16><<<grid, 64 * waves, 0, s>>>(a);
 }
 
 // One wave per token.  Lane l holds the logits of experts l, l + 64, ...;
@@ -399,14 +427,16 @@ int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_
   a.top_k = top_k;
   const int64_t pairs = tokens * top_k;
   const int64_t most = pairs < experts ? pairs : experts;        // experts reached, at least one job each
-  const int64_t want = most * (inter / 8);
-  const unsigned grid = (unsigned)(want < kCus ? want : kCus);
-  if (hidden <= 512 * kStreamWaves) moe_up_kernel<1><<<grid, 64 * kStreamWaves, 0, s>>>(a);
-  else moe_up_kernel<2><<<grid, 64 * kStreamWaves, 0, s>>>(a);
+  const int waves = quad_plan<1>(hidden, kCuWaves).waves;
+  const int64_t want = most * (inter / 8), all = kCus * (kCuWaves / waves);
+  const unsigned grid = (unsigned)(want < all ? want : all);
+  if (hidden % 32 == 0) launch_up<false>(a, grid, waves, s);
+  else launch_up<true>(a, grid, waves, s);
   const int st = launch_status("moe_up_kernel");
   if (st) return st;
-  const unsigned rows = (unsigned)((hidden + 16 * kDownRows - 1) / (16 * kDownRows));
-  moe_down_kernel<<<rows, 64 * kStreamWaves, 0, s>>>(a);
+  const unsigned rows = (unsigned)((hidden + 4 * kDownGroups - 1) / (4 * kDownGroups));
+  if (inter % 32 == 0) moe_down_kernel<false><<<rows, 64 * kDownWaves, 0, s>>>(a);
+  else moe_down_kernel<true><<<rows, 64 * kDownWaves, 0, s>>>(a);
   return launch_status("moe_down_kernel");
 }
 

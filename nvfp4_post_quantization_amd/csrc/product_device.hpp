@@ -13,6 +13,8 @@
 // result, so an operand is never rounded and the products are exact; what
 // rounds is the fp32 accumulation and the final conversion.
 #pragma once
+#include <type_traits>
+
 #include "nvfp4_device.hpp"
 
 namespace nvfp4 {
@@ -76,21 +78,18 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
 
 // ---- a few tokens against many rows -----------------------------------------
 //
-// A unit is 128 channels, a quad four units.  Lane l of a wave works on row
-// (token) l % 16 of a tile and, as group g = l / 16, on chunk g of 32
-// consecutive channels of a unit.  A matrix instruction sums over the groups,
-// so the order of channels within a unit does not matter as long as both
-// operands share it, and a lane's weights of a unit are one 16-byte load.
-//
-// Loads return in order: a wait for one is a wait for all before it.  So the
-// tokens stay in registers (QW quads of them a wave) while the rows go by, and
-// the loop loads nothing but weights: 8 units of them are always on their way,
-// each loaded again as soon as it has been used.
+// The weights are read once and everything else is small, so what matters is
+// that loads are in flight all the time.  Loads return in order: a wait for one
+// is a wait for all before it.  So the tokens stay in registers, a quad (512
+// channels) of them a wave, while the rows go by, and the loop loads nothing
+// but weights and their scales, each register again as soon as it has been
+// used.  One wave issues a vector instruction every 8 cycles, four waves of a
+// SIMD one every 3 to 5 between them, so up to 16 waves share a CU.
 
-constexpr int kStreamWaves = 8;
+constexpr int kCuWaves = 16;
 constexpr uint32_t kBeyond = 0x80000000u;           // past any buffer (they are below 2^31 bytes): reads as zero
 
-// Eight waves meet; what they wrote to LDS is seen.  Loads stay in flight.
+// A workgroup's waves meet; what they wrote to LDS is seen.  Loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -102,27 +101,6 @@ __device__ __forceinline__ void lds_barrier() {
 __device__ __forceinline__ uint4 global_load16(const uint8_t* p) {
   typedef const __attribute__((address_space(1))) ntu32x4* ptr;
   return __builtin_bit_cast(uint4, *(ptr)(uintptr_t)p);
-}
-
-// Exchanges between the groups.  swap32: the upper half of a with the lower
-// half of b; swap16: groups 1 and 3 of a with groups 0 and 2 of b.
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-  const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r.x;
-  b = r.y;
-}
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
-  const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r.x;
-  b = r.y;
-}
-// v[j] of group g becomes v[g] of group j.
-__device__ __forceinline__ void transpose_groups(uint32_t& v0, uint32_t& v1, uint32_t& v2, uint32_t& v3) {
-  swap32(v0, v2);
-  swap32(v1, v3);
-  swap16(v0, v1);
-  swap16(v2, v3);
 }
 
 // Rows of a packed matrix: buffers that start at the first of them (loads past
@@ -145,147 +123,369 @@ __device__ __forceinline__ PackedRows uniform(const PackedRows& r) {
                     (uint32_t)__builtin_amdgcn_readfirstlane(r.s_bytes)};
 }
 
-// One quad of a lane's packed row.  The block scales of a quad are 32 bytes of
-// the row (MXFP4: 16); group g loads those of unit g and the groups exchange
-// them afterwards, which asks memory for a quarter of the pieces that every
-// lane loading its own scales unit by unit would.
-template <int KIND>
-struct Quad {
-  uint4 w[4];
-  u32x2 s;
+// How k channels are dealt out: `waves` waves a workgroup, of at most `most`,
+// QW quads a wave and pass.
+struct QuadPlan { int passes, waves; };
+template <int QW>
+__host__ __device__ inline QuadPlan quad_plan(int64_t k, int most) {
+  const int pieces = (int)((k + 512 * QW - 1) / (512 * QW)), passes = (pieces + most - 1) / most;
+  return QuadPlan{passes, (pieces + passes - 1) / passes};
+}
 
-  // row_w, row_s: byte offsets of the lane's row; q: the quad
-  // (the whole offset is in the lane's part, which is what the bounds check
-  // looks at)
-  __device__ __forceinline__ void load_weights(int u, const PackedRows& t, uint32_t row_w, int q, int g) {
+// NVFP4 weights against 4 NG tokens on the 4x4x4 matrix instruction, whose 16
+// blocks are 16 chunks of 32 channels: lane 4 b + i holds chunk b of row i of a
+// group of four rows (a load instruction reads 256 contiguous bytes of each) or
+// of token i of a group of four tokens.  A block of 16 weights is four
+// instructions; its scale then multiplies their fp32 sum, so that the weights
+// enter as plain E2M1 values, one conversion for two of them.  Per 1 KiB of
+// weights that is 27 vector and 8 matrix instructions for up to four tokens;
+// the 16x16x32 instruction, which needs the scales in the weights, took 132 and
+// held the expert layer to 3.6 TB/s.
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Where a lane reads in four rows of a quad, from the first of them on: its
+// chunk's weights and its two codes.  Codes past channel k are past the buffer
+// and read as zero.  ODD: k is no multiple of 32, so that rows of codes start at
+// odd addresses and the last chunk of a row has one code; a kernel of its own,
+// because the choice inside the loop cost 25 to 50 registers and let it spill
+// (2 quads a wave, 4096x12288: 22 us for one token and 42 for five, else 9 and 11).
+template <bool ODD>
+struct LaneAt {
+  uint32_t w, s, s1;
+  __device__ __forceinline__ LaneAt(uint32_t row, int q, int b, int k) {
+    const int left = k - q * 512 - b * 32;
+    w = row * ((uint32_t)k >> 1) + b * 16;
+    s = row * ((uint32_t)k >> 4) + b * 2;
+    s1 = ODD && left > 16 ? s + 1 : kBeyond;
+    if (left <= 0) s = kBeyond;
+  }
+};
+
+// Four rows' chunk of one quad, as loaded.
+struct RowGroup {
+  uint4 w;
+  uint32_t s;                                        // two codes
+
+  // row: the first of the four in t.  The scalar offset is held to the buffer's
+  // size, which keeps the bounds check (lane's offset against size less scalar
+  // offset) right for rows past the end.
+  template <bool ODD>
+  __device__ __forceinline__ void load(const PackedRows& t, uint32_t row, int q, const LaneAt<ODD>& at, int k) {
+    const auto bw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(t.w), 0, (int)t.w_bytes, 0x00020000);
+    const auto bs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(t.s), 0, (int)t.s_bytes, 0x00020000);
+    const uint32_t ow = min(row * ((uint32_t)k >> 1) + q * 256, t.w_bytes);
+    const uint32_t os = min(row * ((uint32_t)k >> 4) + q * 32, t.s_bytes);
+    w = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(bw, (int)at.w, (int)ow, 0));
+    if constexpr (!ODD) {
+      s = __builtin_amdgcn_raw_buffer_load_b16(bs, (int)at.s, (int)os, 0);
+    } else {
+      const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)at.s, (int)os, 0);
+      const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)at.s1, (int)os, 0);
+      s = lo | hi << 8;
+    }
+  }
+};
+
+// A chunk of 32 channels of one token, bf16, two to a word.
+typedef uint32_t Chunk[16];
+
+template <int HALF>
+__device__ __forceinline__ s16x4 e2m1x4(uint32_t w) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  u32x2_t v;
+  v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2 * HALF));
+  v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2 * HALF + 1));
+  return __builtin_bit_cast(s16x4, v);
+}
+__device__ __forceinline__ s16x4 pair_of(uint32_t a, uint32_t b) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(s16x4, u32x2_t{a, b});
+}
+// lane i of each four gives its value to all four
+template <int I>
+__device__ __forceinline__ float quad_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), I * 0x55, 0xF, 0xF, true));
+}
+
+// acc[n] += 4 rows x 4 tokens over the lane's chunk (register i: row i; the
+// tokens are x[0][n], and x[1][n] to be added to it where PARTS is 2).
+template <int NG, int PARTS>
+__device__ __forceinline__ void multiply_group(const RowGroup& r, const Chunk (&x)[PARTS][NG], f32x4 (&acc)[NG]) {
+  const float s[2] = {e4m3_f32<0>(r.s), e4m3_f32<1>(r.s)};
+  const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {                      // the two blocks of 16
+    s16x4 a[4];
+    a[0] = e2m1x4<0>(w[2 * h]);
+    a[1] = e2m1x4<1>(w[2 * h]);
+    a[2] = e2m1x4<0>(w[2 * h + 1]);
+    a[3] = e2m1x4<1>(w[2 * h + 1]);
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(a[m], pair_of(x[p][n][8 * h + 2 * m], x[p][n][8 * h + 2 * m + 1]), d,
+                                                     0, 0, 0);
+      acc[n][0] = __builtin_fmaf(quad_lane<0>(s[h]), d[0], acc[n][0]);
+      acc[n][1] = __builtin_fmaf(quad_lane<1>(s[h]), d[1], acc[n][1]);
+      acc[n][2] = __builtin_fmaf(quad_lane<2>(s[h]), d[2], acc[n][2]);
+      acc[n][3] = __builtin_fmaf(quad_lane<3>(s[h]), d[3], acc[n][3]);
+    }
+  }
+}
+
+// Exchanges between the four 16-lane rows of a wave.  swap32: the upper half of
+// a with the lower half of b; swap16: rows 1 and 3 of a with rows 0 and 2 of b.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r.x;
+  b = r.y;
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const u32x2 r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r.x;
+  b = r.y;
+}
+__device__ __forceinline__ float add_swap32(float a, float b) {
+  uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  swap32(x, y);
+  return __uint_as_float(x) + __uint_as_float(y);
+}
+__device__ __forceinline__ float add_swap16(float a, float b) {
+  uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  swap16(x, y);
+  return __uint_as_float(x) + __uint_as_float(y);
+}
+// + the lane N further on (around) in its row of 16
+template <int N>
+__device__ __forceinline__ float add_ror(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x120 + N, 0xF, 0xF, true));
+}
+
+// The sums over a wave's 16 chunks of four row groups, two at a time: first
+// pair(a0, a2) and pair(a1, a3), then rest of the two.  Lanes 16 q + j (and + 4,
+// + 8, + 12) get row group q, token j.
+__device__ __forceinline__ f32x4 sum_chunks_pair(const f32x4& a, const f32x4& b) {
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = add_swap32(a[e], b[e]);
+  return v;
+}
+__device__ __forceinline__ f32x4 sum_chunks_rest(const f32x4& a, const f32x4& b) {
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = add_ror<4>(add_ror<8>(add_swap16(a[e], b[e])));
+  return v;
+}
+
+// Row tiles begin .. end - 1 (four groups of four rows) against 4 NG tokens, by
+// a workgroup dealt out as in plan.  A step is RT tiles and QW quads a wave; TB
+// tiles make a batch, whose partial sums the waves leave in `part` (per wave
+// TB * NG * 16).
+//   tile_rows        from a tile's rows to the next one's
+//   group_row[q]     the first row of group q in a tile (the lane's: + lane % 4)
+//   rows_of(t)       the packed rows from which tile t's are counted; they end
+//                    before those of tile end (where RT > 1)
+//   load_tokens(q)   the lane's chunks of the QW quads from q on, into x
+//   done(t, n, q, j, sum)  called once for every row group q of tile t and token
+//                    4 n + j, by some thread, with the sum over the waves, added
+//                    in their order
+template <bool ODD, int NG, int QW, int RT, int TB, typename RowsOf, typename LoadTokens, typename Done>
+__device__ __forceinline__ void stream_rows(int begin, int end, int k, const QuadPlan& plan, uint32_t tile_rows,
+                                            const uint32_t (&group_row)[4], Chunk (&x)[QW][1][NG], f32x4* part,
+                                            RowsOf rows_of, LoadTokens load_tokens, Done done) {
+  static_assert(TB % RT == 0, "whole steps in a batch");
+  const int lane = threadIdx.x & 63, b = lane >> 2, i = lane & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = plan.waves, passes = plan.passes;
+  constexpr int SLOTS = NG * 16;                     // partial sums of a wave and tile
+
+  RowGroup r[RT][QW][4];
+  // what is loaded: from tile at_t on, pass at_pass of the batch from at_batch on
+  int at_batch = begin, at_pass = 0, at_t = begin;
+  PackedRows next;
+  auto quad = [&](int pass, int z) { return (pass * waves + wave) * QW + z; };
+  auto aim = [&]() {
+    next = rows_of(min(at_t, end - 1));
+    if (at_t >= end) next.w_bytes = next.s_bytes = 0;
+    next = uniform(next);
+  };
+  // quads past the last one read as zero: their weights' codes are past the buffer
+  auto load = [&](int t, int z, int q) {
+    const int at = quad(at_pass, z);
+    PackedRows rows = next;
+    if (at * 512 >= k) rows.w_bytes = rows.s_bytes = 0;
+    r[t][z][q].load(rows, group_row[q] + t * tile_rows, at, LaneAt<ODD>(i, at, b, k), k);
+  };
+  auto advance = [&]() {
+    at_t += RT;
+    if (at_t >= min(end, at_batch + TB)) {
+      if (++at_pass == passes) {
+        at_pass = 0;
+        at_batch += TB;
+      }
+      at_t = at_batch;
+    }
+    aim();
+  };
+  auto tokens = [&](int pass) { load_tokens(quad(pass, 0)); };
+  aim();
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)                      // in order of use
+#pragma unroll
+      for (int z = 0; z < QW; ++z) load(t, z, (q & 1) * 2 + (q >> 1));
+  advance();
+  if (passes == 1) tokens(0);
+  for (int batch = begin; batch < end; batch += TB) {
+    const int count = min(TB, end - batch);
+    for (int pass = 0; pass < passes; ++pass) {
+      if (passes > 1) tokens(pass);
+      f32x4* mine = part + wave * TB * SLOTS;
+      for (int t = 0; t < count; t += RT) {
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+          f32x4 half[2][NG];                         // groups 0 and 2, groups 1 and 3
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            f32x4 acc[2][NG];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int q = p + 2 * h;
+#pragma unroll
+              for (int n = 0; n < NG; ++n) acc[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int z = 0; z < QW; ++z) {
+                multiply_group<NG, 1>(r[u][z][q], x[z], acc[h]);
+                load(u, z, q);
+                __builtin_amdgcn_sched_barrier(0);   // the load goes out here, not where its value is near
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) half[p][n] = sum_chunks_pair(acc[0][n], acc[1][n]);
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            f32x4 v = sum_chunks_rest(half[0][n], half[1][n]);
+            if ((lane & 12) == 0) {
+              f32x4& slot = mine[n * 16 + (lane >> 4) * 4 + i];
+              if (pass) v += slot;
+              slot = v;
+            }
+          }
+          mine += SLOTS;
+        }
+        advance();
+      }
+    }
+    lds_barrier();
+    for (int s = threadIdx.x; s < count * SLOTS; s += 64 * waves) {
+      f32x4 v = part[s];
+      for (int z = 1; z < waves; ++z) v += part[z * TB * SLOTS + s];
+      done(batch + s / SLOTS, s / 16 % NG, s / 4 % 4, s & 3, v);
+    }
+    lds_barrier();                                   // before the next batch's partial sums
+  }
+}
+
+// Chunks of bf16 rows, in two steps: the lanes of a token (row: lane 4 b + j's
+// token j) read neighbouring pieces, channels past k as zero, and then exchange
+// them in LDS (4 KiB, the wave's own).
+static __device__ const uint4 kZeroPiece[1] = {};
+__device__ __forceinline__ void load_pieces(Chunk& x, const uint8_t* row, int q, int k) {
+  const int b = (threadIdx.x & 63) >> 2;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroPiece);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int c = q * 512 + (16 * m + b) * 8;
+    const uint4 v = global_load16(c < k ? row + (int64_t)c * 2 : zero);
+    x[4 * m] = v.x;
+    x[4 * m + 1] = v.y;
+    x[4 * m + 2] = v.z;
+    x[4 * m + 3] = v.w;
+  }
+}
+__device__ __forceinline__ void pieces_to_chunk(Chunk& x, uint8_t* lds) {
+  const int lane = threadIdx.x & 63, b = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    *reinterpret_cast<uint4*>(lds + j * 1024 + (16 * m + b) * 16) =
+        make_uint4(x[4 * m], x[4 * m + 1], x[4 * m + 2], x[4 * m + 3]);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint4 p = *reinterpret_cast<const uint4*>(lds + j * 1024 + b * 64 + m * 16);
+    x[4 * m] = p.x;
+    x[4 * m + 1] = p.y;
+    x[4 * m + 2] = p.z;
+    x[4 * m + 3] = p.w;
+  }
+}
+
+// Chunks of packed NVFP4 rows, expanded (without their tensor scale).
+template <bool ODD>
+__device__ __forceinline__ void load_chunk(Chunk& x, const PackedRows& t, uint32_t row, int q, int k) {
+  RowGroup r;
+  r.load(t, 0, q, LaneAt<ODD>(row, q, (threadIdx.x & 63) >> 2, k), k);
+  const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+  const float s0 = e4m3_f32<0>(r.s), s1 = e4m3_f32<1>(r.s);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint4 p = fp4x8_bf16(w[m], m < 2 ? s0 : s1);
+    x[4 * m] = p.x;
+    x[4 * m + 1] = p.y;
+    x[4 * m + 2] = p.z;
+    x[4 * m + 3] = p.w;
+  }
+}
+
+// MXFP4 weights against 16 NT MXFP4 tokens on the scaled 16x16x128 instruction,
+// which takes nibbles and scales as they are.  A unit is 128 channels; lane l
+// works on row (token) l % 16 of a tile and, as group g = l / 16, on chunk g of
+// 32 consecutive channels of a unit.  The order of channels within a unit does
+// not matter as long as both operands share it, so a lane's weights of a unit
+// are one 16-byte load.  The block scales of a quad are 16 bytes of the row;
+// group g loads those of unit g and the groups exchange them, which asks memory
+// for a quarter of the pieces that loading them unit by unit would.
+struct MxQuad {
+  uint4 w[4];
+  uint32_t s;
+
+  // row: the lane's row in t (the whole offset is in the lane's part, which is
+  // what the bounds check looks at)
+  __device__ __forceinline__ void load_unit(int u, const PackedRows& t, uint32_t row, int q, int g, int k) {
     const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(t.w), 0, (int)t.w_bytes, 0x00020000);
-    const uint32_t at = row_w + q * 256 + g * 16 + u * 64;
+    const uint32_t at = row * ((uint32_t)k >> 1) + q * 256 + g * 16 + u * 64;
     w[u] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0));
   }
-  // Past channel k the weights are the next row's; their scales are zero here
-  // (as a power of two: 2^-127), and so is the other operand.
-  __device__ __forceinline__ void load_scales(const PackedRows& t, uint32_t row_s, int q, int g, int k) {
+  // Past channel k the weights are the next row's; their scales are 2^-127
+  // there, and the tokens zero.
+  __device__ __forceinline__ void load_scales(const PackedRows& t, uint32_t row, int q, int g, int k) {
     const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(t.s), 0, (int)t.s_bytes, 0x00020000);
-    constexpr int N = KIND == kMX ? 4 : 8;           // bytes of a unit
-    const uint32_t at = row_s + q * (4 * N) + g * N;
+    const uint32_t at = row * ((uint32_t)k >> 5) + q * 16 + g * 4;
     if ((q + 1) * 512 <= k) {
-      if constexpr (KIND == kMX) s.x = __builtin_amdgcn_raw_buffer_load_b32(b, (int)at, 0, 0);
-      else s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)at, 0, 0));
-    } else {                                         // byte by byte: the words may reach past the buffer
-      uint32_t v[2] = {0, 0};
+      s = __builtin_amdgcn_raw_buffer_load_b32(b, (int)at, 0, 0);
+    } else {                                         // byte by byte: the word may reach past the buffer
+      s = 0;
+      int left = k - q * 512 - g * 128;
+      asm volatile("" : "+v"(left));                 // worked out here, not kept in registers
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool in = q * 512 + g * 128 + i * (128 / N) < k;
-        v[i >> 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(b, (int)(in ? at + i : kBeyond), 0, 0) << (8 * (i & 3));
-      }
-      s.x = v[0];
-      s.y = v[1];
+      for (int i = 0; i < 4; ++i)
+        s |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(b, (int)(i * 32 < left ? at + i : kBeyond), 0, 0) << (8 * i);
     }
   }
-
-  // This lane's scales of the four units.  NVFP4: x = units 0 (low half) and
-  // 2, y = units 1 and 3, two codes each; MXFP4: x = a byte per unit.
-  __device__ __forceinline__ u32x2 scales(int g) const {
-    u32x2 r;
-    if constexpr (KIND == kMX) {
-      uint32_t a = s.x, b = s.x;
-      swap32(a, b);                                  // units g % 2 and g % 2 + 2
-      uint32_t c = __builtin_amdgcn_perm(b, a, g < 2 ? 0x05040100u : 0x07060302u), d = c;
-      swap16(c, d);                                  // units 0 and 2, units 1 and 3
-      r.x = __builtin_amdgcn_perm(d, c, (g & 1) ? 0x07030501u : 0x06020400u);
-      r.y = 0;
-    } else {
-      uint32_t a = s.x, b = s.y;
-      swap32(a, b);                                  // groups 2 (g / 2), 2 (g / 2) + 1 of units g % 2 and g % 2 + 2
-      uint32_t e = __builtin_amdgcn_perm(b, a, 0x05040100u), f = __builtin_amdgcn_perm(b, a, 0x07060302u);
-      swap16(e, f);
-      r.x = e;
-      r.y = f;
-    }
-    return r;
-  }
-  // the two NVFP4 codes of unit u, as fp32
-  static __device__ __forceinline__ void codes(u32x2 s, int u, float& a, float& b) {
-    const uint32_t v = u & 1 ? s.y : s.x;
-    if (u < 2) {
-      a = e4m3_f32<0>(v);
-      b = e4m3_f32<1>(v);
-    } else {
-      a = e4m3_f32<2>(v);
-      b = e4m3_f32<3>(v);
-    }
-  }
-};
-
-// What tokens read past channel k.
-static __device__ const uint4 kZeroPiece[1] = {};
-
-// Where 16 tokens are: the lane's row of bf16 values, or its offsets in the
-// rows of a packed matrix.
-struct TokenRows {
-  const uint8_t* x;
-  PackedRows packed;
-  uint32_t row_w, row_s;
-};
-
-// A quad of 16 tokens in registers: 16-bit values, expanded where they were
-// packed; channels past k are zero.
-template <int KIND>
-struct TokenQuad {
-  uint4 x[4][4];                                     // [unit][8 channels]
-
-  __device__ __forceinline__ void load(const TokenRows& t, int q, int g, int k) {
-    if constexpr (KIND == kW4A16) {
-      // four lanes of a token read 64 neighbouring bytes; the groups then
-      // exchange pieces, so that each holds 32 consecutive channels of a unit
-      const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroPiece);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = q * 512 + u * 128 + j * 32 + g * 8;
-          x[u][j] = global_load16(c < k ? t.x + (int64_t)c * 2 : zero);
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        transpose_groups(x[u][0].x, x[u][1].x, x[u][2].x, x[u][3].x);
-        transpose_groups(x[u][0].y, x[u][1].y, x[u][2].y, x[u][3].y);
-        transpose_groups(x[u][0].z, x[u][1].z, x[u][2].z, x[u][3].z);
-        transpose_groups(x[u][0].w, x[u][1].w, x[u][2].w, x[u][3].w);
-      }
-    } else {
-      Quad<KIND> p;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) p.load_weights(u, t.packed, t.row_w, q, g);
-      p.load_scales(t.packed, t.row_s, q, g, k);
-      const u32x2 s = p.scales(g);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float a, b;
-        Quad<KIND>::codes(s, u, a, b);
-        x[u][0] = fp4x8_f16(p.w[u].x, splat_f16(a));
-        x[u][1] = fp4x8_f16(p.w[u].y, splat_f16(a));
-        x[u][2] = fp4x8_f16(p.w[u].z, splat_f16(b));
-        x[u][3] = fp4x8_f16(p.w[u].w, splat_f16(b));
-      }
-    }
-  }
-};
-
-template <>
-struct TokenQuad<kMX> {
-  uint4 x[4];
-  uint32_t s;                                        // a byte per unit
-
-  __device__ __forceinline__ void load(const TokenRows& t, int q, int g, int k) {
-    Quad<kMX> p;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) p.load_weights(u, t.packed, t.row_w, q, g);
-    p.load_scales(t.packed, t.row_s, q, g, k);
-    s = p.scales(g).x;
-    const int left = k - q * 512 - g * 32;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) x[u] = left > u * 128 ? p.w[u] : make_uint4(0, 0, 0, 0);
+  // the scales of the lane's chunk in the four units, a byte each
+  __device__ __forceinline__ uint32_t scales(int g) const {
+    uint32_t a = s, b = s;
+    swap32(a, b);                                    // units g % 2 and g % 2 + 2
+    uint32_t c = __builtin_amdgcn_perm(b, a, g < 2 ? 0x05040100u : 0x07060302u), d = c;
+    swap16(c, d);                                    // units 0 and 2, units 1 and 3
+    return __builtin_amdgcn_perm(d, c, (g & 1) ? 0x07030501u : 0x06020400u);
   }
 };
 
@@ -296,154 +496,125 @@ __device__ __forceinline__ f32x4 mfma_mx_unit(uint4 a, uint32_t sa, uint4 b, uin
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, U, (int)sa, U, (int)sb);
 }
 
-// acc[n] += unit u of 16 rows x 16 tokens each.  Even and odd pieces add up
-// apart (acc[0], acc[1]), so that one product need not wait for the last.
-template <int KIND, int NT>
-__device__ __forceinline__ void multiply_unit(uint4 w, u32x2 ws, int u, const TokenQuad<KIND> (&x)[NT],
-                                              f32x4 (&acc)[2][NT]) {
-  if constexpr (KIND == kMX) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      f32x4& c = acc[u & 1][n];
-      if (u == 0) c = mfma_mx_unit<0>(w, ws.x, x[n].x[u], x[n].s, c);
-      else if (u == 1) c = mfma_mx_unit<1>(w, ws.x, x[n].x[u], x[n].s, c);
-      else if (u == 2) c = mfma_mx_unit<2>(w, ws.x, x[n].x[u], x[n].s, c);
-      else c = mfma_mx_unit<3>(w, ws.x, x[n].x[u], x[n].s, c);
-    }
-  } else {
-    float s0, s1;
-    Quad<KIND>::codes(ws, u, s0, s1);
-    const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float s = j < 2 ? s0 : s1;
-      const uint4 a = KIND == kW4A16 ? fp4x8_bf16(wv[j], s) : fp4x8_f16(wv[j], splat_f16(s));
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        acc[j & 1][n] = KIND == kW4A16 ? mfma_bf16(a, x[n].x[u][j], acc[j & 1][n])
-                                       : mfma_f16(a, x[n].x[u][j], acc[j & 1][n]);
-    }
-  }
-}
-
-// Row tiles begin .. end - 1 against 16 NT tokens, by a workgroup.  A step is RT
-// row tiles; a pass, kStreamWaves * QW quads of the channels, QW a wave's; TB
-// steps make a batch, whose partial tiles the waves write to `part`
-// (kStreamWaves * TB * RT * NT * 64 of them).
-//   rows_of(t)       the packed rows from tile t on (at least to the end of the
-//                    step's tiles, as far as they exist)
-//   row_w, row_s     byte offsets of the lane's row in a tile; tile_w, tile_s:
-//                    from a tile to the next
-//   done(t, n, l, sum)  called once for every lane l of tile t, token tile n, by
-//                    some thread; sum(l) adds up the waves, in order
-template <int KIND, int NT, int QW, int TB, typename RowsOf, typename Done>
-__device__ __forceinline__ void stream_tiles(int begin, int end, int k, uint32_t row_w, uint32_t row_s, uint32_t tile_w,
-                                             uint32_t tile_s, const TokenRows (&tokens)[NT], f32x4* part, RowsOf rows_of,
-                                             Done done) {
-  constexpr int RT = 2 / QW;
-  static_assert(QW * RT == 2, "8 units in flight");
+// Row tiles begin .. end - 1 of 16 rows; as stream_rows, with per wave
+// TB * NT * 64 partial sums and done(t, n, l, sum) for every lane l of an
+// instruction's result.
+template <int NT, int QW, int RT, int TB, typename RowsOf, typename Done>
+__device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const QuadPlan& plan,
+                                               const PackedRows (&tokens)[NT], const uint32_t (&token_row)[NT],
+                                               f32x4* part, RowsOf rows_of, Done done) {
+  static_assert(TB % RT == 0, "whole steps in a batch");
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int quads = (k + 511) >> 9, passes = (quads + kStreamWaves * QW - 1) / (kStreamWaves * QW);
-  auto quad_of = [&](int pass, int i) { return (pass * kStreamWaves + wave) * QW + i; };
-
-  Quad<KIND> w[2];
-  TokenQuad<KIND> x[QW][NT];
-  // the step that is loaded: tile at_t of pass at_pass of the batch from
-  // at_batch on
+  const int waves = plan.waves, passes = plan.passes;
+  MxQuad w[RT][QW], x[QW][NT];
+  uint32_t xs[QW][NT];
   int at_batch = begin, at_pass = 0, at_t = begin;
-  PackedRows next = uniform(rows_of(begin));
-  auto advance = [&]() {
-    at_t += RT;
-    if (at_t >= end || at_t >= at_batch + TB * RT) {
-      if (++at_pass == passes) {
-        at_pass = 0;
-        at_batch += TB * RT;
-      }
-      at_t = at_batch;
-    }
+  PackedRows next;
+  auto quad = [&](int pass, int z) { return (pass * waves + wave) * QW + z; };
+  auto aim = [&]() {
     next = rows_of(min(at_t, end - 1));
     if (at_t >= end) next.w_bytes = next.s_bytes = 0;
     next = uniform(next);
   };
-  auto load_scales = [&](int i) {                    // i = r * QW + quad of the wave
-    w[i].load_scales(next, row_s + (i / QW) * tile_s, quad_of(at_pass, i % QW), g, k);
+  auto rows = [&](int z) {
+    PackedRows v = next;
+    if (quad(at_pass, z) * 512 >= k) v.w_bytes = v.s_bytes = 0;
+    return v;
   };
-  auto load_weights = [&](int i, int u) {
-    w[i].load_weights(u, next, row_w + (i / QW) * tile_w, quad_of(at_pass, i % QW), g);
+  auto load_unit = [&](int t, int z, int u) {
+    w[t][z].load_unit(u, rows(z), 16 * t + (lane & 15), quad(at_pass, z), g, k);
+  };
+  auto load_scales = [&](int t, int z) { w[t][z].load_scales(rows(z), 16 * t + (lane & 15), quad(at_pass, z), g, k); };
+  auto advance = [&]() {
+    at_t += RT;
+    if (at_t >= min(end, at_batch + TB)) {
+      if (++at_pass == passes) {
+        at_pass = 0;
+        at_batch += TB;
+      }
+      at_t = at_batch;
+    }
+    aim();
   };
   auto load_tokens = [&](int pass) {
 #pragma unroll
-    for (int i = 0; i < QW; ++i)
+    for (int z = 0; z < QW; ++z)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) x[i][n].load(tokens[n], quad_of(pass, i), g, k);
+      for (int n = 0; n < NT; ++n) {
+        const int q = quad(pass, z);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[z][n].load_unit(u, tokens[n], token_row[n], q, g, k);
+        x[z][n].load_scales(tokens[n], token_row[n], q, g, k);
+      }
+#pragma unroll
+    for (int z = 0; z < QW; ++z)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        xs[z][n] = x[z][n].scales(g);
+        const int left = k - quad(pass, z) * 512 - g * 32;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (left <= u * 128) x[z][n].w[u] = make_uint4(0, 0, 0, 0);
+      }
     __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
   };
-
+  aim();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    load_scales(i);
+  for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load_weights(i, u);
-  }
+    for (int z = 0; z < QW; ++z) {
+      load_scales(t, z);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load_unit(t, z, u);
+    }
   advance();
   if (passes == 1) load_tokens(0);
-  for (int batch = begin; batch < end; batch += TB * RT) {
-    f32x4 acc[TB][RT][NT];
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[b][r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int batch = begin; batch < end; batch += TB) {
+    const int count = min(TB, end - batch);
     for (int pass = 0; pass < passes; ++pass) {
       if (passes > 1) load_tokens(pass);
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        if (batch + b * RT >= end) break;
+      f32x4* mine = part + wave * TB * NT * 64 + lane;
+      for (int t = 0; t < count; t += RT) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          f32x4 sum[2][NT];
+          f32x4 sum[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sum[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int z = 0; z < QW; ++z) {
+            MxQuad& m = w[r][z];
+            const uint32_t ws = m.scales(g);
+            load_scales(r, z);
+            auto unit = [&](auto u) {
+              constexpr int U = decltype(u)::value;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) sum[n] = mfma_mx_unit<U>(m.w[U], ws, x[z][n].w[U], xs[z][n], sum[n]);
+              load_unit(r, z, U);
+              __builtin_amdgcn_sched_barrier(0);     // the load goes out here, not where its value is near
+            };
+            unit(std::integral_constant<int, 0>{});
+            unit(std::integral_constant<int, 1>{});
+            unit(std::integral_constant<int, 2>{});
+            unit(std::integral_constant<int, 3>{});
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            sum[0][n] = acc[b][r][n];
-            sum[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (pass) sum[n] += mine[n * 64];
+            mine[n * 64] = sum[n];
           }
-#pragma unroll
-          for (int i = 0; i < QW; ++i) {
-            const int at = r * QW + i;
-            const u32x2 ws = w[at].scales(g);
-            load_scales(at);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              multiply_unit<KIND, NT>(w[at].w[u], ws, u, x[i], sum);
-              load_weights(at, u);
-              __builtin_amdgcn_sched_barrier(0);     // the load goes out here, not where its value is near
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[b][r][n] = sum[0][n] + sum[1][n];
+          mine += NT * 64;
         }
         advance();
       }
     }
-#pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) part[(((wave * TB + b) * RT + r) * NT + n) * 64 + lane] = acc[b][r][n];
     lds_barrier();
-    const int count = min(TB * RT, end - batch);
-    for (int q = threadIdx.x; q < count * NT * 64; q += 64 * kStreamWaves)
-      done(batch + (q >> 6) / NT, (q >> 6) % NT, q & 63, [&](int l) {
-        const f32x4* p = part + (q & ~63) + l;
-        f32x4 v = *p;
-#pragma unroll
-        for (int z = 1; z < kStreamWaves; ++z) v += p[z * TB * RT * NT * 64];
-        return v;
-      });
-    lds_barrier();                                   // before the next batch's partial tiles
+    for (int s = threadIdx.x; s < count * NT * 64; s += 64 * waves) {
+      f32x4 v = part[s];
+      for (int z = 1; z < waves; ++z) v += part[z * TB * NT * 64 + s];
+      done(batch + (s >> 6) / NT, (s >> 6) % NT, s & 63, v);
+    }
+    lds_barrier();                                   // before the next batch's partial sums
   }
 }
 
