@@ -41,9 +41,15 @@ unsigned few_grid(int tiles, int waves, int cu_waves) {
   return (unsigned)(tiles < most ? tiles : most);
 }
 
+// A workgroup's run of tiles.  Those that share a CU (kCus apart) share a run
+// that is as long as any other CU's, also where the tiles per workgroup are not
+// whole.
 __device__ __forceinline__ void tile_run(int tiles, int& begin, int& end) {
-  begin = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
-  end = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+  const int n = gridDim.x, shared = n / kCus;
+  int at = blockIdx.x;
+  if (shared > 1 && n == shared * kCus) at = at % kCus * shared + at / kCus;
+  begin = (int)((int64_t)tiles * at / n);
+  end = (int)((int64_t)tiles * (at + 1) / n);
 }
 
 template <int KIND>
@@ -56,7 +62,7 @@ __device__ __forceinline__ void store_rows(const ProductArgs& a, int row, int to
 
 // 4 NG tokens (the y coordinate's) against NVFP4 rows.  CU: waves that share a
 // CU, MW: waves of a workgroup, both at most.
-template <int KIND, bool ODD, int NG, int QW, int RT, int CU, int MW>
+template <int KIND, bool ODD, int NG, int CU, int MW>
 __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a) {
   constexpr int TB = 4;
   __shared__ f32x4 part[MW * TB * NG * 16];
@@ -68,39 +74,39 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
   int begin, end;
   tile_run((a.out + 15) >> 4, begin, end);
   const uint32_t group_row[4] = {0, 4, 8, 12};
-  Chunk x[QW][1][NG];
+  Chunk x[1][NG];
   auto rows_of = [&](int t) {
     const int row = t * 16;
-    const uint32_t rows = min(min(16 * RT, (end - t) * 16), a.out - row);
+    const uint32_t rows = min(16, a.out - row);
     return PackedRows{a.wp + (int64_t)row * ldw, a.wc + (int64_t)row * lds, rows * ldw, rows * lds};
   };
+  RowGroup packed[NG];
   auto load_tokens = [&](int q) {
 #pragma unroll
-    for (int z = 0; z < QW; ++z)
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int t0 = min(tok0 + 4 * n, a.tokens - 1), t = min(j, a.tokens - 1 - t0);      // others are not stored
-        if constexpr (KIND == kW4A16) {
-          load_pieces(x[z][0][n], a.xp + (int64_t)(t0 + t) * a.ldx, q + z, a.k);
-        } else {
-          const uint32_t rows = (q + z) * 512 < a.k ? min(4, a.tokens - t0) : 0;
-          load_chunk<ODD>(x[z][0][n], PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds}, t,
-                     q + z, a.k);
-        }
+    for (int n = 0; n < NG; ++n) {
+      const int t0 = min(tok0 + 4 * n, a.tokens - 1), t = min(j, a.tokens - 1 - t0);        // others are not stored
+      if constexpr (KIND == kW4A16) {
+        load_pieces(x[0][n], a.xp + (int64_t)(t0 + t) * a.ldx, q, a.k);
+      } else {
+        const uint32_t rows = q * 512 < a.k ? min(4, a.tokens - t0) : 0;
+        packed[n].load(PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds}, 0, q,
+                       LaneAt<ODD>(t, q, lane >> 2, a.k), a.k);
       }
-    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
-    if constexpr (KIND == kW4A16) {
+    }
+  };
+  auto take_tokens = [&]() {
 #pragma unroll
-      for (int z = 0; z < QW; ++z)
-#pragma unroll
-        for (int n = 0; n < NG; ++n) pieces_to_chunk(x[z][0][n], stage + wave * 4096);
+    for (int n = 0; n < NG; ++n) {
+      if constexpr (KIND == kW4A16) pieces_to_chunk(x[0][n], stage + wave * 4096);
+      else expand_chunk(x[0][n], packed[n]);
     }
   };
   auto done = [&](int t, int n, int q, int tj, f32x4 v) {
     const int row = t * 16 + q * 4, tok = tok0 + 4 * n + tj;
     if (tok < a.tokens && row < a.out) store_rows<KIND>(a, row, tok, v);
   };
-  stream_rows<ODD, NG, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), 16, group_row, x, part, rows_of, load_tokens, done);
+  stream_rows<ODD, NG, TB>(begin, end, a.k, quad_plan<1>(a.k, CU), group_row, x, part, rows_of, load_tokens, take_tokens,
+                           done);
 }
 
 // 16 NT tokens against MXFP4 rows.
@@ -134,13 +140,13 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductA
   stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, part, rows_of, done);
 }
 
-template <int KIND, bool ODD, int NG, int QW, int RT, int CU>
+template <int KIND, bool ODD, int NG, int CU>
 int run_few(const ProductArgs& a, hipStream_t s) {
-  const int waves = quad_plan<QW>(a.k, CU).waves;
+  const int waves = quad_plan<1>(a.k, CU).waves;
   const dim3 grid(few_grid((a.out + 15) / 16, waves, CU), (a.tokens + 4 * NG - 1) / (4 * NG));
-  if (waves <= 4) few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, 4><<<grid, 64 * waves, 0, s>>>(a);
-  else if (CU == 8 || waves <= 8) few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, 8><<<grid, 64 * waves, 0, s>>>(a);
-  else few_tokens_kernel<KIND, ODD, NG, QW, RT, CU, CU><<<grid, 64 * waves, 0, s>>>(a);
+  if (waves <= 4) few_tokens_kernel<KIND, ODD, NG, CU, 4><<<grid, 64 * waves, 0, s>>>(a);
+  else if (CU == 8 || waves <= 8) few_tokens_kernel<KIND, ODD, NG, CU, 8><<<grid, 64 * waves, 0, s>>>(a);
+  else few_tokens_kernel<KIND, ODD, NG, CU, CU><<<grid, 64 * waves, 0, s>>>(a);
   return launch_status("few_tokens_kernel");
 }
 
@@ -161,11 +167,10 @@ int run(const ProductArgs& a, hipStream_t s) {
     if (a.tokens <= 16) return narrow ? run_few_mx<1, 1, 2, 8>(a, s) : run_few_mx<1, 2, 1, 12>(a, s);
     return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
   } else {
-    const bool narrow = a.k <= 8192;
-    if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 1, 1, 16>(a, s) : run_few<KIND, true, 4, 1, 2, 8>(a, s);
-    if (a.tokens <= 4) return narrow ? run_few<KIND, false, 1, 1, 1, 16>(a, s) : run_few<KIND, false, 1, 2, 1, 16>(a, s);
-    if (a.tokens <= 8) return narrow ? run_few<KIND, false, 2, 1, 1, 16>(a, s) : run_few<KIND, false, 2, 2, 1, 12>(a, s);
-    return run_few<KIND, false, 4, 1, 2, 8>(a, s);
+    if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s) : run_few<KIND, true, 4, 8>(a, s);
+    if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s);
+    if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s);
+    return run_few<KIND, false, 4, 8>(a, s);
   }
 }
 

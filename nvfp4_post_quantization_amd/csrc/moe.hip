@@ -141,7 +141,7 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
   const uint8_t* c = a.c13 + (int64_t)e * 2 * a.inter * lds;
   const float s13 = a.s13[e];
   const uint32_t group_row[4] = {0, 4, (uint32_t)a.inter, (uint32_t)a.inter + 4};
-  Chunk x[1][1][NG];
+  Chunk x[1][NG];
   auto rows_of = [&](int t) {
     const uint32_t rows = a.inter + CH;              // to the end of the tile's up rows
     return PackedRows{w + (int64_t)t * CH * ldw, c + (int64_t)t * CH * lds, rows * ldw, rows * lds};
@@ -150,11 +150,12 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       const int tok = token_of_place(mask, first_tok + min(4 * n + j, count - 1));
-      load_pieces(x[0][0][n], a.x + tok * a.ldx, q, a.hidden);
+      load_pieces(x[0][n], a.x + tok * a.ldx, q, a.hidden);
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
+  };
+  auto take_tokens = [&]() {
 #pragma unroll
-    for (int n = 0; n < NG; ++n) pieces_to_chunk(x[0][0][n], stage + wave * 4096);
+    for (int n = 0; n < NG; ++n) pieces_to_chunk(x[0][n], stage + wave * 4096);
   };
   // done is called for the up rows by the lanes 8 after those of the gate rows
   auto done = [&](int t, int n, int q, int tj, f32x4 v) {
@@ -183,7 +184,7 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
     if ((t + 1) * CH == a.inter && q == 0)           // the rest of the row's last quad
       for (int ch = a.inter; ch < a.ldh; ch += 4) put(ch, make_uint2(0, 0), make_uint2(0, 0));
   };
-  stream_rows<ODD, NG, 1, 1, 4>(t0, t1, a.hidden, plan, CH, group_row, x, part, rows_of, load_tokens, done);
+  stream_rows<ODD, NG, 4>(t0, t1, a.hidden, plan, group_row, x, part, rows_of, load_tokens, take_tokens, done);
 }
 
 // h of a run of (job, 8 channels) pieces of work, as many runs as there are

@@ -149,7 +149,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // and read as zero.  ODD: k is no multiple of 32, so that rows of codes start at
 // odd addresses and the last chunk of a row has one code; a kernel of its own,
 // because the choice inside the loop cost 25 to 50 registers and let it spill
-// (2 quads a wave, 4096x12288: 22 us for one token and 42 for five, else 9 and 11).
+// (2 quads a wave, 4096x12288, five tokens: 42 us against 15).
 template <bool ODD>
 struct LaneAt {
   uint32_t w, s, s1;
@@ -284,47 +284,38 @@ __device__ __forceinline__ f32x4 sum_chunks_rest(const f32x4& a, const f32x4& b)
 }
 
 // Row tiles begin .. end - 1 (four groups of four rows) against 4 NG tokens, by
-// a workgroup dealt out as in plan.  A step is RT tiles and QW quads a wave; TB
-// tiles make a batch, whose partial sums the waves leave in `part` (per wave
-// TB * NG * 16).
-//   tile_rows        from a tile's rows to the next one's
+// a workgroup dealt out as in plan, a quad a wave and pass.  TB tiles make a
+// batch, whose partial sums the waves leave in `part` (per wave TB * NG * 16).
 //   group_row[q]     the first row of group q in a tile (the lane's: + lane % 4)
-//   rows_of(t)       the packed rows from which tile t's are counted; they end
-//                    before those of tile end (where RT > 1)
-//   load_tokens(q)   the lane's chunks of the QW quads from q on, into x
+//   rows_of(t)       the packed rows from which tile t's are counted
+//   load_tokens(q)   starts the loads of the lane's chunks of quad q,
+//   take_tokens()    puts them into x
 //   done(t, n, q, j, sum)  called once for every row group q of tile t and token
 //                    4 n + j, by some thread, with the sum over the waves, added
 //                    in their order
-template <bool ODD, int NG, int QW, int RT, int TB, typename RowsOf, typename LoadTokens, typename Done>
-__device__ __forceinline__ void stream_rows(int begin, int end, int k, const QuadPlan& plan, uint32_t tile_rows,
-                                            const uint32_t (&group_row)[4], Chunk (&x)[QW][1][NG], f32x4* part,
-                                            RowsOf rows_of, LoadTokens load_tokens, Done done) {
-  static_assert(TB % RT == 0, "whole steps in a batch");
+template <bool ODD, int NG, int TB, typename RowsOf, typename LoadTokens, typename TakeTokens, typename Done>
+__device__ __forceinline__ void stream_rows(int begin, int end, int k, const QuadPlan& plan, const uint32_t (&group_row)[4],
+                                            Chunk (&x)[1][NG], f32x4* part, RowsOf rows_of, LoadTokens load_tokens,
+                                            TakeTokens take_tokens, Done done) {
   const int lane = threadIdx.x & 63, b = lane >> 2, i = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = plan.waves, passes = plan.passes;
   constexpr int SLOTS = NG * 16;                     // partial sums of a wave and tile
 
-  RowGroup r[RT][QW][4];
-  // what is loaded: from tile at_t on, pass at_pass of the batch from at_batch on
+  RowGroup r[4];
+  // what is loaded: tile at_t of pass at_pass of the batch from at_batch on
   int at_batch = begin, at_pass = 0, at_t = begin;
   PackedRows next;
-  auto quad = [&](int pass, int z) { return (pass * waves + wave) * QW + z; };
+  LaneAt<ODD> at(i, wave, b, k);
   auto aim = [&]() {
     next = rows_of(min(at_t, end - 1));
-    if (at_t >= end) next.w_bytes = next.s_bytes = 0;
+    if (at_t >= end || (at_pass * waves + wave) * 512 >= k) next.w_bytes = next.s_bytes = 0;
     next = uniform(next);
+    if (passes > 1) at = LaneAt<ODD>(i, at_pass * waves + wave, b, k);
   };
-  // quads past the last one read as zero: their weights' codes are past the buffer
-  auto load = [&](int t, int z, int q) {
-    const int at = quad(at_pass, z);
-    PackedRows rows = next;
-    if (at * 512 >= k) rows.w_bytes = rows.s_bytes = 0;
-    r[t][z][q].load(rows, group_row[q] + t * tile_rows, at, LaneAt<ODD>(i, at, b, k), k);
-  };
+  auto load = [&](int q) { r[q].load(next, group_row[q], at_pass * waves + wave, at, k); };
   auto advance = [&]() {
-    at_t += RT;
-    if (at_t >= min(end, at_batch + TB)) {
+    if (++at_t >= min(end, at_batch + TB)) {
       if (++at_pass == passes) {
         at_pass = 0;
         at_batch += TB;
@@ -333,54 +324,48 @@ __device__ __forceinline__ void stream_rows(int begin, int end, int k, const Qua
     }
     aim();
   };
-  auto tokens = [&](int pass) { load_tokens(quad(pass, 0)); };
+  load_tokens(wave);                                 // first, so that taking them awaits no weights
   aim();
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)                      // in order of use
-#pragma unroll
-      for (int z = 0; z < QW; ++z) load(t, z, (q & 1) * 2 + (q >> 1));
+  for (int q = 0; q < 4; ++q) load((q & 1) * 2 + (q >> 1));          // in order of use
   advance();
-  if (passes == 1) tokens(0);
+  take_tokens();
   for (int batch = begin; batch < end; batch += TB) {
     const int count = min(TB, end - batch);
     for (int pass = 0; pass < passes; ++pass) {
-      if (passes > 1) tokens(pass);
+      if (passes > 1 && (pass || batch > begin)) {
+        load_tokens(pass * waves + wave);
+        __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0): the loop awaits nothing of the tokens
+        take_tokens();
+      }
       f32x4* mine = part + wave * TB * SLOTS;
-      for (int t = 0; t < count; t += RT) {
+      for (int t = 0; t < count; ++t) {
+        f32x4 half[2][NG];                           // groups 0 and 2, groups 1 and 3
 #pragma unroll
-        for (int u = 0; u < RT; ++u) {
-          f32x4 half[2][NG];                         // groups 0 and 2, groups 1 and 3
+        for (int p = 0; p < 2; ++p) {
+          f32x4 acc[2][NG];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            f32x4 acc[2][NG];
+          for (int h = 0; h < 2; ++h) {
+            const int q = p + 2 * h;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int q = p + 2 * h;
-#pragma unroll
-              for (int n = 0; n < NG; ++n) acc[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int z = 0; z < QW; ++z) {
-                multiply_group<NG, 1>(r[u][z][q], x[z], acc[h]);
-                load(u, z, q);
-                __builtin_amdgcn_sched_barrier(0);   // the load goes out here, not where its value is near
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n) half[p][n] = sum_chunks_pair(acc[0][n], acc[1][n]);
+            for (int n = 0; n < NG; ++n) acc[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            multiply_group<NG, 1>(r[q], x, acc[h]);
+            load(q);
+            __builtin_amdgcn_sched_barrier(0);       // the load goes out here, not where its value is near
           }
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            f32x4 v = sum_chunks_rest(half[0][n], half[1][n]);
-            if ((lane & 12) == 0) {
-              f32x4& slot = mine[n * 16 + (lane >> 4) * 4 + i];
-              if (pass) v += slot;
-              slot = v;
-            }
-          }
-          mine += SLOTS;
+          for (int n = 0; n < NG; ++n) half[p][n] = sum_chunks_pair(acc[0][n], acc[1][n]);
         }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          f32x4 v = sum_chunks_rest(half[0][n], half[1][n]);
+          if ((lane & 12) == 0) {
+            f32x4& slot = mine[n * 16 + (lane >> 4) * 4 + i];
+            if (pass) v += slot;
+            slot = v;
+          }
+        }
+        mine += SLOTS;
         advance();
       }
     }
@@ -427,11 +412,8 @@ __device__ __forceinline__ void pieces_to_chunk(Chunk& x, uint8_t* lds) {
   }
 }
 
-// Chunks of packed NVFP4 rows, expanded (without their tensor scale).
-template <bool ODD>
-__device__ __forceinline__ void load_chunk(Chunk& x, const PackedRows& t, uint32_t row, int q, int k) {
-  RowGroup r;
-  r.load(t, 0, q, LaneAt<ODD>(row, q, (threadIdx.x & 63) >> 2, k), k);
+// A chunk of packed NVFP4 values, expanded (without their tensor scale).
+__device__ __forceinline__ void expand_chunk(Chunk& x, const RowGroup& r) {
   const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
   const float s0 = e4m3_f32<0>(r.s), s1 = e4m3_f32<1>(r.s);
 #pragma unroll
