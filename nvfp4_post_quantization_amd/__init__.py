@@ -563,10 +563,13 @@ def scale_sweep_stats(w: torch.Tensor, H: torch.Tensor, scale2: torch.Tensor, st
     return packed, codes, stats
 
 
-def _flat(t: torch.Tensor, dtype, shape, name: str, device=None) -> torch.Tensor:
-    """A contiguous GPU tensor of one dtype and shape, on `device` when given."""
+def _flat(t: torch.Tensor, dtype, shape: tuple, name: str, device=None) -> torch.Tensor:
+    """A contiguous GPU tensor of one dtype and shape, on `device` (a GPU) when given."""
+    if (device is not None and isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return t
     _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor (got {list(t.shape)})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -574,29 +577,46 @@ def _flat(t: torch.Tensor, dtype, shape, name: str, device=None) -> torch.Tensor
 
 
 def _scalar(t: torch.Tensor, name: str, device) -> torch.Tensor:
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.device == device and t.numel() >= 1:
+        return t
     _dev(t, torch.float32, name)
     if t.numel() < 1 or t.device != device:
         raise ValueError(f"{name} must hold one float32 on {device}")
     return t
 
 
-def _rows_out(out: torch.Tensor | None, rows: int, cols: int, device) -> torch.Tensor:
-    """The bf16 [rows, cols] output: made here, or checked."""
+def _rows_out(out: torch.Tensor | None, rows: int, cols: int, device) -> tuple[torch.Tensor, int]:
+    """The bf16 [rows, cols] output, made here or checked, and its row stride."""
     if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device), cols
     _dev(out, torch.bfloat16, "out", 2)
-    if tuple(out.shape) != (rows, cols) or out.device != device:
+    if out.shape != (rows, cols) or out.device != device:
         raise ValueError(f"out must be [{rows}, {cols}] on {device}")
-    return out
+    return out, _row_major(out, "out")
 
 
-def _scratch(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor:
+def _scratch(workspace: torch.Tensor | None, device, need, *sizes) -> torch.Tensor:
+    """The workspace: checked (its size by the library), or made here with need(*sizes) bytes."""
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return torch.empty(max(need(*sizes), 1), dtype=torch.uint8, device=device)
     _dev(workspace, torch.uint8, "workspace")
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {device}")
     return workspace
+
+
+def _call(fn: str, device, *args) -> None:
+    """fn(*args, the device's current stream), with the device made current.
+    The stream's handle comes without the Stream object, whose making is a
+    sixth of a small call (1.9 of 12 us)."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = getattr(load(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(load(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(fn, status)
 
 
 def mxfp4_quantize(x: torch.Tensor, out=None):
@@ -611,9 +631,7 @@ def mxfp4_quantize(x: torch.Tensor, out=None):
     else:
         packed = _flat(out[0], torch.uint8, (rows, k // 2), "packed", x.device)
         e8m0 = _flat(out[1], torch.uint8, (rows, k // 32), "e8m0", x.device)
-    with torch.cuda.device(x.device):
-        _check("mxfp4_quantize", load().mxfp4_quantize(
-            x.data_ptr(), rows, k, ldx, packed.data_ptr(), e8m0.data_ptr(), _stream(x)))
+    _call("mxfp4_quantize", x.device, x.data_ptr(), rows, k, ldx, packed.data_ptr(), e8m0.data_ptr())
     return packed, e8m0
 
 
@@ -621,14 +639,13 @@ def mxfp4_dequant(packed: torch.Tensor, e8m0: torch.Tensor, out: torch.Tensor | 
     """bf16 [rows, k] of MXFP4 (packed u8 [rows, k/2], e8m0 u8 [rows, k/32])."""
     _dev(packed, torch.uint8, "packed", 2)
     rows, k = packed.shape[0], packed.shape[1] * 2
-    _flat(packed, torch.uint8, (rows, k // 2), "packed")
+    _flat(packed, torch.uint8, (rows, k // 2), "packed", packed.device)
     _flat(e8m0, torch.uint8, (rows, k // 32), "e8m0", packed.device)
     if out is None:
         out = torch.empty((rows, k), dtype=torch.bfloat16, device=packed.device)
-    _flat(out, torch.bfloat16, (rows, k), "out", packed.device)
-    with torch.cuda.device(packed.device):
-        _check("mxfp4_dequant", load().mxfp4_dequant(packed.data_ptr(), e8m0.data_ptr(), rows, k, out.data_ptr(),
-                                                     _stream(packed)))
+    else:
+        _flat(out, torch.bfloat16, (rows, k), "out", packed.device)
+    _call("mxfp4_dequant", packed.device, packed.data_ptr(), e8m0.data_ptr(), rows, k, out.data_ptr())
     return out
 
 
@@ -645,16 +662,14 @@ def mxfp4_matmul(x_packed: torch.Tensor, x_e8m0: torch.Tensor, w_packed: torch.T
     _dev(w_packed, torch.uint8, "w_packed", 2)
     dev = x_packed.device
     tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
-    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed")
+    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed", dev)
     _flat(x_e8m0, torch.uint8, (tokens, k // 32), "x_e8m0", dev)
     _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
     _flat(w_e8m0, torch.uint8, (o, k // 32), "w_e8m0", dev)
-    y = _rows_out(out, tokens, o, dev)
-    ws = _scratch(workspace, mxfp4_matmul_workspace_bytes(tokens, o, k), dev)
-    with torch.cuda.device(dev):
-        _check("mxfp4_matmul", load().mxfp4_matmul(
-            x_packed.data_ptr(), x_e8m0.data_ptr(), tokens, k, w_packed.data_ptr(), w_e8m0.data_ptr(), o, y.data_ptr(),
-            _row_major(y, "out"), ws.data_ptr(), ws.numel(), _stream(x_packed)))
+    y, ldy = _rows_out(out, tokens, o, dev)
+    ws = _scratch(workspace, dev, mxfp4_matmul_workspace_bytes, tokens, o, k)
+    _call("mxfp4_matmul", dev, x_packed.data_ptr(), x_e8m0.data_ptr(), tokens, k, w_packed.data_ptr(),
+          w_e8m0.data_ptr(), o, y.data_ptr(), ldy, ws.data_ptr(), ws.numel())
     return y
 
 
@@ -671,17 +686,17 @@ def matmul_w4a16(x: torch.Tensor, w_packed: torch.Tensor, w_codes: torch.Tensor,
     workspace: uint8, at least matmul_workspace_bytes(...) bytes."""
     _dev(x, torch.bfloat16, "x", 2)
     _dev(w_packed, torch.uint8, "w_packed", 2)
+    dev = x.device
     tokens, k = x.shape
     o = w_packed.shape[0]
-    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", x.device)
-    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", x.device)
-    _scalar(w_scale2, "w_scale2", x.device)
-    y = _rows_out(out, tokens, o, x.device)
-    ws = _scratch(workspace, matmul_workspace_bytes(tokens, o, k), x.device)
-    with torch.cuda.device(x.device):
-        _check("nvfp4_matmul_w4a16", load().nvfp4_matmul_w4a16(
-            x.data_ptr(), tokens, k, _row_major(x, "x"), w_packed.data_ptr(), w_codes.data_ptr(), w_scale2.data_ptr(),
-            o, y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(), _stream(x)))
+    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
+    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", dev)
+    _scalar(w_scale2, "w_scale2", dev)
+    y, ldy = _rows_out(out, tokens, o, dev)
+    ws = _scratch(workspace, dev, matmul_workspace_bytes, tokens, o, k)
+    _call("nvfp4_matmul_w4a16", dev, x.data_ptr(), tokens, k, _row_major(x, "x"), w_packed.data_ptr(),
+          w_codes.data_ptr(), w_scale2.data_ptr(), o, y.data_ptr(), ldy, ws.data_ptr(),
+          ws.numel())
     return y
 
 
@@ -695,19 +710,17 @@ def matmul_w4a4(x_packed: torch.Tensor, x_codes: torch.Tensor, x_scale2: torch.T
     _dev(w_packed, torch.uint8, "w_packed", 2)
     dev = x_packed.device
     tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
-    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed")
+    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed", dev)
     _flat(x_codes, torch.uint8, (tokens, k // 16), "x_codes", dev)
     _scalar(x_scale2, "x_scale2", dev)
     _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
     _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", dev)
     _scalar(w_scale2, "w_scale2", dev)
-    y = _rows_out(out, tokens, o, dev)
-    ws = _scratch(workspace, matmul_workspace_bytes(tokens, o, k), dev)
-    with torch.cuda.device(dev):
-        _check("nvfp4_matmul_w4a4", load().nvfp4_matmul_w4a4(
-            x_packed.data_ptr(), x_codes.data_ptr(), x_scale2.data_ptr(), tokens, k, w_packed.data_ptr(),
-            w_codes.data_ptr(), w_scale2.data_ptr(), o, y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(),
-            _stream(x_packed)))
+    y, ldy = _rows_out(out, tokens, o, dev)
+    ws = _scratch(workspace, dev, matmul_workspace_bytes, tokens, o, k)
+    _call("nvfp4_matmul_w4a4", dev, x_packed.data_ptr(), x_codes.data_ptr(), x_scale2.data_ptr(), tokens, k,
+          w_packed.data_ptr(), w_codes.data_ptr(), w_scale2.data_ptr(), o, y.data_ptr(), ldy,
+          ws.data_ptr(), ws.numel())
     return y
 
 
@@ -726,10 +739,8 @@ def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None
     else:
         ids = _flat(out[0], torch.int32, (tokens, top_k), "ids", logits.device)
         wts = _flat(out[1], torch.float32, (tokens, top_k), "weights", logits.device)
-    with torch.cuda.device(logits.device):
-        _check("nvfp4_moe_route", load().nvfp4_moe_route(
-            logits.data_ptr(), tokens, experts, ldl, top_k, int(bool(normalize)), ids.data_ptr(), wts.data_ptr(),
-            _stream(logits)))
+    _call("nvfp4_moe_route", logits.device, logits.data_ptr(), tokens, experts, ldl, top_k, int(bool(normalize)),
+          ids.data_ptr(), wts.data_ptr())
     return ids, wts
 
 
@@ -767,12 +778,10 @@ def moe_forward(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_p
     _flat(w2_packed, torch.uint8, (e, *mid, hidden, inter // 2), "w2_packed", dev)
     _flat(w2_codes, torch.uint8, (e, *mid, hidden, inter // 16), "w2_codes", dev)
     _flat(w2_scale2, torch.float32, (e,), "w2_scale2", dev)
-    y = _rows_out(out, tokens, hidden, dev)
-    ws = _scratch(workspace, moe_workspace_bytes(tokens, top_k, inter), dev)
-    with torch.cuda.device(dev):
-        _check("nvfp4_moe_forward", load().nvfp4_moe_forward(
-            x.data_ptr(), tokens, hidden, _row_major(x, "x"), ids.data_ptr(), weights.data_ptr(), top_k, e, inter,
-            w13_packed.data_ptr(), w13_codes.data_ptr(), w13_scale2.data_ptr(), w2_packed.data_ptr(),
-            w2_codes.data_ptr(), w2_scale2.data_ptr(), y.data_ptr(), _row_major(y, "out"), ws.data_ptr(), ws.numel(),
-            _stream(x)))
+    y, ldy = _rows_out(out, tokens, hidden, dev)
+    ws = _scratch(workspace, dev, moe_workspace_bytes, tokens, top_k, inter)
+    _call("nvfp4_moe_forward", dev, x.data_ptr(), tokens, hidden, _row_major(x, "x"), ids.data_ptr(),
+          weights.data_ptr(), top_k, e, inter, w13_packed.data_ptr(), w13_codes.data_ptr(), w13_scale2.data_ptr(),
+          w2_packed.data_ptr(), w2_codes.data_ptr(), w2_scale2.data_ptr(), y.data_ptr(), ldy,
+          ws.data_ptr(), ws.numel())
     return y

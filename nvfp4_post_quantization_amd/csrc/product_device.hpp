@@ -529,6 +529,8 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
         for (int u = 0; u < 4; ++u) x[z][n].load_unit(u, tokens[n], token_row[n], q, g, k);
         x[z][n].load_scales(tokens[n], token_row[n], q, g, k);
       }
+  };
+  auto take_tokens = [&](int pass) {
 #pragma unroll
     for (int z = 0; z < QW; ++z)
 #pragma unroll
@@ -539,8 +541,8 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
         for (int u = 0; u < 4; ++u)
           if (left <= u * 128) x[z][n].w[u] = make_uint4(0, 0, 0, 0);
       }
-    __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0): the loop awaits nothing of the tokens
   };
+  load_tokens(0);                                    // first, so that taking them awaits no weights
   aim();
 #pragma unroll
   for (int t = 0; t < RT; ++t)
@@ -551,11 +553,15 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
       for (int u = 0; u < 4; ++u) load_unit(t, z, u);
     }
   advance();
-  if (passes == 1) load_tokens(0);
+  take_tokens(0);
   for (int batch = begin; batch < end; batch += TB) {
     const int count = min(TB, end - batch);
     for (int pass = 0; pass < passes; ++pass) {
-      if (passes > 1) load_tokens(pass);
+      if (passes > 1 && (pass || batch > begin)) {
+        load_tokens(pass);
+        __builtin_amdgcn_s_waitcnt(0x0F70);          // vmcnt(0): the loop awaits nothing of the tokens
+        take_tokens(pass);
+      }
       f32x4* mine = part + wave * TB * NT * 64 + lane;
       for (int t = 0; t < count; t += RT) {
 #pragma unroll
