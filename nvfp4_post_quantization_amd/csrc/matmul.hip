@@ -66,9 +66,10 @@ template <int KIND, bool ODD, int NG, int CU, int MW>
 __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a) {
   constexpr int TB = 4;
   __shared__ f32x4 part[MW * TB * NG * 16];
-  __shared__ __attribute__((aligned(16))) uint8_t stage[KIND == kW4A16 ? MW * 4096 : 16];
+  constexpr int STAGE = KIND == kW4A16 ? 4096 : 1024;      // of a wave: tokens, then weights, change their order there
+  __shared__ __attribute__((aligned(16))) uint8_t stage[MW * STAGE];
   const int lane = threadIdx.x & 63, j = lane & 3;
-  const int wave = threadIdx.x >> 6;
+  uint8_t* const lds_wave = stage + (threadIdx.x >> 6) * STAGE;
   const int tok0 = blockIdx.y * 4 * NG;
   const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 4;
   int begin, end;
@@ -84,29 +85,29 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
   auto load_tokens = [&](int q) {
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      const int t0 = min(tok0 + 4 * n, a.tokens - 1), t = min(j, a.tokens - 1 - t0);        // others are not stored
+      const int t0 = min(tok0 + 4 * n, a.tokens - 1), last = a.tokens - 1 - t0;               // others are not stored
       if constexpr (KIND == kW4A16) {
-        load_pieces(x[0][n], a.xp + (int64_t)(t0 + t) * a.ldx, q, a.k);
+        load_pieces(x[0][n], a.xp + (int64_t)(t0 + min(j, last)) * a.ldx, q, a.k);
       } else {
         const uint32_t rows = q * 512 < a.k ? min(4, a.tokens - t0) : 0;
         packed[n].load(PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds}, 0, q,
-                       LaneAt<ODD>(t, q, lane >> 2, a.k), a.k);
+                       LaneAt<ODD>(min(lane >> 4, last), q, a.k), a.k);
       }
     }
   };
   auto take_tokens = [&]() {
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      if constexpr (KIND == kW4A16) pieces_to_chunk(x[0][n], stage + wave * 4096);
-      else expand_chunk(x[0][n], packed[n]);
+      if constexpr (KIND == kW4A16) pieces_to_chunk(x[0][n], lds_wave);
+      else expand_chunk(x[0][n], packed[n].arranged(lds_wave));
     }
   };
   auto done = [&](int t, int n, int q, int tj, f32x4 v) {
     const int row = t * 16 + q * 4, tok = tok0 + 4 * n + tj;
     if (tok < a.tokens && row < a.out) store_rows<KIND>(a, row, tok, v);
   };
-  stream_rows<ODD, NG, TB>(begin, end, a.k, quad_plan<1>(a.k, CU), group_row, x, part, rows_of, load_tokens, take_tokens,
-                           done);
+  stream_rows<ODD, NG, TB>(begin, end, a.k, quad_plan<1>(a.k, CU), group_row, x, part, lds_wave, rows_of, load_tokens,
+                           take_tokens, done);
 }
 
 // 16 NT tokens against MXFP4 rows.

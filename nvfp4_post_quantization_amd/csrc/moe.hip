@@ -184,7 +184,8 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
     if ((t + 1) * CH == a.inter && q == 0)           // the rest of the row's last quad
       for (int ch = a.inter; ch < a.ldh; ch += 4) put(ch, make_uint2(0, 0), make_uint2(0, 0));
   };
-  stream_rows<ODD, NG, 4>(t0, t1, a.hidden, plan, group_row, x, part, rows_of, load_tokens, take_tokens, done);
+  stream_rows<ODD, NG, 4>(t0, t1, a.hidden, plan, group_row, x, part, stage + wave * 4096, rows_of, load_tokens, take_tokens,
+                           done);
 }
 
 // h of a run of (job, 8 channels) pieces of work, as many runs as there are
@@ -233,6 +234,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
   constexpr int ROWS = 4 * kDownGroups;
   __shared__ Routing r;
   __shared__ __attribute__((aligned(16))) float sums[kDownWaves * kMoeMaxTokens * ROWS];   // [wave][tokens][32]
+  __shared__ __attribute__((aligned(16))) uint8_t turn[kDownWaves][1024];          // weights change their order there
   const int lane = threadIdx.x & 63, b = lane >> 2, j = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int each = a.tokens * ROWS;
@@ -274,7 +276,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
         d[p][0][4 * m + 3] = v.w;
       }
   };
-  auto load_w = [&](int q) { w[q].load(next, 4 * q, next_q, LaneAt<ODD>(j, next_q, b, a.inter), a.inter); };
+  auto load_w = [&](int q) { w[q].load(next, 4 * q, next_q, LaneAt<ODD>(lane >> 4, next_q, a.inter), a.inter); };
   auto step = [&](int i, const Chunk (&x)[2][1], Chunk (&x_next)[2][1]) {
     const int job = i / quads;
     aim(i + kDownWaves);
@@ -283,9 +285,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
 #pragma unroll
     for (int q = 0; q < kDownGroups; ++q) {
       acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-      multiply_group<1, 2>(w[q], x, acc[q]);
+      const RowGroup r = w[q].arranged(turn[wave]);
       load_w(q);
       __builtin_amdgcn_sched_barrier(0);             // the load goes out here, not where its value is near
+      multiply_group<1, 2>(r, x, acc[q]);
     }
     const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job];
     const uint64_t mask = tokens_of(r, e);

@@ -133,14 +133,19 @@ __host__ __device__ inline QuadPlan quad_plan(int64_t k, int most) {
 }
 
 // NVFP4 weights against 4 NG tokens on the 4x4x4 matrix instruction, whose 16
-// blocks are 16 chunks of 32 channels: lane 4 b + i holds chunk b of row i of a
-// group of four rows (a load instruction reads 256 contiguous bytes of each) or
-// of token i of a group of four tokens.  A block of 16 weights is four
-// instructions; its scale then multiplies their fp32 sum, so that the weights
-// enter as plain E2M1 values, one conversion for two of them.  Per 1 KiB of
-// weights that is 27 vector and 8 matrix instructions for up to four tokens;
-// the 16x16x32 instruction, which needs the scales in the weights, took 132 and
-// held the expert layer to 3.6 TB/s.
+// blocks are 16 chunks of 32 channels: lane 4 b + i works on chunk b of row i of
+// a group of four rows, or of token i of a group of four tokens.  A block of 16
+// weights is four instructions; its scale then multiplies their fp32 sum, so
+// that the weights enter as plain E2M1 values, one conversion for two of them.
+// Per 1 KiB of weights that is 27 vector and 8 matrix instructions for up to
+// four tokens; the 16x16x32 instruction, which needs the scales in the weights,
+// took 132 and held the expert layer to 3.6 TB/s.
+//
+// Memory is read by lane 16 i + b instead, so that neighbouring lanes read
+// neighbouring pieces: a load of 16 bytes a lane looks up a cache line for every
+// four lanes that share one, and for every lane that does not (80 lookups a KiB
+// the one way, 20 the other, one a cycle).  A trip through a KiB of LDS of the
+// wave's own exchanges the two orders.
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -153,8 +158,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 template <bool ODD>
 struct LaneAt {
   uint32_t w, s, s1;
-  __device__ __forceinline__ LaneAt(uint32_t row, int q, int b, int k) {
-    const int left = k - q * 512 - b * 32;
+  // row: the lane's (lane / 16, or the last one there is)
+  __device__ __forceinline__ LaneAt(uint32_t row, int q, int k) {
+    const int b = threadIdx.x & 15, left = k - q * 512 - b * 32;
     w = row * ((uint32_t)k >> 1) + b * 16;
     s = row * ((uint32_t)k >> 4) + b * 2;
     s1 = ODD && left > 16 ? s + 1 : kBeyond;
@@ -184,6 +190,21 @@ struct RowGroup {
       const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b8(bs, (int)at.s1, (int)os, 0);
       s = lo | hi << 8;
     }
+  }
+
+  // From the order of loading to that of the matrix instruction.  In lds (1 KiB)
+  // piece i of chunk b is at 64 b + 16 (i', with bits of b): both sides then
+  // touch every bank once.
+  __device__ __forceinline__ RowGroup arranged(uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
+    auto place = [](int b, int i) { return b * 64 + (((b >> 2) ^ (0x9C >> (2 * i) & 3)) << 4); };
+    *reinterpret_cast<uint4*>(lds + place(lane & 15, lane >> 4)) = w;
+    __builtin_amdgcn_wave_barrier();
+    RowGroup r;
+    r.w = *reinterpret_cast<const uint4*>(lds + place(lane >> 2, lane & 3));
+    r.s = (uint32_t)__builtin_amdgcn_ds_bpermute(((lane & 3) << 4 | lane >> 2) << 2, (int)s);
+    __builtin_amdgcn_wave_barrier();
+    return r;
   }
 };
 
@@ -286,7 +307,8 @@ __device__ __forceinline__ f32x4 sum_chunks_rest(const f32x4& a, const f32x4& b)
 // Row tiles begin .. end - 1 (four groups of four rows) against 4 NG tokens, by
 // a workgroup dealt out as in plan, a quad a wave and pass.  TB tiles make a
 // batch, whose partial sums the waves leave in `part` (per wave TB * NG * 16).
-//   group_row[q]     the first row of group q in a tile (the lane's: + lane % 4)
+//   group_row[q]     the first row of group q in a tile
+//   lds              1 KiB of the wave's
 //   rows_of(t)       the packed rows from which tile t's are counted
 //   load_tokens(q)   starts the loads of the lane's chunks of quad q,
 //   take_tokens()    puts them into x
@@ -295,9 +317,9 @@ __device__ __forceinline__ f32x4 sum_chunks_rest(const f32x4& a, const f32x4& b)
 //                    in their order
 template <bool ODD, int NG, int TB, typename RowsOf, typename LoadTokens, typename TakeTokens, typename Done>
 __device__ __forceinline__ void stream_rows(int begin, int end, int k, const QuadPlan& plan, const uint32_t (&group_row)[4],
-                                            Chunk (&x)[1][NG], f32x4* part, RowsOf rows_of, LoadTokens load_tokens,
-                                            TakeTokens take_tokens, Done done) {
-  const int lane = threadIdx.x & 63, b = lane >> 2, i = lane & 3;
+                                            Chunk (&x)[1][NG], f32x4* part, uint8_t* lds, RowsOf rows_of,
+                                            LoadTokens load_tokens, TakeTokens take_tokens, Done done) {
+  const int lane = threadIdx.x & 63, i = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = plan.waves, passes = plan.passes;
   constexpr int SLOTS = NG * 16;                     // partial sums of a wave and tile
@@ -306,12 +328,12 @@ __device__ __forceinline__ void stream_rows(int begin, int end, int k, const Qua
   // what is loaded: tile at_t of pass at_pass of the batch from at_batch on
   int at_batch = begin, at_pass = 0, at_t = begin;
   PackedRows next;
-  LaneAt<ODD> at(i, wave, b, k);
+  LaneAt<ODD> at(lane >> 4, wave, k);
   auto aim = [&]() {
     next = rows_of(min(at_t, end - 1));
     if (at_t >= end || (at_pass * waves + wave) * 512 >= k) next.w_bytes = next.s_bytes = 0;
     next = uniform(next);
-    if (passes > 1) at = LaneAt<ODD>(i, at_pass * waves + wave, b, k);
+    if (passes > 1) at = LaneAt<ODD>(lane >> 4, at_pass * waves + wave, k);
   };
   auto load = [&](int q) { r[q].load(next, group_row[q], at_pass * waves + wave, at, k); };
   auto advance = [&]() {
@@ -349,9 +371,10 @@ __device__ __forceinline__ void stream_rows(int begin, int end, int k, const Qua
             const int q = p + 2 * h;
 #pragma unroll
             for (int n = 0; n < NG; ++n) acc[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-            multiply_group<NG, 1>(r[q], x, acc[h]);
+            const RowGroup w = r[q].arranged(lds);
             load(q);
             __builtin_amdgcn_sched_barrier(0);       // the load goes out here, not where its value is near
+            multiply_group<NG, 1>(w, x, acc[h]);
           }
 #pragma unroll
           for (int n = 0; n < NG; ++n) half[p][n] = sum_chunks_pair(acc[0][n], acc[1][n]);
