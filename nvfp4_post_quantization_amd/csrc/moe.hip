@@ -31,7 +31,7 @@ struct MoeArgs {
   const float *s13, *s2;
   uint16_t* y;
   int64_t ldy;
-  uint16_t* h;                    // [pairs][ldh] bf16, then the same for the low parts
+  uint16_t* h;                    // [groups of four tokens][ldh][4] bf16 (see place_of), then the low parts
   int64_t ldh;                    // inter rounded up to whole quads, zero past inter
   int64_t lo;                     // bytes from a value's high part to its low part
   int tokens, hidden, inter, experts, top_k;
@@ -41,9 +41,9 @@ struct MoeArgs {
 struct Routing {
   uint32_t mask[kMoeMaxExperts][2];       // tokens of an expert
   uint16_t expert[kMaxJobs];              // by job: its expert, experts in ascending order,
-  uint16_t base[kMaxJobs];                // its first pair (rows of h),
+  uint16_t base[kMaxJobs];                // its first group of four tokens (of h),
   uint8_t first[kMaxJobs];                // its first token's place among the expert's
-  uint32_t part[16];                      // per wave: jobs and pairs (upper half)
+  uint32_t part[16];                      // per wave: jobs and groups (upper half)
   int jobs;
 };
 
@@ -56,19 +56,20 @@ template <int JOB>
 __device__ __forceinline__ void read_routing(Routing& r, const MoeArgs& a) {
   const int threads = blockDim.x, per = (kMoeMaxExperts + threads - 1) / threads;
   const int n = a.tokens * a.top_k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e0 = tid < n ? a.ids[tid] : -1;                // on its way while the masks are cleared
   for (int i = tid; i < 2 * a.experts; i += threads) (&r.mask[0][0])[i] = 0;
   __syncthreads();
   for (int i = tid; i < n; i += threads) {
-    const int e = a.ids[i], t = i / a.top_k;
+    const int e = i == tid ? e0 : a.ids[i], t = i / a.top_k;
     if (e >= 0 && e < a.experts) atomicOr(&r.mask[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
   // prefix sums over the experts, `per` of them a thread: jobs in the lower half
-  // of the word, pairs (at most 1024) in the upper
+  // of the word, groups of four tokens (at most 1024) in the upper
   auto own = [&](int i) {
     const int e = tid * per + i;
     const uint32_t c = e < a.experts ? __popc(r.mask[e][0]) + __popc(r.mask[e][1]) : 0;
-    return (c + JOB - 1) / JOB | c << 16;
+    return (c + JOB - 1) / JOB | (c + 3) / 4 << 16;
   };
   uint32_t sum = 0;
   for (int i = 0; i < per; ++i) sum += own(i);
@@ -91,7 +92,7 @@ __device__ __forceinline__ void read_routing(Routing& r, const MoeArgs& a) {
     for (int q = 0; q < (int)(mine & 0xFFFF); ++q) {
       const int job = (before & 0xFFFF) + q;
       r.expert[job] = (uint16_t)(tid * per + i);
-      r.base[job] = (uint16_t)((before >> 16) + JOB * q);
+      r.base[job] = (uint16_t)((before >> 16) + JOB / 4 * q);
       r.first[job] = (uint8_t)(JOB * q);
     }
     before += mine;
@@ -121,11 +122,12 @@ __device__ __forceinline__ float weight_of(const MoeArgs& a, int t, int e) {
   return w;
 }
 
-// Where channel c of a row of h is kept: within each quad (512 channels) in the
-// order in which the second launch's lanes read them, piece m (8 channels) of
-// the 16 chunks of 32 next to each other.
-__device__ __forceinline__ int place_of(int c) {
-  return (c & ~511) | ((c >> 3) & 3) << 7 | ((c >> 5) & 15) << 3 | (c & 7);
+// Where channel c of token j of a group of four is kept in the group's part of
+// h: within each quad (512 channels) in the order in which the second launch's
+// lanes read them, 16 bytes a lane: piece m (8 channels) of the 16 chunks of 32
+// next to each other, the four tokens' pieces next to each other.
+__device__ __forceinline__ int place_of(int c, int j) {
+  return (c & ~511) << 2 | ((c >> 3) & 3) << 9 | ((c >> 5) & 15) << 5 | j << 3 | (c & 7);
 }
 
 // h of 4 NG tokens (tok: the lane's of each four) of a job, for row tiles
@@ -173,9 +175,9 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
       hi[z] = to_bf16(h);                            // two bf16 parts keep 16 significant bits of h
       lo[z] = to_bf16(h - bf16_to_f32(hi[z]));
     }
-    uint16_t* row_h = a.h + (int64_t)(base + col) * a.ldh;
+    uint16_t* group_h = a.h + (int64_t)(base + col / 4) * a.ldh * 4;
     auto put = [&](int ch, uint2 high, uint2 low) {
-      uint8_t* dst = reinterpret_cast<uint8_t*>(row_h + place_of(ch));
+      uint8_t* dst = reinterpret_cast<uint8_t*>(group_h + place_of(ch, col & 3));
       *reinterpret_cast<uint2*>(dst) = high;
       *reinterpret_cast<uint2*>(dst + a.lo) = low;
     };
@@ -221,21 +223,20 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
   }
 }
 
-// 32 output channels for all tokens.  The (job, quad of its channels) steps, a
+// ROWS output channels for all tokens.  The (job, quad of its channels) steps, a
 // job being up to four tokens of an expert, are dealt to the waves, and a wave
 // loads the next step's weights and h as it uses the current one's.  A product
 // has a column for each token of the job, added to the token's sums in the
 // wave's own part of LDS, step after step.  The waves are added at the end.
-constexpr int kDownGroups = 8;            // row groups of 4
 constexpr int kDownWaves = 8;
 
-template <bool ODD>
+template <bool ODD, int GROUPS>           // row groups of four
 __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a) {
-  constexpr int ROWS = 4 * kDownGroups;
+  constexpr int ROWS = 4 * GROUPS;
   __shared__ Routing r;
-  __shared__ __attribute__((aligned(16))) float sums[kDownWaves * kMoeMaxTokens * ROWS];   // [wave][tokens][32]
+  __shared__ __attribute__((aligned(16))) float sums[kDownWaves * kMoeMaxTokens * ROWS];   // [wave][tokens][ROWS]
   __shared__ __attribute__((aligned(16))) uint8_t turn[kDownWaves][1024];          // weights change their order there
-  const int lane = threadIdx.x & 63, b = lane >> 2, j = lane & 3;
+  const int lane = threadIdx.x & 63, j = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int each = a.tokens * ROWS;
   for (int i = threadIdx.x; i < kDownWaves * each; i += 64 * kDownWaves) sums[i] = 0.f;
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
   const uint32_t rows = min(ROWS, a.hidden - row0);
   float* mine = sums + wave * each;
 
-  RowGroup w[kDownGroups];
+  RowGroup w[GROUPS];
   Chunk h[2][1], h_next[2][1];            // high and low parts
   PackedRows next{};
   const uint8_t* next_h = nullptr;
@@ -258,18 +259,17 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
     const int job = i / quads;
     next_q = i - job * quads;
     const int e = __builtin_amdgcn_readfirstlane(r.expert[job]);
-    const int count = min(4, __popcll(tokens_of(r, e)) - r.first[job]);
     const int64_t row = (int64_t)e * a.hidden + row0;
     next = uniform(PackedRows{a.p2 + row * ldw, a.c2 + row * lds, there ? rows * ldw : 0, there ? rows * lds : 0});
-    next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)(r.base[job] + min(j, count - 1)) * a.ldh * 2 +
-             next_q * 1024 + b * 16;
+    // (a group's tokens past the last one hold anything: their columns are not added)
+    next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)job * a.ldh * 8 + next_q * 4096 + lane * 16;
   };
   auto load_h = [&](Chunk (&d)[2][1]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const uint4 v = global_load16(next_h + (p ? a.lo : 0) + m * 256);
+        const uint4 v = global_load16(next_h + (p ? a.lo : 0) + m * 1024);
         d[p][0][4 * m] = v.x;
         d[p][0][4 * m + 1] = v.y;
         d[p][0][4 * m + 2] = v.z;
@@ -281,10 +281,11 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
     const int job = i / quads;
     aim(i + kDownWaves);
     load_h(x_next);
-    f32x4 acc[kDownGroups][1];
+    f32x4 acc[8][1];
 #pragma unroll
-    for (int q = 0; q < kDownGroups; ++q) {
-      acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < 8; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
       const RowGroup r = w[q].arranged(turn[wave]);
       load_w(q);
       __builtin_amdgcn_sched_barrier(0);             // the load goes out here, not where its value is near
@@ -294,18 +295,21 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
     const uint64_t mask = tokens_of(r, e);
     const int tok = token_of_place(mask, first + j);
     const f32x4 v0 = sum_chunks_rest(sum_chunks_pair(acc[0][0], acc[2][0]), sum_chunks_pair(acc[1][0], acc[3][0]));
-    const f32x4 v1 = sum_chunks_rest(sum_chunks_pair(acc[4][0], acc[6][0]), sum_chunks_pair(acc[5][0], acc[7][0]));
+    f32x4 v1;
+    if constexpr (GROUPS > 4)
+      v1 = sum_chunks_rest(sum_chunks_pair(acc[4][0], acc[6][0]), sum_chunks_pair(acc[5][0], acc[7][0]));
     if ((lane & 12) == 0 && j < __popcll(mask) - first) {
-      f32x4* dst = reinterpret_cast<f32x4*>(mine + tok * ROWS + 4 * (lane >> 4));
+      f32x4* dst = reinterpret_cast<f32x4*>(mine + tok * ROWS) + (lane >> 4);
       dst[0] += v0;
-      dst[4] += v1;
+      if constexpr (GROUPS > 4)
+        if (4 + (lane >> 4) < GROUPS) dst[4] += v1;
     }
   };
   if (wave < steps) {
     aim(wave);
     load_h(h);
 #pragma unroll
-    for (int q = 0; q < kDownGroups; ++q) load_w(q);
+    for (int q = 0; q < GROUPS; ++q) load_w(q);
     for (int i = wave; i < steps; i += 2 * kDownWaves) {
       step(i, h, h_next);
       if (i + kDownWaves < steps) step(i + kDownWaves, h_next, h);
@@ -326,6 +330,29 @@ void launch_up(const MoeArgs& a, unsigned grid, int waves, hipStream_t s) {
   if (waves <= 4) moe_up_kernel<ODD, 4><<<grid, 64 * waves, 0, s>>>(a);
   else if (waves <= 8) moe_up_kernel<ODD, 8><<<grid, 64 * waves, 0, s>>>(a);
   else moe_up_kernel<ODD, 16><<<grid, 64 * waves, 0, s>>>(a);
+}
+
+// Output channels of a workgroup: those with which the busiest CU has the
+// fewest to do, among 16 to 32 (more of them read h less often).
+template <bool ODD>
+int launch_down(const MoeArgs& a, hipStream_t s) {
+  int groups = 8, least = 0;
+  for (int g = 8; g >= 4; --g) {
+    const int n = (a.hidden + 4 * g - 1) / (4 * g), busiest = (n + kCus - 1) / kCus * g;
+    if (g == 8 || busiest < least) {
+      least = busiest;
+      groups = g;
+    }
+  }
+  const unsigned grid = (unsigned)((a.hidden + 4 * groups - 1) / (4 * groups));
+  switch (groups) {
+    case 4: moe_down_kernel<ODD, 4><<<grid, 64 * kDownWaves, 0, s>>>(a); break;
+    case 5: moe_down_kernel<ODD, 5><<<grid, 64 * kDownWaves, 0, s>>>(a); break;
+    case 6: moe_down_kernel<ODD, 6><<<grid, 64 * kDownWaves, 0, s>>>(a); break;
+    case 7: moe_down_kernel<ODD, 7><<<grid, 64 * kDownWaves, 0, s>>>(a); break;
+    default: moe_down_kernel<ODD, 8><<<grid, 64 * kDownWaves, 0, s>>>(a); break;
+  }
+  return launch_status("moe_down_kernel");
 }
 
 // One wave per token.  Lane l holds the logits of experts l, l + 64, ...;
@@ -389,7 +416,8 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const float* __restrict_
 static int64_t moe_ldh(int64_t inter) { return (inter + 511) / 512 * 512; }
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
-  return 2 * ((size_t)(tokens * top_k) * (size_t)moe_ldh(inter) * 2);
+  // groups of four tokens: as many as pairs where no two tokens share an expert
+  return 2 * ((size_t)(tokens * top_k) * 4 * (size_t)moe_ldh(inter) * 2);
 }
 
 int launch_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
@@ -438,10 +466,7 @@ int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_
   else launch_up<true>(a, grid, waves, s);
   const int st = launch_status("moe_up_kernel");
   if (st) return st;
-  const unsigned rows = (unsigned)((hidden + 4 * kDownGroups - 1) / (4 * kDownGroups));
-  if (inter % 32 == 0) moe_down_kernel<false><<<rows, 64 * kDownWaves, 0, s>>>(a);
-  else moe_down_kernel<true><<<rows, 64 * kDownWaves, 0, s>>>(a);
-  return launch_status("moe_down_kernel");
+  return inter % 32 == 0 ? launch_down<false>(a, s) : launch_down<true>(a, s);
 }
 
 }  // namespace nvfp4
