@@ -101,7 +101,7 @@ int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, i
 int launch_mxfp4_matmul(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp,
                         const uint8_t* we, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);
 // the tile kernels behind them (matmul_tile.hip)
-bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes);
+bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, int64_t ldx_bytes);
 size_t tile_product_workspace(int64_t tokens, int64_t out, int64_t k, bool mx);
 int launch_tile_mx(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t k, const uint8_t* wp, const uint8_t* we,
                    int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);

@@ -6,6 +6,11 @@
 // takes a run of row tiles; its waves split the channels, hold their part of
 // the tokens in registers and stream the rows' packed weights past them from
 // HBM.  The waves' partial sums meet in LDS and are added in wave order.
+// 12288x4096, weights 28 MB (MXFP4 27): W4A16 8.3 us for one token (3.4 TB/s of
+// weights), 10.6 for five, 15.1 for 16; MXFP4 8.2, 8.2 and 9.0; 28672x8192, one
+// W4A16 token: 26 us (5.0 TB/s).  What is left at the small end is a launch, one
+// trip to memory and the sum over the waves; at the large end, 55 vector
+// instructions a KiB keep the SIMDs busy for over 60% of the time.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -164,10 +169,16 @@ int run_few_mx(const ProductArgs& a, hipStream_t s) {
 template <int KIND>
 int run(const ProductArgs& a, hipStream_t s) {
   if constexpr (KIND == kMX) {
+    // Two row tiles a step and 8 waves where those hold the channels, else two
+    // quads a wave: 12288x4096, one token: 8.2 us, 9.5 with one tile and 16 waves.
     const bool narrow = a.k <= 4096;
     if (a.tokens <= 16) return narrow ? run_few_mx<1, 1, 2, 8>(a, s) : run_few_mx<1, 2, 1, 12>(a, s);
     return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
   } else {
+    // Tokens a workgroup: what their registers leave of the waves that share a
+    // CU counts.  4096x12288: one token takes 10.1 us with 4 and 16 waves; five
+    // 13.8 with 8 and 16, 14.7 with two quads a wave and 12; sixteen 22.9 with 16
+    // and 8, 34 as two workgroups of 8 tokens.  k off 32 has few uses: two sizes.
     if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s) : run_few<KIND, true, 4, 8>(a, s);
     if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s);
     if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s);
@@ -182,7 +193,7 @@ int run(const ProductArgs& a, hipStream_t s) {
 // weights, which are read again for every 16 tokens: 16 tokens take 22.9 us
 // here and 22.5 in tiles (12288x4096: 15.2 and 21), 32 take 40 and 22.5.
 static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
-  return tokens > (mx ? 32 : 16) && tile_product_fits(tokens, out, k, mx, ldx_bytes);
+  return tokens > (mx ? 32 : 16) && tile_product_fits(tokens, out, k, ldx_bytes);
 }
 
 size_t product_workspace_bytes(int64_t tokens, int64_t out, int64_t k, bool mx) {

@@ -750,12 +750,10 @@ TileArgs tile_args(const Plan& p, const PrepArgs& q, int64_t tokens, int64_t out
 
 }  // namespace
 
-// Byte offsets inside a tile's rows and inside the scale words stay below 2^31.
-bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
+// Byte offsets inside a tile's rows, and the number of tiles, stay below 2^31.
+bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, int64_t ldx_bytes) {
   const int64_t lim = INT64_C(1) << 31;
-  const int64_t steps = (k + (mx ? 127 : 63)) / (mx ? 128 : 64);
-  return 256 * ldx_bytes < lim && 256 * k < lim && steps * (out + 255) * 4 < lim && steps * (tokens + 255) * 4 < lim &&
-         (out + 127) / 128 * ((tokens + 127) / 128) < lim / 64;
+  return 256 * ldx_bytes < lim && 256 * k < lim && (out + 127) / 128 * ((tokens + 127) / 128) < lim / 64;
 }
 
 size_t tile_product_workspace(int64_t tokens, int64_t out, int64_t k, bool mx) {

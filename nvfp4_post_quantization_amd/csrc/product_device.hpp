@@ -7,6 +7,8 @@
 //           and lies in [2^-10, 2688], so it is exact in bf16.
 //   kW4A4   both NVFP4.  e2m1 * e4m3 is exact in fp16 as well, and fp16 is
 //           cheaper to make: one convert and one packed multiply per pair.
+//           (With few tokens the weights enter as e2m1 alone, exact in either,
+//           and e4m3 multiplies the fp32 sums of 16.)
 //   kMX     both MXFP4: the scaled FP4 matrix instruction takes the packed
 //           nibbles and E8M0 bytes as they are.
 // The tensor scales (scale_2) stay out of the sum and multiply the fp32
@@ -23,11 +25,9 @@ enum ProductKind { kW4A16 = 0, kW4A4 = 1, kMX = 2 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef __fp16 fp16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
@@ -58,20 +58,7 @@ __device__ __forceinline__ uint4 fp4x8_f16(uint32_t w, f16x2 s) {
 }
 __device__ __forceinline__ f16x2 splat_f16(float s) { return f16x2{(_Float16)s, (_Float16)s}; }
 
-__device__ __forceinline__ f32x4 mfma_bf16(uint4 a, uint4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                 0);
-}
-__device__ __forceinline__ f32x4 mfma_f16(uint4 a, uint4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma_mx(uint4 a, uint32_t sa, uint4 b, uint32_t sb, f32x4 c) {
-  const i32x8 va = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const i32x8 vb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// Two fp32 to bf16, nearest even.
+// fp32 to bf16, nearest even.
 __device__ __forceinline__ uint16_t to_bf16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
@@ -80,10 +67,10 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
 //
 // The weights are read once and everything else is small, so what matters is
 // that loads are in flight all the time.  Loads return in order: a wait for one
-// is a wait for all before it.  So the tokens stay in registers, a quad (512
-// channels) of them a wave, while the rows go by, and the loop loads nothing
-// but weights and their scales, each register again as soon as it has been
-// used.  One wave issues a vector instruction every 8 cycles, four waves of a
+// is a wait for all before it.  So the tokens, loaded first, stay in registers,
+// a quad (512 channels) of them a wave, while the rows go by, and the loop loads
+// nothing but weights and their scales, each register again as soon as it has
+// been used.  One wave issues a vector instruction every 8 cycles, four waves of a
 // SIMD one every 3 to 5 between them, so up to 16 waves share a CU.
 
 constexpr int kCuWaves = 16;

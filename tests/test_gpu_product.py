@@ -201,6 +201,48 @@ def test_product_half_chunk_rows(kind, tokens, out, k):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tokens", [3, 6, 12, 16, 24])
+def test_product_few_tokens_many_channels(kind, tokens):
+    """More channels than the waves of a workgroup hold at a time, the last
+    ones a part of a wave's share."""
+    for out, k in ((70, 12320), (33, 8224), (4100, 8704)):
+        note(f"{kind} tokens={tokens} out={out} k={k}")
+        c = Case(kind, np.random.default_rng(tokens + out), tokens, out, k)
+        c.check(c.fn(*c.args, workspace=c.workspace(0xFF)))
+    if kind != "mx":
+        note(f"{kind} tokens={tokens} k=8208")
+        c = Case(kind, np.random.default_rng(tokens), tokens, 90, 8208)
+        c.check(c.fn(*c.args, workspace=c.workspace(0xFF)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tokens,out,k", [(300, 13000, 320), (300, 13000, 416), (130, 140, 4992), (70, 260, 20000),
+                                          (40, 1000, 128), (200, 2050, 1152)])
+def test_product_small_tiles(kind, tokens, out, k):
+    """Tiles that share a CU, and channels split into parts of unequal length."""
+    note(f"{kind} tokens={tokens} out={out} k={k}")
+    c = Case(kind, np.random.default_rng(tokens + k), tokens, out, k)
+    c.check(c.fn(*c.args, workspace=c.workspace(0xFF)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_product_two_streams(kind):
+    note(f"{kind} two streams")
+    a, b = (Case(kind, np.random.default_rng(i), t, 2000, 2048) for i, t in ((1, 5), (2, 150)))
+    want = [c.fn(*c.args).clone() for c in (a, b)]
+    ws = [c.workspace(0xFF) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for c, w, s in zip((a, b), ws, streams):
+            with torch.cuda.stream(s):
+                got.append(c.fn(*c.args, workspace=w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_product_no_tokens(kind):
     note(f"{kind} no tokens")
     c = Case(kind, np.random.default_rng(0), 1, 16, 64)
@@ -392,6 +434,16 @@ def test_layer(tokens, hidden, inter, experts, top_k, px):
     assert bool((buf[0] == 5).all()) and bool((buf[-1] == 5).all()) and bool((buf[:, hidden:] == 5).all())
     again = L.run(workspace=L.workspace(0x3C))
     assert torch.equal(again.view(torch.int16), y.contiguous().view(torch.int16))
+
+
+# Every number of output rows a workgroup takes, and more channels than the
+# waves of a workgroup hold at a time.
+@pytest.mark.parametrize("hidden,inter", [(4112, 48), (5152, 32), (6160, 544), (7184, 32), (8704, 32), (9232, 16)])
+def test_layer_wide(hidden, inter):
+    for tokens in (2, 5):
+        note(f"moe tokens={tokens} hidden={hidden} inter={inter}")
+        L = Layer(np.random.default_rng(hidden + tokens), tokens, hidden, inter, 3, 2)
+        L.check(L.run(workspace=L.workspace(0xFF)))
 
 
 @pytest.mark.parametrize("tokens", [4, 20, 64])
