@@ -136,6 +136,8 @@ def _stream(t: torch.Tensor) -> int:
 
 
 def _dev(t: torch.Tensor, dtype, name: str, dims: int | None = None) -> torch.Tensor:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and (dims is None or t.dim() == dims):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -588,7 +590,7 @@ def _scalar(t: torch.Tensor, name: str, device) -> torch.Tensor:
 def _rows_out(out: torch.Tensor | None, rows: int, cols: int, device) -> tuple[torch.Tensor, int]:
     """The bf16 [rows, cols] output, made here or checked, and its row stride."""
     if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device), cols
+        return torch.empty(rows, cols, dtype=torch.bfloat16, device=device), cols
     _dev(out, torch.bfloat16, "out", 2)
     if out.shape != (rows, cols) or out.device != device:
         raise ValueError(f"out must be [{rows}, {cols}] on {device}")
@@ -609,12 +611,12 @@ def _call(fn: str, device, *args) -> None:
     """fn(*args, the device's current stream), with the device made current.
     The stream's handle comes without the Stream object, whose making is a
     sixth of a small call (1.9 of 12 us)."""
-    index = device.index
+    index, lib = device.index, _lib or load()
     if torch.cuda.current_device() == index:
-        status = getattr(load(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+        status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = getattr(load(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         _check(fn, status)
 
@@ -626,8 +628,8 @@ def mxfp4_quantize(x: torch.Tensor, out=None):
     rows, k = x.shape
     ldx = _row_major(x, "x")
     if out is None:
-        packed = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
-        e8m0 = torch.empty((rows, k // 32), dtype=torch.uint8, device=x.device)
+        packed = torch.empty(rows, k // 2, dtype=torch.uint8, device=x.device)
+        e8m0 = torch.empty(rows, k // 32, dtype=torch.uint8, device=x.device)
     else:
         packed = _flat(out[0], torch.uint8, (rows, k // 2), "packed", x.device)
         e8m0 = _flat(out[1], torch.uint8, (rows, k // 32), "e8m0", x.device)
@@ -642,7 +644,7 @@ def mxfp4_dequant(packed: torch.Tensor, e8m0: torch.Tensor, out: torch.Tensor | 
     _flat(packed, torch.uint8, (rows, k // 2), "packed", packed.device)
     _flat(e8m0, torch.uint8, (rows, k // 32), "e8m0", packed.device)
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.bfloat16, device=packed.device)
+        out = torch.empty(rows, k, dtype=torch.bfloat16, device=packed.device)
     else:
         _flat(out, torch.bfloat16, (rows, k), "out", packed.device)
     _call("mxfp4_dequant", packed.device, packed.data_ptr(), e8m0.data_ptr(), rows, k, out.data_ptr())
@@ -734,8 +736,8 @@ def moe_route(logits: torch.Tensor, top_k: int, normalize: bool = True, out=None
     tokens, experts = logits.shape
     ldl = _row_major(logits, "logits")
     if out is None:
-        ids = torch.empty((tokens, max(top_k, 0)), dtype=torch.int32, device=logits.device)
-        wts = torch.empty((tokens, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+        ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
+        wts = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
     else:
         ids = _flat(out[0], torch.int32, (tokens, top_k), "ids", logits.device)
         wts = _flat(out[1], torch.float32, (tokens, top_k), "weights", logits.device)
