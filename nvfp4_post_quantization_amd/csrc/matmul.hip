@@ -7,7 +7,7 @@
 // the tokens in registers and stream the rows' packed weights past them from
 // HBM.  The waves' partial sums meet in LDS and are added in wave order.
 // 12288x4096, weights 28 MB (MXFP4 27): W4A16 8.3 us for one token (3.4 TB/s of
-// weights), 10.6 for five, 15.1 for 16; MXFP4 8.2, 8.2 and 9.0; 28672x8192, one
+// weights), 10.0 for five, 13.0 for 16; MXFP4 8.2, 8.2 and 9.0; 28672x8192, one
 // W4A16 token: 26 us (5.0 TB/s).  What is left at the small end is a launch, one
 // trip to memory and the sum over the waves; at the large end, 55 vector
 // instructions a KiB keep the SIMDs busy for over 60% of the time.
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
   __shared__ f32x4 part[MW * TB * NG * 16];
   constexpr int STAGE = KIND == kW4A16 ? 4096 : 1024;      // of a wave: tokens, then weights, change their order there
   __shared__ __attribute__((aligned(16))) uint8_t stage[MW * STAGE];
-  const int lane = threadIdx.x & 63, j = lane & 3;
+  const int lane = threadIdx.x & 63;
   uint8_t* const lds_wave = stage + (threadIdx.x >> 6) * STAGE;
   const int tok0 = blockIdx.y * 4 * NG;
   const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 4;
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
     for (int n = 0; n < NG; ++n) {
       const int t0 = min(tok0 + 4 * n, a.tokens - 1), last = a.tokens - 1 - t0;               // others are not stored
       if constexpr (KIND == kW4A16) {
-        load_pieces(x[0][n], a.xp + (int64_t)(t0 + min(j, last)) * a.ldx, q, a.k);
+        load_pieces(x[0][n], a.xp + (int64_t)(t0 + min(lane >> 4, last)) * a.ldx, q, a.k);
       } else {
         const uint32_t rows = q * 512 < a.k ? min(4, a.tokens - t0) : 0;
         packed[n].load(PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds}, 0, q,
@@ -176,9 +176,10 @@ int run(const ProductArgs& a, hipStream_t s) {
     return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
   } else {
     // Tokens a workgroup: what their registers leave of the waves that share a
-    // CU counts.  4096x12288: one token takes 10.1 us with 4 and 16 waves; five
-    // 13.8 with 8 and 16, 14.7 with two quads a wave and 12; sixteen 22.9 with 16
-    // and 8, 34 as two workgroups of 8 tokens.  k off 32 has few uses: two sizes.
+    // CU counts.  4096x12288: one token takes 8.9 us with 4 and 16 waves; five
+    // 11.2 with 8 and 16 (two quads a wave and 12 waves: 1 more); sixteen 16.7 with
+    // 16 and 8 (as two workgroups of 8: half as much again).  k off 32 has few
+    // uses: two sizes.
     if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s) : run_few<KIND, true, 4, 8>(a, s);
     if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s);
     if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s);
@@ -190,8 +191,8 @@ int run(const ProductArgs& a, hipStream_t s) {
 
 // Tokens up to which the streaming kernels are used.  MXFP4 (4096x12288): 32
 // tokens take 14.1 us here and 13.9 in tiles (12288x4096: 10.9 and 14); NVFP4
-// weights, which are read again for every 16 tokens: 16 tokens take 22.9 us
-// here and 22.5 in tiles (12288x4096: 15.2 and 21), 32 take 40 and 22.5.
+// weights, which are read again for every 16 tokens: 16 tokens take 16.7 us
+// here and 22.5 in tiles (12288x4096: 13.0 and 21), 32 take over 30 and 22.5.
 static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
   return tokens > (mx ? 32 : 16) && tile_product_fits(tokens, out, k, ldx_bytes);
 }

@@ -137,7 +137,7 @@ template <bool ODD, int NG>
 __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, int e, int base, int count, int first_tok,
                                         uint64_t mask, int t0, int t1, const float* wt, f32x4* part, uint8_t* stage) {
   constexpr int CH = 8;                              // channels of a tile
-  const int wave = threadIdx.x >> 6, j = threadIdx.x & 3;
+  const int wave = threadIdx.x >> 6, j = (threadIdx.x & 63) >> 4;
   const uint32_t ldw = (uint32_t)a.hidden >> 1, lds = (uint32_t)a.hidden >> 4;
   const uint8_t* w = a.p13 + (int64_t)e * 2 * a.inter * ldw;
   const uint8_t* c = a.c13 + (int64_t)e * 2 * a.inter * lds;
