@@ -535,7 +535,7 @@ NVFP4_CHECKED int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, i
  *   w4a16:  y[t][o] = RN_bf16( w_scale2 * sum_k x[t][k] v[o][k] ),  x in bf16
  *   w4a4:   y[t][o] = RN_bf16( w_scale2 * x_scale2 * sum_k u[t][k] v[o][k] )
  * with v = e2m1 * e4m3(code) of w, u the same of x: exact operands, summed in
- * fp32.  (nvfp4_quantlinear_forward rounds its operands to bf16 after scale_2;
+ * fp32 (partial sums may overflow where |x| exceeds 2^100).  (nvfp4_quantlinear_forward rounds its operands to bf16 after scale_2;
  * these do not.)  Code 0x7F (NaN) makes the outputs it enters NaN.
  *
  * x          w4a16: [tokens][ldx] bf16, columns 0..k-1, 16-byte aligned rows.

@@ -12,6 +12,12 @@
 // from the ids by every workgroup (at most 1024 of them), which costs less
 // than a launch that writes it down: a 64-bit token mask per expert, and the
 // list of the jobs to do.
+//
+// 8 of 128 experts of 7168 x 2048: 1 token 50 us (198 MB, 4.0 TB/s), 16 tokens
+// 430 (2.15 GB, 5.0 TB/s), 61 tokens 710 (3.1 GB, 4.4 TB/s).  The first launch
+// takes two thirds of it and waits for memory; the second, at 61 tokens, issues
+// instructions 90% of the time, for it multiplies both parts of h and reads the
+// weights of an expert once for every four of its tokens.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -228,6 +234,7 @@ __global__ __launch_bounds__(64 * MW, 4) void moe_up_kernel(MoeArgs a) {
 // loads the next step's weights and h as it uses the current one's.  A product
 // has a column for each token of the job, added to the token's sums in the
 // wave's own part of LDS, step after step.  The waves are added at the end.
+// (12 waves: the same within 1%.)
 constexpr int kDownWaves = 8;
 
 template <bool ODD, int GROUPS>           // row groups of four
