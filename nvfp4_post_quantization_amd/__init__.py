@@ -565,6 +565,9 @@ def scale_sweep_stats(w: torch.Tensor, H: torch.Tensor, scale2: torch.Tensor, st
     return packed, codes, stats
 
 
+_U8, _BF16 = torch.uint8, torch.bfloat16
+
+
 def _flat(t: torch.Tensor, dtype, shape: tuple, name: str, device=None) -> torch.Tensor:
     """A contiguous GPU tensor of one dtype and shape, on `device` (a GPU) when given."""
     if (device is not None and isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
@@ -590,8 +593,8 @@ def _scalar(t: torch.Tensor, name: str, device) -> torch.Tensor:
 def _rows_out(out: torch.Tensor | None, rows: int, cols: int, device) -> tuple[torch.Tensor, int]:
     """The bf16 [rows, cols] output, made here or checked, and its row stride."""
     if out is None:
-        return torch.empty(rows, cols, dtype=torch.bfloat16, device=device), cols
-    _dev(out, torch.bfloat16, "out", 2)
+        return torch.empty(rows, cols, dtype=_BF16, device=device), cols
+    _dev(out, _BF16, "out", 2)
     if out.shape != (rows, cols) or out.device != device:
         raise ValueError(f"out must be [{rows}, {cols}] on {device}")
     return out, _row_major(out, "out")
@@ -601,7 +604,7 @@ def _scratch(workspace: torch.Tensor | None, device, need, *sizes) -> torch.Tens
     """The workspace: checked (its size by the library), or made here with need(*sizes) bytes."""
     if workspace is None:
         return torch.empty(max(need(*sizes), 1), dtype=torch.uint8, device=device)
-    _dev(workspace, torch.uint8, "workspace")
+    _dev(workspace, _U8, "workspace")
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {device}")
     return workspace
@@ -609,10 +612,10 @@ def _scratch(workspace: torch.Tensor | None, device, need, *sizes) -> torch.Tens
 
 def _call(fn: str, device, *args) -> None:
     """fn(*args, the device's current stream), with the device made current.
-    The stream's handle comes without the Stream object, whose making is a
-    sixth of a small call (1.9 of 12 us)."""
+    Device and stream are looked up without the torch.cuda functions and the
+    Stream object, which would be a fifth of a small call (2.1 of 10 us)."""
     index, lib = device.index, _lib or load()
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -624,29 +627,29 @@ def _call(fn: str, device, *args) -> None:
 def mxfp4_quantize(x: torch.Tensor, out=None):
     """MXFP4 form of bf16 x[rows, k] (k % 32 == 0): (packed u8 [rows, k/2],
     e8m0 u8 [rows, k/32]); out=(packed, e8m0) reuses buffers."""
-    _dev(x, torch.bfloat16, "x", 2)
+    _dev(x, _BF16, "x", 2)
     rows, k = x.shape
     ldx = _row_major(x, "x")
     if out is None:
-        packed = torch.empty(rows, k // 2, dtype=torch.uint8, device=x.device)
-        e8m0 = torch.empty(rows, k // 32, dtype=torch.uint8, device=x.device)
+        packed = torch.empty(rows, k // 2, dtype=_U8, device=x.device)
+        e8m0 = torch.empty(rows, k // 32, dtype=_U8, device=x.device)
     else:
-        packed = _flat(out[0], torch.uint8, (rows, k // 2), "packed", x.device)
-        e8m0 = _flat(out[1], torch.uint8, (rows, k // 32), "e8m0", x.device)
+        packed = _flat(out[0], _U8, (rows, k // 2), "packed", x.device)
+        e8m0 = _flat(out[1], _U8, (rows, k // 32), "e8m0", x.device)
     _call("mxfp4_quantize", x.device, x.data_ptr(), rows, k, ldx, packed.data_ptr(), e8m0.data_ptr())
     return packed, e8m0
 
 
 def mxfp4_dequant(packed: torch.Tensor, e8m0: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """bf16 [rows, k] of MXFP4 (packed u8 [rows, k/2], e8m0 u8 [rows, k/32])."""
-    _dev(packed, torch.uint8, "packed", 2)
+    _dev(packed, _U8, "packed", 2)
     rows, k = packed.shape[0], packed.shape[1] * 2
-    _flat(packed, torch.uint8, (rows, k // 2), "packed", packed.device)
-    _flat(e8m0, torch.uint8, (rows, k // 32), "e8m0", packed.device)
+    _flat(packed, _U8, (rows, k // 2), "packed", packed.device)
+    _flat(e8m0, _U8, (rows, k // 32), "e8m0", packed.device)
     if out is None:
-        out = torch.empty(rows, k, dtype=torch.bfloat16, device=packed.device)
+        out = torch.empty(rows, k, dtype=_BF16, device=packed.device)
     else:
-        _flat(out, torch.bfloat16, (rows, k), "out", packed.device)
+        _flat(out, _BF16, (rows, k), "out", packed.device)
     _call("mxfp4_dequant", packed.device, packed.data_ptr(), e8m0.data_ptr(), rows, k, out.data_ptr())
     return out
 
@@ -660,14 +663,14 @@ def mxfp4_matmul(x_packed: torch.Tensor, x_e8m0: torch.Tensor, w_packed: torch.T
     """y [tokens, out_features] bf16 = x w^T of two MXFP4 matrices (exact
     products, fp32 sums, one rounding).  out may have any row stride;
     workspace: uint8, at least mxfp4_matmul_workspace_bytes(...) bytes."""
-    _dev(x_packed, torch.uint8, "x_packed", 2)
-    _dev(w_packed, torch.uint8, "w_packed", 2)
+    _dev(x_packed, _U8, "x_packed", 2)
+    _dev(w_packed, _U8, "w_packed", 2)
     dev = x_packed.device
     tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
-    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed", dev)
-    _flat(x_e8m0, torch.uint8, (tokens, k // 32), "x_e8m0", dev)
-    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
-    _flat(w_e8m0, torch.uint8, (o, k // 32), "w_e8m0", dev)
+    _flat(x_packed, _U8, (tokens, k // 2), "x_packed", dev)
+    _flat(x_e8m0, _U8, (tokens, k // 32), "x_e8m0", dev)
+    _flat(w_packed, _U8, (o, k // 2), "w_packed", dev)
+    _flat(w_e8m0, _U8, (o, k // 32), "w_e8m0", dev)
     y, ldy = _rows_out(out, tokens, o, dev)
     ws = _scratch(workspace, dev, mxfp4_matmul_workspace_bytes, tokens, o, k)
     _call("mxfp4_matmul", dev, x_packed.data_ptr(), x_e8m0.data_ptr(), tokens, k, w_packed.data_ptr(),
@@ -686,13 +689,13 @@ def matmul_w4a16(x: torch.Tensor, w_packed: torch.Tensor, w_codes: torch.Tensor,
     weight (packed u8 [out_features, k/2], codes u8 [out_features, k/16],
     scale2 f32[1]), the weight taken exactly.  out may have any row stride;
     workspace: uint8, at least matmul_workspace_bytes(...) bytes."""
-    _dev(x, torch.bfloat16, "x", 2)
-    _dev(w_packed, torch.uint8, "w_packed", 2)
+    _dev(x, _BF16, "x", 2)
+    _dev(w_packed, _U8, "w_packed", 2)
     dev = x.device
     tokens, k = x.shape
     o = w_packed.shape[0]
-    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
-    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", dev)
+    _flat(w_packed, _U8, (o, k // 2), "w_packed", dev)
+    _flat(w_codes, _U8, (o, k // 16), "w_codes", dev)
     _scalar(w_scale2, "w_scale2", dev)
     y, ldy = _rows_out(out, tokens, o, dev)
     ws = _scratch(workspace, dev, matmul_workspace_bytes, tokens, o, k)
@@ -708,15 +711,15 @@ def matmul_w4a4(x_packed: torch.Tensor, x_codes: torch.Tensor, x_scale2: torch.T
     """y [tokens, out_features] bf16 = x w^T of two NVFP4 matrices (packed,
     codes, scale2 as quantize_dynamic and scale_sweep return them), both taken
     exactly.  out may have any row stride; workspace as for matmul_w4a16."""
-    _dev(x_packed, torch.uint8, "x_packed", 2)
-    _dev(w_packed, torch.uint8, "w_packed", 2)
+    _dev(x_packed, _U8, "x_packed", 2)
+    _dev(w_packed, _U8, "w_packed", 2)
     dev = x_packed.device
     tokens, k, o = x_packed.shape[0], x_packed.shape[1] * 2, w_packed.shape[0]
-    _flat(x_packed, torch.uint8, (tokens, k // 2), "x_packed", dev)
-    _flat(x_codes, torch.uint8, (tokens, k // 16), "x_codes", dev)
+    _flat(x_packed, _U8, (tokens, k // 2), "x_packed", dev)
+    _flat(x_codes, _U8, (tokens, k // 16), "x_codes", dev)
     _scalar(x_scale2, "x_scale2", dev)
-    _flat(w_packed, torch.uint8, (o, k // 2), "w_packed", dev)
-    _flat(w_codes, torch.uint8, (o, k // 16), "w_codes", dev)
+    _flat(w_packed, _U8, (o, k // 2), "w_packed", dev)
+    _flat(w_codes, _U8, (o, k // 16), "w_codes", dev)
     _scalar(w_scale2, "w_scale2", dev)
     y, ldy = _rows_out(out, tokens, o, dev)
     ws = _scratch(workspace, dev, matmul_workspace_bytes, tokens, o, k)
@@ -764,21 +767,21 @@ def moe_forward(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_p
     w2_packed u8 [experts, 1, hidden, inter/2] (or without the 1) with w2_codes
     [.., inter/16] and w2_scale2 f32[experts].  workspace: uint8, at least
     moe_workspace_bytes(tokens, top_k, inter) bytes."""
-    _dev(x, torch.bfloat16, "x", 2)
+    _dev(x, _BF16, "x", 2)
     _dev(ids, torch.int32, "ids", 2)
-    _dev(w13_packed, torch.uint8, "w13_packed", 4)
+    _dev(w13_packed, _U8, "w13_packed", 4)
     dev = x.device
     tokens, hidden = x.shape
     top_k = ids.shape[1]
     e, _, inter, _ = w13_packed.shape
     _flat(ids, torch.int32, (tokens, top_k), "ids", dev)
     _flat(weights, torch.float32, (tokens, top_k), "weights", dev)
-    _flat(w13_packed, torch.uint8, (e, 2, inter, hidden // 2), "w13_packed", dev)
-    _flat(w13_codes, torch.uint8, (e, 2, inter, hidden // 16), "w13_codes", dev)
+    _flat(w13_packed, _U8, (e, 2, inter, hidden // 2), "w13_packed", dev)
+    _flat(w13_codes, _U8, (e, 2, inter, hidden // 16), "w13_codes", dev)
     _flat(w13_scale2, torch.float32, (e,), "w13_scale2", dev)
     mid = (1,) if w2_packed.dim() == 4 else ()
-    _flat(w2_packed, torch.uint8, (e, *mid, hidden, inter // 2), "w2_packed", dev)
-    _flat(w2_codes, torch.uint8, (e, *mid, hidden, inter // 16), "w2_codes", dev)
+    _flat(w2_packed, _U8, (e, *mid, hidden, inter // 2), "w2_packed", dev)
+    _flat(w2_codes, _U8, (e, *mid, hidden, inter // 16), "w2_codes", dev)
     _flat(w2_scale2, torch.float32, (e,), "w2_scale2", dev)
     y, ldy = _rows_out(out, tokens, hidden, dev)
     ws = _scratch(workspace, dev, moe_workspace_bytes, tokens, top_k, inter)
