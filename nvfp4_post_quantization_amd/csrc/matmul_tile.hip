@@ -55,6 +55,10 @@ __device__ __forceinline__ i32x4 make_buffer(const void* p, uint32_t bytes) {
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
+// (m0 is the compiler's to set anew before each of its own uses, of which these
+// kernels have none; it only warns that it is named.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int AT>
 __device__ __forceinline__ void load_lds16(i32x4 b, uint32_t dst, uint32_t offset, int base) {
   asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
@@ -65,6 +69,7 @@ __device__ __forceinline__ void load_lds4(i32x4 b, uint32_t dst, uint32_t offset
   asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                ::"s"(dst), "v"(offset), "s"(b), "s"(base), "n"(AT) : "memory", "m0", "scc");
 }
+#pragma clang diagnostic pop
 // f(0), f(1) .. f(N - 1), each with a constant
 template <int N, typename F, int... I>
 __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }
