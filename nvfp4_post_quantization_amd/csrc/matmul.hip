@@ -120,18 +120,20 @@ template <int NT, int QW, int RT, int CU, int MW>
 __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductArgs a) {
   constexpr int TB = 4 / NT;
   __shared__ f32x4 part[MW * TB * NT * 64];
-  const int r16 = threadIdx.x & 15;
+  const int r16 = threadIdx.x & 15, r4 = (threadIdx.x & 63) >> 2;
+  __shared__ __attribute__((aligned(16))) uint8_t turn[MW][1024];
   const int tok0 = blockIdx.y * 16 * NT;
   const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 5;
   int begin, end;
   tile_run((a.out + 15) >> 4, begin, end);
   PackedRows tokens[NT];
-  uint32_t token_row[NT];
+  uint32_t token_row[NT], token_row_w[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t0 = min(tok0 + 16 * n, a.tokens - 1);
     const uint32_t rows = min(16, a.tokens - t0);
     tokens[n] = PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds};
+    token_row_w[n] = min(r4, a.tokens - 1 - t0);
     token_row[n] = min(r16, a.tokens - 1 - t0);                                  // others are not stored
   }
   auto rows_of = [&](int t) {
@@ -143,7 +145,8 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductA
     const int row = t * 16 + 4 * (l >> 4), tok = tok0 + 16 * n + (l & 15);
     if (tok < a.tokens && row < a.out) store_rows<kMX>(a, row, tok, v);
   };
-  stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, part, rows_of, done);
+  stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, token_row_w, part, turn[threadIdx.x >> 6],
+                                 rows_of, done);
 }
 
 template <int KIND, bool ODD, int NG, int CU>

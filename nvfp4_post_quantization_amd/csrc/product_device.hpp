@@ -480,6 +480,17 @@ struct MxQuad {
         s |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(b, (int)(i * 32 < left ? at + i : kBeyond), 0, 0) << (8 * i);
     }
   }
+  // Unit u from the order of loading (lane 4 r + g: piece g of row r, a cache line
+  // for four lanes) to the instruction's, through 1 KiB of LDS as RowGroup's.
+  __device__ __forceinline__ uint4 arranged(int u, uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
+    auto place = [](int r, int g) { return r * 64 + (((r >> 2) ^ (0x9C >> (2 * g) & 3)) << 4); };
+    *reinterpret_cast<uint4*>(lds + place(lane >> 2, lane & 3)) = w[u];
+    __builtin_amdgcn_wave_barrier();
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + place(lane & 15, lane >> 4));
+    __builtin_amdgcn_wave_barrier();
+    return v;
+  }
   // the scales of the lane's chunk in the four units, a byte each
   __device__ __forceinline__ uint32_t scales(int g) const {
     uint32_t a = s, b = s;
@@ -503,7 +514,8 @@ __device__ __forceinline__ f32x4 mfma_mx_unit(uint4 a, uint32_t sa, uint4 b, uin
 template <int NT, int QW, int RT, int TB, typename RowsOf, typename Done>
 __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const QuadPlan& plan,
                                                const PackedRows (&tokens)[NT], const uint32_t (&token_row)[NT],
-                                               f32x4* part, RowsOf rows_of, Done done) {
+                                               const uint32_t (&token_row_w)[NT],
+                                               f32x4* part, uint8_t* lds, RowsOf rows_of, Done done) {
   static_assert(TB % RT == 0, "whole steps in a batch");
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -524,7 +536,7 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
     return v;
   };
   auto load_unit = [&](int t, int z, int u) {
-    w[t][z].load_unit(u, rows(z), 16 * t + (lane & 15), quad(at_pass, z), g, k);
+    w[t][z].load_unit(u, rows(z), 16 * t + (lane >> 2), quad(at_pass, z), lane & 3, k);
   };
   auto load_scales = [&](int t, int z) { w[t][z].load_scales(rows(z), 16 * t + (lane & 15), quad(at_pass, z), g, k); };
   auto advance = [&]() {
@@ -545,7 +557,7 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
       for (int n = 0; n < NT; ++n) {
         const int q = quad(pass, z);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[z][n].load_unit(u, tokens[n], token_row[n], q, g, k);
+        for (int u = 0; u < 4; ++u) x[z][n].load_unit(u, tokens[n], token_row_w[n], q, lane & 3, k);
         x[z][n].load_scales(tokens[n], token_row[n], q, g, k);
       }
   };
@@ -557,8 +569,10 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
         xs[z][n] = x[z][n].scales(g);
         const int left = k - quad(pass, z) * 512 - g * 32;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u) {
+          x[z][n].w[u] = x[z][n].arranged(u, lds);
           if (left <= u * 128) x[z][n].w[u] = make_uint4(0, 0, 0, 0);
+        }
       }
   };
   load_tokens(0);                                    // first, so that taking them awaits no weights
@@ -593,13 +607,18 @@ __device__ __forceinline__ void stream_mx_rows(int begin, int end, int k, const 
             MxQuad& m = w[r][z];
             const uint32_t ws = m.scales(g);
             load_scales(r, z);
+            uint4 v[4];
             auto unit = [&](auto u) {
               constexpr int U = decltype(u)::value;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) sum[n] = mfma_mx_unit<U>(m.w[U], ws, x[z][n].w[U], xs[z][n], sum[n]);
-              load_unit(r, z, U);
-              __builtin_amdgcn_sched_barrier(0);     // the load goes out here, not where its value is near
+              for (int n = 0; n < NT; ++n) sum[n] = mfma_mx_unit<U>(v[U], ws, x[z][n].w[U], xs[z][n], sum[n]);
             };
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              v[u] = m.arranged(u, lds);
+              load_unit(r, z, u);
+              __builtin_amdgcn_sched_barrier(0);     // the load goes out here, not where its value is near
+            }
             unit(std::integral_constant<int, 0>{});
             unit(std::integral_constant<int, 1>{});
             unit(std::integral_constant<int, 2>{});
