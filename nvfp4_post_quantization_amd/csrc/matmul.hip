@@ -7,8 +7,8 @@
 // the tokens in registers and stream the rows' packed weights past them from
 // HBM.  The waves' partial sums meet in LDS and are added in wave order.
 // 12288x4096, weights 28 MB (MXFP4 27): W4A16 8.3 us for one token (3.4 TB/s of
-// weights), 10.0 for five, 13.0 for 16; MXFP4 8.2, 8.2 and 9.0; 28672x8192, one
-// W4A16 token: 26 us (5.0 TB/s).  What is left at the small end is a launch, one
+// weights), 10.0 for five, 13.0 for 16; MXFP4 6.4, 6.4 and 6.7; 28672x8192, one
+// W4A16 token: 26 us (5.0 TB/s), 16 MXFP4 tokens 22 (5.6 TB/s).  What is left at the small end is a launch, one
 // trip to memory and the sum over the waves; at the large end, 55 vector
 // instructions a KiB keep the SIMDs busy for over 60% of the time.
 #include "common.hpp"
@@ -120,21 +120,20 @@ template <int NT, int QW, int RT, int CU, int MW>
 __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductArgs a) {
   constexpr int TB = 4 / NT;
   __shared__ f32x4 part[MW * TB * NT * 64];
-  const int r16 = threadIdx.x & 15, r4 = (threadIdx.x & 63) >> 2;
-  __shared__ __attribute__((aligned(16))) uint8_t turn[MW][1024];
+  __shared__ __attribute__((aligned(16))) uint8_t turn[MW][1024];          // operands change their order there
+  const int r4 = (threadIdx.x & 63) >> 2;
   const int tok0 = blockIdx.y * 16 * NT;
   const uint32_t ldw = (uint32_t)a.k >> 1, lds = (uint32_t)a.k >> 5;
   int begin, end;
   tile_run((a.out + 15) >> 4, begin, end);
   PackedRows tokens[NT];
-  uint32_t token_row[NT], token_row_w[NT];
+  uint32_t token_row[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t0 = min(tok0 + 16 * n, a.tokens - 1);
     const uint32_t rows = min(16, a.tokens - t0);
     tokens[n] = PackedRows{a.xp + (int64_t)t0 * ldw, a.xc + (int64_t)t0 * lds, rows * ldw, rows * lds};
-    token_row_w[n] = min(r4, a.tokens - 1 - t0);
-    token_row[n] = min(r16, a.tokens - 1 - t0);                                  // others are not stored
+    token_row[n] = min(r4, a.tokens - 1 - t0);                                   // others are not stored
   }
   auto rows_of = [&](int t) {
     const int row = t * 16;
@@ -145,8 +144,8 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductA
     const int row = t * 16 + 4 * (l >> 4), tok = tok0 + 16 * n + (l & 15);
     if (tok < a.tokens && row < a.out) store_rows<kMX>(a, row, tok, v);
   };
-  stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, token_row_w, part, turn[threadIdx.x >> 6],
-                                 rows_of, done);
+  stream_mx_rows<NT, QW, RT, TB>(begin, end, a.k, quad_plan<QW>(a.k, CU), tokens, token_row, part, turn[threadIdx.x >> 6], rows_of,
+                                 done);
 }
 
 template <int KIND, bool ODD, int NG, int CU>
@@ -173,7 +172,8 @@ template <int KIND>
 int run(const ProductArgs& a, hipStream_t s) {
   if constexpr (KIND == kMX) {
     // Two row tiles a step and 8 waves where those hold the channels, else two
-    // quads a wave: 12288x4096, one token: 8.2 us, 9.5 with one tile and 16 waves.
+    // quads a wave: 12288x4096, one token: 8.2 us against 9.5 with one tile and 16
+    // waves (before lanes shared cache lines, 6.4 since).
     const bool narrow = a.k <= 4096;
     if (a.tokens <= 16) return narrow ? run_few_mx<1, 1, 2, 8>(a, s) : run_few_mx<1, 2, 1, 12>(a, s);
     return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
@@ -193,7 +193,8 @@ int run(const ProductArgs& a, hipStream_t s) {
 }  // namespace
 
 // Tokens up to which the streaming kernels are used.  MXFP4 (4096x12288): 32
-// tokens take 14.1 us here and 13.9 in tiles (12288x4096: 10.9 and 14); NVFP4
+// tokens take 9.1 us here and 13.5 in tiles, 64 would take twice 9.1 here and
+// 15.5 in tiles; NVFP4
 // weights, which are read again for every 16 tokens: 16 tokens take 16.7 us
 // here and 22.5 in tiles (12288x4096: 13.0 and 21), 32 take over 30 and 22.5.
 static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
