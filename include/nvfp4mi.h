@@ -519,7 +519,8 @@ NVFP4_CHECKED int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int6
  * workspace  16-byte aligned, at least mxfp4_matmul_workspace_bytes(tokens,
  *            out_features, k) bytes (the query returns 0 where none is needed;
  *            workspace may then be NULL); scratch.  Results do not depend on
- *            what it held, and are the same bits on every call.
+ *            what it held, and are the same bits on every call.  Calls (or
+ *            replays of captured ones) that overlap in time need one each.
  * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED, WORKSPACE, HIP.
  */
 NVFP4_CHECKED size_t mxfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k);
@@ -603,7 +604,7 @@ NVFP4_CHECKED int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t e
  * tokens     0 .. 64;  top_k 1 .. 16;  experts 1 .. 1024.
  * hidden, inter: multiples of 16, at most 2^26, their product below 2^31.
  * workspace  16-byte aligned, at least nvfp4_moe_workspace_bytes(tokens, top_k,
- *            inter) bytes; scratch.
+ *            inter) bytes; scratch, one for each call that overlaps in time.
  * Errors: NULL_ARG, BAD_SHAPE, BAD_INPUT (tokens, top_k or experts out of
  *         range), MISALIGNED, WORKSPACE, HIP.
  */
