@@ -588,8 +588,8 @@ NVFP4_CHECKED int nvfp4_moe_route(const float* logits, int64_t tokens, int64_t e
  * 攻略" §3: w1 and w3 of an expert share one scale_2):
  *   y[t] = RN_bf16( sum_s weights[t][s] W2_e ( silu(W1_e x[t]) * (W3_e x[t]) ) ),
  * e = ids[t][s], silu(a) = a / (1 + exp(-a)), every W the exact NVFP4 value.
- * Sums are in fp32; the product silu * up enters the second product as two
- * bf16 parts (16 significant bits).  Results are the same bits on every call.
+ * Sums are in fp32, and so is weights * scale_2 * silu * up, which enters the
+ * second product with its 24 bits.  Results are the same bits on every call.
  * An id outside 0..experts-1 (a place the router left empty, an expert that
  * lives elsewhere) adds nothing; a token without any gets zeros.  An expert
  * that a token names twice counts with both weights.

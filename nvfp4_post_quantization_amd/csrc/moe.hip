@@ -16,7 +16,7 @@
 // 8 of 128 experts of 7168 x 2048: 1 token 50 us (198 MB, 4.0 TB/s), 16 tokens
 // 430 (2.15 GB, 5.0 TB/s), 61 tokens 710 (3.1 GB, 4.4 TB/s).  The first launch
 // takes two thirds of it and waits for memory; the second, at 61 tokens, issues
-// instructions 90% of the time, for it multiplies both parts of h and reads the
+// instructions 90% of the time, for it multiplies three parts of h and reads the
 // weights of an expert once for every four of its tokens.
 #include "common.hpp"
 #include "product_device.hpp"
@@ -27,6 +27,12 @@ namespace {
 
 constexpr int kCus = 256;
 constexpr int kMaxJobs = kMoeMaxTokens * kMoeMaxTopK;
+// h is a float32 value, kept as the sum of three bf16 ones, which hold its 24
+// bits; bf16 matrix instructions multiply them one after another.  Two parts, 16
+// bits, moved 0.25% of 437248 outputs off the rounded exact value, three move
+// 0.025% (float32 products in another order 0.1%); the layer took 411 and 696 us
+// for 16 and 61 tokens with two, takes 428 and 755 with three.
+constexpr int kParts = 3;
 
 struct MoeArgs {
   const uint8_t* x;               // bf16 rows
@@ -37,9 +43,9 @@ struct MoeArgs {
   const float *s13, *s2;
   uint16_t* y;
   int64_t ldy;
-  uint16_t* h;                    // [groups of four tokens][ldh][4] bf16 (see place_of), then the low parts
+  uint16_t* h;                    // [parts][groups of four tokens][ldh][4] bf16 (see place_of)
   int64_t ldh;                    // inter rounded up to whole quads, zero past inter
-  int64_t lo;                     // bytes from a value's high part to its low part
+  int64_t part;                   // bytes from a part of a value to the next one
   int tokens, hidden, inter, experts, top_k;
 };
 
@@ -136,6 +142,17 @@ __device__ __forceinline__ int place_of(int c, int j) {
   return (c & ~511) << 2 | ((c >> 3) & 3) << 9 | ((c >> 5) & 15) << 5 | j << 3 | (c & 7);
 }
 
+// v = a + b + c in bf16, 8 bits each, cut off and not rounded: a finite v stays
+// finite, and the differences are exact.  An infinity or NaN is in a alone.
+__device__ __forceinline__ void split(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint32_t bits = __float_as_uint(v), top = bits & 0xFFFF0000u;
+  const float rest = (bits & 0x7F800000u) == 0x7F800000u ? 0.f : v - __uint_as_float(top);
+  const uint32_t middle = __float_as_uint(rest) & 0xFFFF0000u;
+  a = top >> 16;
+  b = middle >> 16;
+  c = __float_as_uint(rest - __uint_as_float(middle)) >> 16;
+}
+
 // h of 4 NG tokens (tok: the lane's of each four) of a job, for row tiles
 // t0 .. t1 - 1.  A tile's first two row groups are the gate rows of 8 channels,
 // the others their up rows, so that one pass over the tokens serves both.
@@ -173,24 +190,22 @@ __device__ __forceinline__ void up_rows(const MoeArgs& a, const QuadPlan& plan, 
     const int col = 4 * n + tj;
     if (q >= 2 || col >= count) return;
     const float scale = wt[col];
-    uint32_t hi[4], lo[4];
+    uint32_t h[kParts][4];
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
       const float gate = v[z] * s13;
-      const float h = gate / (1.0f + expf(-gate)) * (up[z] * s13) * scale;
-      hi[z] = to_bf16(h);                            // two bf16 parts keep 16 significant bits of h
-      lo[z] = to_bf16(h - bf16_to_f32(hi[z]));
+      split(gate / (1.0f + expf(-gate)) * (up[z] * s13) * scale, h[0][z], h[1][z], h[2][z]);
     }
     uint16_t* group_h = a.h + (int64_t)(base + col / 4) * a.ldh * 4;
-    auto put = [&](int ch, uint2 high, uint2 low) {
-      uint8_t* dst = reinterpret_cast<uint8_t*>(group_h + place_of(ch, col & 3));
-      *reinterpret_cast<uint2*>(dst) = high;
-      *reinterpret_cast<uint2*>(dst + a.lo) = low;
+    auto put = [&](int p, int ch, uint2 value) {
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(group_h + place_of(ch, col & 3)) + p * a.part) = value;
     };
-    put(t * CH + 4 * q, make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
-        make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16));
-    if ((t + 1) * CH == a.inter && q == 0)           // the rest of the row's last quad
-      for (int ch = a.inter; ch < a.ldh; ch += 4) put(ch, make_uint2(0, 0), make_uint2(0, 0));
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      put(p, t * CH + 4 * q, make_uint2(h[p][0] | h[p][1] << 16, h[p][2] | h[p][3] << 16));
+      if ((t + 1) * CH == a.inter && q == 0)         // the rest of the row's last quad
+        for (int ch = a.inter; ch < a.ldh; ch += 4) put(p, ch, make_uint2(0, 0));
+    }
   };
   stream_rows<ODD, NG, 4>(t0, t1, a.hidden, plan, group_row, x, part, stage + wave * 4096, rows_of, load_tokens, take_tokens,
                            done);
@@ -256,7 +271,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
   float* mine = sums + wave * each;
 
   RowGroup w[GROUPS];
-  Chunk h[2][1], h_next[2][1];            // high and low parts
+  Chunk h[kParts][1], h_next[kParts][1];
   PackedRows next{};
   const uint8_t* next_h = nullptr;
   int next_q = 0;
@@ -271,12 +286,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
     // (a group's tokens past the last one hold anything: their columns are not added)
     next_h = reinterpret_cast<const uint8_t*>(a.h) + (int64_t)job * a.ldh * 8 + next_q * 4096 + lane * 16;
   };
-  auto load_h = [&](Chunk (&d)[2][1]) {
+  auto load_h = [&](Chunk (&d)[kParts][1]) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < kParts; ++p)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const uint4 v = global_load16(next_h + (p ? a.lo : 0) + m * 1024);
+        const uint4 v = global_load16(next_h + p * a.part + m * 1024);
         d[p][0][4 * m] = v.x;
         d[p][0][4 * m + 1] = v.y;
         d[p][0][4 * m + 2] = v.z;
@@ -284,7 +299,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
       }
   };
   auto load_w = [&](int q) { w[q].load(next, 4 * q, next_q, LaneAt<ODD>(lane >> 4, next_q, a.inter), a.inter); };
-  auto step = [&](int i, const Chunk (&x)[2][1], Chunk (&x_next)[2][1]) {
+  auto step = [&](int i, const Chunk (&x)[kParts][1], Chunk (&x_next)[kParts][1]) {
     const int job = i / quads;
     aim(i + kDownWaves);
     load_h(x_next);
@@ -296,7 +311,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down_kernel(MoeArgs a)
       const RowGroup r = w[q].arranged(turn[wave]);
       load_w(q);
       __builtin_amdgcn_sched_barrier(0);             // the load goes out here, not where its value is near
-      multiply_group<1, 2>(r, x, acc[q]);
+      multiply_group<1, kParts>(r, x, acc[q]);
     }
     const int e = __builtin_amdgcn_readfirstlane(r.expert[job]), first = r.first[job];
     const uint64_t mask = tokens_of(r, e);
@@ -442,7 +457,7 @@ static int64_t moe_ldh(int64_t inter) { return (inter + 511) / 512 * 512; }
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
   // groups of four tokens: as many as pairs where no two tokens share an expert
-  return 2 * ((size_t)(tokens * top_k) * 4 * (size_t)moe_ldh(inter) * 2);
+  return kParts * ((size_t)(tokens * top_k) * 4 * (size_t)moe_ldh(inter) * 2);
 }
 
 int launch_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
@@ -476,7 +491,7 @@ int launch_moe_forward(const uint16_t* x, int64_t tokens, int64_t hidden, int64_
   a.ldy = ldy;
   a.h = reinterpret_cast<uint16_t*>(workspace);
   a.ldh = moe_ldh(inter);
-  a.lo = (int64_t)(moe_workspace_bytes(tokens, top_k, inter) / 2);
+  a.part = (int64_t)(moe_workspace_bytes(tokens, top_k, inter) / kParts);
   a.tokens = (int)tokens;
   a.hidden = (int)hidden;
   a.inter = (int)inter;
