@@ -513,7 +513,8 @@ NVFP4_CHECKED int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int6
  *
  * x_packed [tokens][k/2], x_e8m0 [tokens][k/32], w_packed [out_features][k/2],
  * w_e8m0 [out_features][k/32]: uint8, contiguous, 16-byte aligned;
- * k % 32 == 0, k at most 2^26; tokens and out_features below 2^31 - 15.
+ * k % 32 == 0, k at most 2^26; tokens at most 2^31 - 256, out_features
+ * 2^31 - 16.
  * y          [tokens][ldy] bf16, columns 0..out_features-1; any ldy >=
  *            out_features (other columns are left as they were).
  * workspace  16-byte aligned, at least mxfp4_matmul_workspace_bytes(tokens,
@@ -543,7 +544,7 @@ NVFP4_CHECKED int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, i
  * x_packed, x_codes  w4a4: [tokens][k/2], [tokens][k/16].
  * w_packed, w_codes  [out_features][k/2], [out_features][k/16].  All packed
  *            and code arrays: uint8, contiguous, 16-byte aligned; k % 16 == 0,
- *            k at most 2^26; tokens and out_features below 2^31 - 15.
+ *            k at most 2^26; tokens at most 2^31 - 256, out_features 2^31 - 16.
  * x_scale2, w_scale2  device float[1].
  * y, workspace: as for mxfp4_matmul, with nvfp4_matmul_workspace_bytes (one
  *            size serves both).

@@ -402,12 +402,14 @@ int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int6
   return launch_mxfp4_dequant(packed, e8m0, rows, k, out, as_stream(stream));
 }
 
-// Sizes of a product: rows and columns are indexed with 32 bits, and 16 rows of
-// packed channels have 32-bit offsets.
+// Sizes of a product: rows and columns are indexed with 32 bits, up to the end
+// of the last tile (256 tokens; 16 output rows, since the tiles that have more
+// are not used where they would pass 2^31), and 16 rows of packed channels have
+// 32-bit offsets.
 constexpr int64_t kMaxChannels = INT64_C(1) << 26;
 static int check_product(int64_t tokens, int64_t out, int64_t k, int64_t block, int64_t ldy) {
   if (tokens < 0 || out <= 0 || k <= 0 || k % block || ldy < out) return NVFP4_ERR_BAD_SHAPE;
-  if (tokens > INT32_MAX || out > INT32_MAX - 15 || k > kMaxChannels) return NVFP4_ERR_BAD_SHAPE;
+  if (tokens > INT32_MAX - 255 || out > INT32_MAX - 15 || k > kMaxChannels) return NVFP4_ERR_BAD_SHAPE;
   return check_matrix(tokens, out, ldy, 2);
 }
 

@@ -177,7 +177,7 @@ __device__ __forceinline__ void store_tiles(const TileArgs& a, const f32x16 (&ac
         const int t = t0 + 32 * m + r + row0;
         if (t >= a.tokens) continue;
         uint16_t* dst = a.y + (int64_t)t * a.ldy + o;
-        if (o + 8 <= a.out) {
+        if (o <= a.out - 8) {                        // (o + 8 may be 2^31)
           *reinterpret_cast<uint4*>(dst) = v;
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -761,10 +761,12 @@ TileArgs tile_args(const Plan& p, const PrepArgs& q, int64_t tokens, int64_t out
 
 }  // namespace
 
-// Byte offsets inside a tile's rows, and the number of tiles, stay below 2^31.
+// Byte offsets inside a tile's rows stay below 2^31, and the threads of a launch
+// below 2^32: a tile, large or small, has at most 512, and small ones are used
+// for fewer than 3/4 kCus large ones.
 bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, int64_t ldx_bytes) {
-  const int64_t lim = INT64_C(1) << 31;
-  return 256 * ldx_bytes < lim && 256 * k < lim && (out + 127) / 128 * ((tokens + 127) / 128) < lim / 64;
+  const int64_t lim = INT64_C(1) << 31, threads = 512;
+  return 256 * ldx_bytes < lim && 256 * k < lim && (out + 255) / 256 * ((tokens + 255) / 256) < 2 * lim / threads;
 }
 
 size_t tile_product_workspace(int64_t tokens, int64_t out, int64_t k, bool mx) {
