@@ -397,57 +397,59 @@ __device__ __forceinline__ float wave_max(float v) {
 // each of the top_k rounds takes the wave's largest remaining one, the lowest
 // expert that has it.  The rounds follow one another, so what counts is their
 // length: the maximum by lane permutes and its place by votes, 5.1 us for 16
-// tokens and 8 of 128 experts; shuffles of value and place took 6.5.
+// tokens and 8 of 128 experts; shuffles of value and place took 6.5.  A launch
+// has fewer than 2^32 threads, so that many tokens go round by round.
+constexpr unsigned kRouteGrid = 1 << 22;
 template <int PER>
 __global__ __launch_bounds__(256) void moe_route_kernel(const float* __restrict__ logits, int64_t tokens, int experts,
                                                         int64_t ldl, int top_k, int normalize,
                                                         int32_t* __restrict__ ids, float* __restrict__ weights) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= tokens) return;
   const float ninf = -__builtin_inff();
-  float v[PER];
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tokens; t += (int64_t)gridDim.x * 4) {
+    float v[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    const float l = e < experts ? logits[t * ldl + e] : ninf;
-    v[i] = l > ninf ? fminf(l, 3.40282347e38f) : ninf;           // NaN is out, like -inf
-  }
-  float top = 0.f, mine = 0.f, sum = 0.f;
-  int my_id = -1;
-  for (int s = 0; s < top_k; ++s) {
-    float bv = v[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) bv = fmaxf(bv, v[i]);
-    bv = wave_max(bv);
-    int bi = 0;
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i) {
-      const uint64_t has = __ballot(v[i] == bv);
-      if (has) bi = 64 * i + __builtin_ctzll(has);
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 64 * i;
+      const float l = e < experts ? logits[t * ldl + e] : ninf;
+      v[i] = l > ninf ? fminf(l, 3.40282347e38f) : ninf;           // NaN is out, like -inf
     }
-    if (s == 0) {
-      top = bv;
-      if (!normalize) {
-        float z = 0.f;
+    float top = 0.f, mine = 0.f, sum = 0.f;
+    int my_id = -1;
+    for (int s = 0; s < top_k; ++s) {
+      float bv = v[0];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) z += v[i] > ninf ? expf(v[i] - bv) : 0.f;
+      for (int i = 1; i < PER; ++i) bv = fmaxf(bv, v[i]);
+      bv = wave_max(bv);
+      int bi = 0;
 #pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) z += __shfl_xor(z, m);
-        sum = z;
+      for (int i = PER - 1; i >= 0; --i) {
+        const uint64_t has = __ballot(v[i] == bv);
+        if (has) bi = 64 * i + __builtin_ctzll(has);
       }
-    }
-    const bool some = bv > ninf;
-    const float p = some ? expf(bv - top) : 0.f;
-    if (normalize) sum += p;
-    if (lane == s) { mine = p; my_id = some ? bi : -1; }
+      if (s == 0) {
+        top = bv;
+        if (!normalize) {
+          float z = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 64 * i == bi) v[i] = ninf;
-  }
-  if (lane < top_k) {
-    ids[t * top_k + lane] = my_id;
-    weights[t * top_k + lane] = my_id >= 0 ? mine / sum : 0.f;
+          for (int i = 0; i < PER; ++i) z += v[i] > ninf ? expf(v[i] - bv) : 0.f;
+#pragma unroll
+          for (int m = 32; m >= 1; m >>= 1) z += __shfl_xor(z, m);
+          sum = z;
+        }
+      }
+      const bool some = bv > ninf;
+      const float p = some ? expf(bv - top) : 0.f;
+      if (normalize) sum += p;
+      if (lane == s) { mine = p; my_id = some ? bi : -1; }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane + 64 * i == bi) v[i] = ninf;
+    }
+    if (lane < top_k) {
+      ids[t * top_k + lane] = my_id;
+      weights[t * top_k + lane] = my_id >= 0 ? mine / sum : 0.f;
+    }
   }
 }
 
@@ -462,7 +464,8 @@ size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t inter) {
 
 int launch_moe_route(const float* logits, int64_t tokens, int64_t experts, int64_t ldl, int top_k, int normalize,
                      int32_t* ids, float* weights, hipStream_t s) {
-  const unsigned grid = (unsigned)((tokens + 3) / 4);
+  const int64_t want = (tokens + 3) / 4;
+  const unsigned grid = want < kRouteGrid ? (unsigned)want : kRouteGrid;
   const int e = (int)experts;
   if (e <= 64) moe_route_kernel<1><<<grid, 256, 0, s>>>(logits, tokens, e, ldl, top_k, normalize, ids, weights);
   else if (e <= 128) moe_route_kernel<2><<<grid, 256, 0, s>>>(logits, tokens, e, ldl, top_k, normalize, ids, weights);

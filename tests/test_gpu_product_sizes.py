@@ -46,3 +46,19 @@ def test_product_of_the_most_outputs(out):
         assert not bool(row[:out].any())
     del y, wp, wc
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [((1 << 26) + 5, 2, 1), ((1 << 26) - 3, 1, 1)])
+def test_route_of_more_tokens_than_a_launch_has_places(tokens, experts, top_k):
+    """A wave a token would be 2^32 threads and more."""
+    note(f"route tokens={tokens}")
+    z = torch.zeros((tokens, experts), dtype=torch.float32, device=DEV)
+    rng = np.random.default_rng(tokens)
+    at = np.r_[0, 1, tokens - 2, tokens - 1, rng.choice(tokens, 2000, replace=False)]
+    some = rng.normal(0, 1, (len(at), experts)).astype(np.float32)
+    where = torch.from_numpy(at).to(DEV)
+    z[where] = torch.from_numpy(some).to(DEV)
+    ids, w = nq.moe_route(z, top_k)
+    ri, rw = O.moe_route(host(z[where]), top_k, True)
+    assert np.array_equal(host(ids[where]), ri) and np.array_equal(host(w[where]), rw.astype(np.float32))
+    assert int(ids.min()) == 0 and int(ids.max()) < experts and bool((w == 1).all())
