@@ -79,6 +79,15 @@ __device__ __forceinline__ void each(F f) { each_of<N>(f, std::make_integer_sequ
 template <int N>
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
+// Waves meet, and the compiler moves no read of LDS across (the builtin alone
+// would let it).  Reads in flight stay so: what they read is overwritten after
+// the next meeting at the earliest.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Piece swizzles of LDS rows of 64, 128 and 32 bytes: piece p of a row lies at
 // place p ^ swizzle.  A 16-byte read of a wave is served in four groups of 16
 // lanes (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; the same + 32) over 64 banks;
@@ -407,7 +416,7 @@ __global__ __launch_bounds__(64 * (WM * WN + NL), NL ? 4 : 2) void mx_tile_kerne
     if (s_begin + AHEAD <= s_end) wait_loads<(AHEAD - 1) * LOADS>();
     else wait_loads<0>();
   }
-  __builtin_amdgcn_s_barrier();
+  stage_barrier();
   if (multiplies) {
     read_scales(s_begin);
     read_frags(0, s_begin);
@@ -416,7 +425,7 @@ __global__ __launch_bounds__(64 * (WM * WN + NL), NL ? 4 : 2) void mx_tile_kerne
   auto next_stage = [&](int s, auto way) {
     if constexpr (way == kLast) return;
     if (loads) wait_loads<way == kDrain ? 0 : (AHEAD - 2) * LOADS>();
-    __builtin_amdgcn_s_barrier();
+    stage_barrier();
     if constexpr (way == kWhole || way == kCut)
       if (loads) load_stage(s + AHEAD, std::bool_constant<way == kWhole>{});
   };
@@ -539,13 +548,13 @@ __global__ __launch_bounds__(64 * (WM * WN + NL), NL && AHEAD == 2 ? 4 : 2) void
     if (s_begin + AHEAD <= s_end) wait_loads<(AHEAD - 1) * LOADS>();
     else wait_loads<0>();
   }
-  __builtin_amdgcn_s_barrier();
+  stage_barrier();
   int buf = 0, free = AHEAD;                                      // stage s, and where stage s + AHEAD goes
   // on to stage s + 1, in one of the ways below
   auto next_stage = [&](int s, auto way) {
     if constexpr (way == kLast) return;
     if (loads) wait_loads<way == kDrain ? 0 : (AHEAD - 2) * LOADS>();
-    __builtin_amdgcn_s_barrier();
+    stage_barrier();
     if constexpr (way == kWhole || way == kCut)
       if (loads) load_stage(s + AHEAD, free, std::bool_constant<way == kWhole>{});
     free = buf;
