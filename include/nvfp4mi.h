@@ -507,9 +507,10 @@ NVFP4_CHECKED int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int6
 /*
  * Product of two MXFP4 matrices (the weights as Linear [out][in]):
  *   y[t][o] = RN_bf16( sum_k xh[t][k] wh[o][k] ),
- * xh, wh the exact values e2m1 * 2^(code-127); products are exact and summed
- * in fp32 on the scaled FP4 matrix instructions.  Code 255 (NaN) makes every
- * output of its row or column NaN.
+ * xh, wh the exact values e2m1 * 2^(code-127); products are exact, also where
+ * one scale alone would leave the range of fp32, and summed in fp32 on the
+ * scaled FP4 matrix instructions.  Code 255 (NaN) makes every output of its row
+ * or column NaN.
  *
  * x_packed [tokens][k/2], x_e8m0 [tokens][k/32], w_packed [out_features][k/2],
  * w_e8m0 [out_features][k/32]: uint8, contiguous, 16-byte aligned;
@@ -536,9 +537,11 @@ NVFP4_CHECKED int mxfp4_matmul(const uint8_t* x_packed, const uint8_t* x_e8m0, i
  * W4A16 and W4A4 tiers):
  *   w4a16:  y[t][o] = RN_bf16( w_scale2 * sum_k x[t][k] v[o][k] ),  x in bf16
  *   w4a4:   y[t][o] = RN_bf16( w_scale2 * x_scale2 * sum_k u[t][k] v[o][k] )
- * with v = e2m1 * e4m3(code) of w, u the same of x: exact operands, summed in
- * fp32 (partial sums may overflow where |x| exceeds 2^100).  (nvfp4_quantlinear_forward rounds its operands to bf16 after scale_2;
- * these do not.)  Code 0x7F (NaN) makes the outputs it enters NaN.
+ * with v = e2m1 * e4m3(code) of w, u the same of x: exact operands, subnormal
+ * ones too, summed in fp32 (partial sums may overflow where k max |x| exceeds
+ * 2^116).  (nvfp4_quantlinear_forward rounds its operands to bf16 after
+ * scale_2; these do not.)  Code 0x7F (NaN) makes the outputs it enters NaN, an
+ * infinity or NaN in x those of its token.
  *
  * x          w4a16: [tokens][ldx] bf16, columns 0..k-1, 16-byte aligned rows.
  * x_packed, x_codes  w4a4: [tokens][k/2], [tokens][k/16].
