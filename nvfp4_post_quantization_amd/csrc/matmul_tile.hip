@@ -660,9 +660,12 @@ __global__ __launch_bounds__(256) void join_kernel(TileArgs a) {
 
 constexpr int kCus = 256;
 
-// How a product is cut.  Large tiles where they fill the card, else tiles of
-// 128 x 128, with the channels split where that is quicker: a stage of such a
-// tile takes 0.29 us (MXFP4) or 0.37, 1.4 times that where two share a CU, and
+// How a product is cut.  Large tiles where they fill the card and more than half
+// of their rows are tokens (a small tile's time goes by its rows, a large one's
+// too: 128 tokens of 151936x4096 take 119 us in large tiles and 94 in small ones
+// (MXFP4), 302 and 184 (W4A16), 291 and 184 (W4A4); 129 take 119 and 126, 302 and
+// 305, 290 and 299), else tiles of 128 x 128, with the channels split where that
+// is quicker: a stage of such a tile takes 0.29 us (MXFP4) or 0.37, 1.4 times that where two share a CU, and
 // a split costs a launch and a trip of its fp32 partial sums through memory.
 // MXFP4, 333 tokens: 4096x4096 takes 13.5 us whole and 17.3 in two, 4096x12288
 // 32.6 and 26.3.
@@ -680,7 +683,8 @@ Plan plan_product(int64_t tokens, int64_t out, int64_t k, bool mx) {
   const int span = mx ? 128 : 64;        // channels of a stage: four scales
   p.steps = (int)((k + span - 1) / span);
   p.pad = k % span != 0;
-  const bool large = (tokens + 255) / 256 * ((out + 255) / 256) >= kCus * 3 / 4;
+  const bool many = out >= INT64_C(1) << 26;                      // more small tiles than a launch has places
+  const bool large = (tokens > 128 || many) && (tokens + 255) / 256 * ((out + 255) / 256) >= kCus * 3 / 4;
   p.rows = p.cols = large ? 256 : 128;
   p.tiles_m = (int)((tokens + p.rows - 1) / p.rows);
   p.tiles_n = (int)((out + p.cols - 1) / p.cols);
@@ -771,8 +775,9 @@ TileArgs tile_args(const Plan& p, const PrepArgs& q, int64_t tokens, int64_t out
 }  // namespace
 
 // Byte offsets inside a tile's rows stay below 2^31, and the threads of a launch
-// below 2^32: a tile, large or small, has at most 512, and small ones are used
-// for fewer than 3/4 kCus large ones.
+// below 2^32: a tile, large or small, has at most 512.  Small ones, in up to 16
+// parts, are used in place of fewer than 3/4 kCus large ones, or fewer than 2^19
+// of them for up to 128 tokens.
 bool tile_product_fits(int64_t tokens, int64_t out, int64_t k, int64_t ldx_bytes) {
   const int64_t lim = INT64_C(1) << 31, threads = 512;
   return 256 * ldx_bytes < lim && 256 * k < lim && (out + 255) / 256 * ((tokens + 255) / 256) < 2 * lim / threads;

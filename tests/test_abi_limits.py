@@ -52,6 +52,20 @@ def test_tiles_are_used_where_their_launch_holds(lib):
         assert q(257, (1 << 30) - 256, k) > 0 and q(257, 1 << 30, k) == 0
 
 
+def test_tiles_of_few_tokens_are_not_the_large_ones(lib):
+    """Up to 128 tokens fill one row of small tiles, and half a large one at
+    most, however many outputs there are.  Small tiles show by the channel
+    parts that this many of them are split into, whose sums need a workspace."""
+    k = 1 << 18                                     # enough that parts pay: 1 part 1.4 x 2048 stages, 4 parts 3/4 of that
+    for q, own in ((lib.mxfp4_matmul_workspace_bytes, 0),
+                   (lib.nvfp4_matmul_workspace_bytes, 2)):                  # bytes of W4A4's activations a channel
+        for t in (33, 128):
+            assert q(t, 49152, k) - own * t * k >= 2 * t * 49152 * 4
+            # where small tiles might be more than a launch holds: no parts, no sums
+            assert q(t, 1 << 26, 2048) == own * t * 2048
+        assert q(129, 49152, k) == own * 129 * k
+
+
 def test_too_little_workspace_at_the_limit(lib):
     for call, q in zip(_calls(lib), (lib.mxfp4_matmul_workspace_bytes, lib.nvfp4_matmul_workspace_bytes,
                                      lib.nvfp4_matmul_workspace_bytes)):

@@ -6,6 +6,7 @@ import torch
 import nvfp4_post_quantization_amd as nq
 import oracle as O
 from oracle import formats as F
+from oracle import mxcast as M
 
 from _gpu import DEV, need_gpu, note, host, to_dev_bf16, to_dev_f32, to_dev_u8, to_host_bits
 
@@ -62,6 +63,36 @@ def test_route_of_more_tokens_than_a_launch_has_places(tokens, experts, top_k):
     ri, rw = O.moe_route(host(z[where]), top_k, True)
     assert np.array_equal(host(ids[where]), ri) and np.array_equal(host(w[where]), rw.astype(np.float32))
     assert int(ids.min()) == 0 and int(ids.max()) < experts and bool((w == 1).all())
+
+
+@pytest.mark.parametrize("kind", ["mx", "w4a16", "w4a4"])
+@pytest.mark.parametrize("tokens", [33, 128, 129])
+@pytest.mark.parametrize("k", [512, 544])
+def test_few_tokens_of_a_wide_output(kind, tokens, k):
+    """Outputs enough to fill the card with large tiles, and tokens to fill
+    a small one; sampled columns."""
+    note(f"{kind} tokens={tokens} out=49300 k={k}")
+    rng = np.random.default_rng(tokens)
+    out = 49300
+    at = np.unique(np.r_[0, 1, out - 140:out, rng.integers(0, out, 300)])
+    unit, lo, hi = (32, 118, 134) if kind == "mx" else (16, 0, 127)
+    def packed(rows):
+        return rng.integers(0, 256, (rows, k // 2), dtype=np.uint8), rng.integers(lo, hi, (rows, k // unit), dtype=np.uint8)
+    values = M.mxfp4_dequant if kind == "mx" else O.nvfp4_values
+    w, x = packed(out), packed(tokens)
+    wd, xd, one = [to_dev_u8(a) for a in w], [to_dev_u8(a) for a in x], to_dev_f32([1.0])
+    xv = values(*x)
+    if kind == "mx":
+        y = nq.mxfp4_matmul(*xd, *wd)
+    elif kind == "w4a4":
+        y = nq.matmul_w4a4(*xd, one, *wd, one)
+    else:
+        bits = F.f64_to_bf16_rne(rng.normal(0, 1, (tokens, k)))
+        xv = F.bf16_bits_to_f64(bits)
+        y = nq.matmul_w4a16(to_dev_bf16(bits), *wd, one)
+    ref, mag = O.matmul(xv, values(w[0][at], w[1][at]))
+    got = F.bf16_bits_to_f64(to_host_bits(y))[:, at]
+    assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + (k + 3) * 2.0 ** -23 * mag * (1 + HALF))
 
 
 # The most channels, altogether and in tiles.  All but some hundred activations
