@@ -6,11 +6,18 @@
 // takes a run of row tiles; its waves split the channels, hold their part of
 // the tokens in registers and stream the rows' packed weights past them from
 // HBM.  The waves' partial sums meet in LDS and are added in wave order.
-// 12288x4096, weights 28 MB (MXFP4 27): W4A16 8.3 us for one token (3.4 TB/s of
-// weights), 10.0 for five, 13.0 for 16; MXFP4 6.4, 6.4 and 6.7; 28672x8192, one
-// W4A16 token: 26 us (5.0 TB/s), 16 MXFP4 tokens 22 (5.6 TB/s).  What is left at the small end is a launch, one
-// trip to memory and the sum over the waves; at the large end, 55 vector
-// instructions a KiB keep the SIMDs busy for over 60% of the time.
+// A call in a captured graph, with the weights cold (768 MB of others since their
+// last use; in brackets: one set, which the 256 MB MALL keeps), us:
+//   12288x4096 (28 MB; MXFP4 27)  W4A16, 1, 5, 16 tokens  8.9, 11.2, 14.7  (7.1, 8.8, 12.2)
+//                                 W4A4                    9.2, 11.3, 14.3  (7.2, 8.8, 12.1)
+//                                 MXFP4                   8.3,  8.4,  8.7  (5.1, 5.2,  5.6)
+//   4096x12288                    W4A16                  10.0, 12.4, 17.0  (7.4, 9.4, 14.4)
+//   28672x8192 (132 MB; 125)      W4A16, 1, 16 tokens    30, 50 (24, 44);  MXFP4, 16: 27.5 (21)
+// that is 3.2 TB/s of cold weights for one token at the small end and 4.4 at the
+// large one.  What is left at the small end is a launch, one trip to memory and
+// the sum over the waves; at the large end the SIMDs issue something over 90% of
+// the time (52 to 55 vector instructions a KiB for up to four tokens).
+// Comparisons of variants below that do not say cold are of one set of weights.
 #include "common.hpp"
 #include "product_device.hpp"
 
@@ -173,16 +180,16 @@ int run(const ProductArgs& a, hipStream_t s) {
   if constexpr (KIND == kMX) {
     // Two row tiles a step and 8 waves where those hold the channels, else two
     // quads a wave: 12288x4096, one token: 8.2 us against 9.5 with one tile and 16
-    // waves (before lanes shared cache lines, 6.4 since).
+    // waves (both before lanes shared cache lines, which took the first to 5.1).
     const bool narrow = a.k <= 4096;
     if (a.tokens <= 16) return narrow ? run_few_mx<1, 1, 2, 8>(a, s) : run_few_mx<1, 2, 1, 12>(a, s);
     return narrow ? run_few_mx<2, 1, 2, 8>(a, s) : run_few_mx<2, 2, 1, 12>(a, s);
   } else {
     // Tokens a workgroup: what their registers leave of the waves that share a
-    // CU counts.  4096x12288: one token takes 8.9 us with 4 and 16 waves; five
-    // 11.2 with 8 and 16 (two quads a wave and 12 waves: 1 more); sixteen 16.7 with
-    // 16 and 8 (as two workgroups of 8: half as much again).  k off 32 has few
-    // uses: two sizes.
+    // CU counts.  4096x12288: one token takes 7.4 us with 4 and 16 waves; five 9.4
+    // with 8 and 16 (two quads a wave and 12 waves: 1 more); sixteen 14.4 with 16
+    // and 8 (as two workgroups of 8: half as much again).  k off 32 has few uses:
+    // two sizes.
     if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s) : run_few<KIND, true, 4, 8>(a, s);
     if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s);
     if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s);
@@ -192,11 +199,18 @@ int run(const ProductArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tokens up to which the streaming kernels are used.  MXFP4 (4096x12288): 32
-// tokens take 9.1 us here and 13.5 in tiles, 64 would take twice 9.1 here and
-// 15.5 in tiles; NVFP4
-// weights, which are read again for every 16 tokens: 16 tokens take 16.7 us
-// here and 22.5 in tiles (12288x4096: 13.0 and 21), 32 take over 30 and 22.5.
+// Tokens up to which the streaming kernels are used.  Weights cold, us here and
+// in tiles:
+//             4096x12288      12288x4096      28672x8192
+//   MXFP4 32  11.2 and 15.6   10.2 and 15.2   30 and 38
+//         48  17.2 and 16.5
+//         64  17.7 and 17.0   15.7 and 17.0   48 and 38
+//   W4A16 16  17.8 and 24.2   14.7 and 22.6   50 and 68
+//         24  31.5 and 24.9   25.3 and 23.2
+//         32  31.6 and 25.2   25.3 and 24.2   96 and 68
+//   W4A4  16  16.5 and 26.0   14.3 and 24.1
+//         32  29.5 and 27.3   25.3 and 25.8
+// (MXFP4 tokens are taken 32 at a time, NVFP4 weights are read again for every 16.)
 static bool use_tiles(int64_t tokens, int64_t out, int64_t k, bool mx, int64_t ldx_bytes) {
   return tokens > (mx ? 32 : 16) && tile_product_fits(tokens, out, k, ldx_bytes);
 }

@@ -27,11 +27,17 @@
 // of four bytes; where k does not give that, a small launch first copies them
 // to such rows in the workspace.
 //
-// 8192 tokens: MXFP4 12288x4096 242 us (3.4 PFLOP/s) and 12288x16384 825 (4.0),
-// W4A16 4096x12288 655 (1.26 PFLOP/s); 4095 tokens: W4A4 12288x4096 332 with the
-// expansion (1.24).  Power bounds these: with zeros for data they take 188, 690,
-// 470 and 253.  333 tokens, 4096x12288: MXFP4 24 us, where LDS traffic (16 KB in
-// and 32 KB out a stage) bounds the small tile; W4A16 53, W4A4 59.
+// 8192 tokens: MXFP4 12288x4096 243 us (3.4 PFLOP/s) and 12288x16384 826 (4.0),
+// W4A16 4096x12288 650 (1.27 PFLOP/s); 4095 tokens: W4A4 12288x4096 327 with the
+// expansion (1.26).  With zeros for data they take 213, 687, 472 and 262, the rest
+// being a clock that power lowers to 1.6 - 1.8 GHz.  The matrix cores are busy for
+// 0.72 (W4A16), 0.70 (W4A4) and 0.46 (MXFP4) of the cycles; in the last, LDS reads
+// take 0.39 (0.15 of it conflicts of the scale words), direct loads come on top,
+// and neither is full: they do not overlap well enough, and tiles end.
+// 333 tokens, 4096x12288: MXFP4 24 us, W4A16 51, W4A4 54 (weights cold: 30, 53 and
+// 55).  On the MXFP4 ones' 192 CUs the matrix cores are busy for 0.29 and LDS for
+// 0.29 of the time: one multiplying wave a SIMD waits for its operands and meets
+// a barrier every eight products.
 #include <type_traits>
 #include <utility>
 
@@ -92,7 +98,7 @@ __device__ __forceinline__ void stage_barrier() {
 // place p ^ swizzle.  A 16-byte read of a wave is served in four groups of 16
 // lanes (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; the same + 32) over 64 banks;
 // with these, the lanes of a group that read one piece of their 16 rows touch
-// every bank once (no conflict counted; the plain row-order ones cost 4
+// every bank once (no conflict counted for operands; the plain row-order ones cost 4
 // cycles in 12).
 __device__ __forceinline__ int swizzle64(int row) { return (row >> 2) & 3; }
 __device__ __forceinline__ int swizzle128(int row) { return (row >> 1) & 7; }
@@ -233,7 +239,8 @@ __device__ __forceinline__ f32x16 mfma32_mx(uint4 a, uint32_t sa, uint4 b, uint3
 // replaces has been read: stages are AHEAD steps ahead, so two groups are kept
 // for three steps and four for up to eight.  16-bit x, 8192x4096x12288: 675 us
 // with quarters, 706 without; MXFP4, which has scales of x too, 8192x12288x4096:
-// 252 and 247 us.
+// 252 and 247 us (without quarters the words of 32 rows lie in 16 of the 64 banks:
+// 36 of 99 LDS cycles of a wave and stage of the large tile are their conflicts).
 template <int RX, int RW, int NW, int AHEAD, bool QUARTERS>
 struct ScaleStages {
   static constexpr int CHUNKS = (RX + RW) / 64, LOADS = (CHUNKS + NW - 1) / NW, GROUP = (RX + RW) * 16;
@@ -665,10 +672,10 @@ constexpr int kCus = 256;
 // too: 128 tokens of 151936x4096 take 119 us in large tiles and 94 in small ones
 // (MXFP4), 302 and 184 (W4A16), 291 and 184 (W4A4); 129 take 119 and 126, 302 and
 // 305, 290 and 299), else tiles of 128 x 128, with the channels split where that
-// is quicker: a stage of such a tile takes 0.29 us (MXFP4) or 0.37, 1.4 times that where two share a CU, and
-// a split costs a launch and a trip of its fp32 partial sums through memory.
-// MXFP4, 333 tokens: 4096x4096 takes 13.5 us whole and 17.3 in two, 4096x12288
-// 32.6 and 26.3.
+// is quicker: a stage of such a tile takes 0.29 us (MXFP4) or 0.37, 1.4 times that
+// where two share a CU, and a split costs a launch and a trip of its fp32 partial
+// sums through memory.  MXFP4, 333 tokens: 4096x4096 takes 13.5 us whole and 17.3
+// in two, 4096x12288 32.6 and 26.3 (one set of weights, in the MALL).
 struct Plan {
   int rows, cols;                        // of a tile: tokens x outputs
   int tiles_m, tiles_n, splits, steps;

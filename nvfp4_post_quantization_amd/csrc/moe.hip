@@ -13,11 +13,13 @@
 // than a launch that writes it down: a 64-bit token mask per expert, and the
 // list of the jobs to do.
 //
-// 8 of 128 experts of 7168 x 2048: 1 token 50 us (198 MB, 4.0 TB/s), 16 tokens
-// 430 (2.15 GB, 5.0 TB/s), 61 tokens 710 (3.1 GB, 4.4 TB/s).  The first launch
-// takes two thirds of it and waits for memory; the second, at 61 tokens, issues
-// instructions 90% of the time, for it multiplies three parts of h and reads the
-// weights of an expert once for every four of its tokens.
+// 8 of 128 experts of 7168 x 2048, with the router's launch: 1 token 61 us (198 MB;
+// 55 with the same inputs again, whose weights the MALL keeps), 16 tokens 425 to
+// 460 as they reach 80 to 87 experts (2.0 to 2.2 GB, 4.6 TB/s), 61 tokens 745 to
+// 770 (3.1 GB, 4.1 TB/s).  The first product takes 60% of it and waits for memory
+// (it issues something 0.73 of the time); the second issues 0.79 (16 tokens) and
+// 0.84 (61) of the time, for it multiplies three parts of h and reads the weights
+// of an expert once for every four of its tokens.
 #include "common.hpp"
 #include "product_device.hpp"
 

@@ -125,8 +125,9 @@ __host__ __device__ inline QuadPlan quad_plan(int64_t k, int most) {
 // weights is four instructions; its scale then multiplies their fp32 sum, so
 // that the weights enter as plain E2M1 values, one conversion for two of them.
 // Per 1 KiB of weights that is 27 vector and 8 matrix instructions for up to
-// four tokens; the 16x16x32 instruction, which needs the scales in the weights,
-// took 132 and held the expert layer to 3.6 TB/s.
+// four tokens, and 52 to 55 vector ones with the exchange, the sums and the
+// addresses (counted); the 16x16x32 instruction, which needs the scales in the
+// weights, took 132 and held the expert layer to 3.6 TB/s.
 //
 // Memory is read by lane 16 i + b instead, so that neighbouring lanes read
 // neighbouring pieces: a load of 16 bytes a lane looks up a cache line for every
@@ -394,7 +395,7 @@ __device__ __forceinline__ void stream_rows(int begin, int end, int k, const Qua
 // exchange them in LDS (4 KiB, the wave's own; pieces of a chunk are swapped
 // with its place and token, so that 16 lanes touch every bank once).  With token
 // lane % 4, which looks up a cache line for every lane, 16 tokens of
-// 4096x12288 took 22.9 us, so 17.3.
+// 4096x12288, weights in the MALL, took 22.9 us, so 17.3.
 static __device__ const uint4 kZeroPiece[1] = {};
 __device__ __forceinline__ void load_pieces(Chunk& x, const uint8_t* row, int q, int k) {
   const int b = threadIdx.x & 15;
@@ -455,7 +456,8 @@ __device__ __forceinline__ void expand_chunk(Chunk& x, const RowGroup& r) {
 // for a quarter of the pieces that loading them unit by unit would.
 //
 // Memory is read by lane 4 r + g, so that four lanes share a cache line (see
-// above): 32 tokens of 4096x12288 took 14.3 us with lanes l % 16, 9.5 so.
+// above): 32 tokens of 4096x12288, weights in the MALL, took 14.3 us with lanes
+// l % 16, 9.5 so.
 struct MxQuad {
   uint4 w[4];
   uint32_t s;

@@ -44,8 +44,10 @@ exact-quotient rounding rule, nibble order within a byte, the clamp of a
 nonzero block's code to 0x01, the synthetic input recipes, (for the W4A4
 Hessian variant) that the layer input is taken after its activation
 quantizer, (FP8 tier) the static scale amax/448 and the exact-quotient
-encode, and (rotation) the per-group input-channel rotation, its butterfly
-order and the single rounding to bf16.
+encode, (rotation) the per-group input-channel rotation, its butterfly
+order and the single rounding to bf16, and (packed products) the MXFP4
+quantizer's scale rule and NaN blocks, the exact operands, the layer's
+formula and the router's ties and non-finite logits.
 """
 from .formats import (
     E2M1_MAGNITUDES, E4M3_VALUES, e2m1_decode, e2m1_encode, e4m3_value,
