@@ -18,6 +18,13 @@ Functions (names as in the C ABI):
   matmul_w4a4(x_packed, x_codes, x_scale2, w_packed, w_codes, w_scale2) -> bf16 x w^T
   moe_route(logits, top_k) -> (ids i32, weights f32)
   moe_forward(x, ids, weights, w13_packed, w13_codes, w13_scale2, w2_packed, w2_codes, w2_scale2) -> bf16
+
+and, from libnvfp4mi_layer.so (layer.py):
+  moe_sort(ids, experts) -> (order i32, place i32, offsets i32)
+  moe_dispatch(x, place) -> rows;  moe_dispatch_grad(dxs, place) -> bf16
+  moe_combine(ys, place, weights) -> bf16;  moe_combine_grad(dy, ys, place, weights) -> (bf16, f32)
+  moe_forward_sorted(...) -> bf16: moe_forward for any number of tokens
+  matmul_w4a16_lora(x, w_packed, w_codes, w_scale2, adapter_ids, lora_a, lora_b, lora_scale) -> bf16
 """
 from __future__ import annotations
 
@@ -790,3 +797,9 @@ def moe_forward(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13_p
           w2_packed.data_ptr(), w2_codes.data_ptr(), w2_scale2.data_ptr(), y.data_ptr(), ldy,
           ws.data_ptr(), ws.numel())
     return y
+
+
+from . import layer as _layer  # noqa: E402  (it uses the helpers above)
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

@@ -1,7 +1,8 @@
-"""Build the HIP library libnvfp4mi.so for gfx950, in-tree.
+"""Build the HIP libraries for gfx950, in-tree.
 
 Every source under csrc/ is compiled by hipcc to an object in _build/ (in
-parallel) and linked into nvfp4_post_quantization_amd/libnvfp4mi.so.
+parallel) and linked into nvfp4_post_quantization_amd/libnvfp4mi.so, or, those
+of the layer operators, into libnvfp4mi_layer.so beside it, which uses the first.
 """
 from __future__ import annotations
 
@@ -18,6 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4mi.so")
 SOURCES = ["api.hip", "quant.hip", "hessian.hip", "sweep.hip", "cast.hip", "fp8.hip", "rotate.hip", "linear.hip",
            "probe.hip", "sweep_stats.hip", "mxfp4.hip", "matmul.hip", "matmul_tile.hip", "moe.hip"]
+LAYER_LIB = os.path.join(HERE, "libnvfp4mi_layer.so")
+LAYER_SOURCES = ["layer_api.hip", "moe_rows.hip", "moe_sorted.hip", "lora.hip"]
 ARCH = os.environ.get("NVFP4MI_ARCH", "gfx950")
 
 FLAGS = [
@@ -30,6 +33,7 @@ FLAGS = [
 ]
 # hipBLASLt serves the plain bf16 GEMM of the QuantLinear forward
 LINK = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
+LAYER_LINK = ["-L", HERE, "-l:libnvfp4mi.so", "-Wl,-rpath,$ORIGIN", "-Wl,--no-undefined"]
 
 
 def _hipcc() -> str:
@@ -53,19 +57,25 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    """Compile all sources and link libnvfp4mi.so; returns the library path."""
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp, *LINK]
+def _link(sources: list[str], lib: str, link: list[str], verbose: bool) -> None:
+    objs = [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in sources]
+    cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", lib + ".tmp", *link]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
+    os.replace(lib + ".tmp", lib)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile all sources and link both libraries; returns the path of libnvfp4mi.so."""
+    os.makedirs(BUILD, exist_ok=True)
+    sources = SOURCES + LAYER_SOURCES
+    with cf.ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 4)) as ex:
+        list(ex.map(lambda s: _compile(s, verbose), sources))
+    _link(SOURCES, LIB, LINK, verbose)
+    _link(LAYER_SOURCES, LAYER_LIB, LAYER_LINK, verbose)
     return LIB
 
 

@@ -6,7 +6,7 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include "common.hpp"
+#include "check.hpp"
 #include "../../include/nvfp4mi_probe.h"
 
 namespace nvfp4 {
@@ -28,21 +28,6 @@ int force_exact_flag() {
   const char* v = getenv("NVFP4MI_FORCE_EXACT");
   if (!v || !v[0] || v[0] == '0') return 0;
   return (v[0] == '2' || v[0] == '3') ? v[0] - '0' : 1;
-}
-
-// a * b <= INT64_MAX for non-negative a, b
-static bool mul_fits(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / a; }
-
-// [rows][ld] matrix of `elem` bytes with `cols` used columns.
-static int check_matrix(int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
-  if (rows < 0 || cols <= 0 || ld < cols) return NVFP4_ERR_BAD_SHAPE;
-  if (!mul_fits(rows, ld) || !mul_fits(rows * ld, elem)) return NVFP4_ERR_BAD_SHAPE;
-  return NVFP4_OK;
-}
-
-static int check_bf16_rows(const void* p, int64_t ld) {
-  if (!aligned16(p) || (ld % 8) != 0) return NVFP4_ERR_MISALIGNED;
-  return NVFP4_OK;
 }
 
 }  // namespace nvfp4
@@ -402,26 +387,9 @@ int mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int6
   return launch_mxfp4_dequant(packed, e8m0, rows, k, out, as_stream(stream));
 }
 
-// Sizes of a product: rows and columns are indexed with 32 bits, up to the end
-// of the last tile (256 tokens; 16 output rows, since the tiles that have more
-// are not used where they would pass 2^31), and 16 rows of packed channels have
-// 32-bit offsets.
-constexpr int64_t kMaxChannels = INT64_C(1) << 26;
-static int check_product(int64_t tokens, int64_t out, int64_t k, int64_t block, int64_t ldy) {
-  if (tokens < 0 || out <= 0 || k <= 0 || k % block || ldy < out) return NVFP4_ERR_BAD_SHAPE;
-  if (tokens > INT32_MAX - 255 || out > INT32_MAX - 15 || k > kMaxChannels) return NVFP4_ERR_BAD_SHAPE;
-  return check_matrix(tokens, out, ldy, 2);
-}
-
 static size_t matmul_workspace(int64_t tokens, int64_t out_features, int64_t k, int64_t block, bool mx) {
   if (tokens <= 0 || check_product(tokens, out_features, k, block, out_features)) return 0;
   return product_workspace_bytes(tokens, out_features, k, mx);
-}
-
-static int check_workspace(const void* workspace, size_t have, size_t need) {
-  if (have < need) return NVFP4_ERR_WORKSPACE;
-  if (need && !workspace) return NVFP4_ERR_NULL_ARG;
-  return need && !aligned16(workspace) ? NVFP4_ERR_MISALIGNED : NVFP4_OK;
 }
 
 size_t mxfp4_matmul_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k) {

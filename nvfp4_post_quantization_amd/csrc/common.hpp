@@ -92,9 +92,11 @@ int launch_mxfp4_quantize(const uint16_t* x, int64_t rows, int64_t k, int64_t ld
                           hipStream_t s);
 int launch_mxfp4_dequant(const uint8_t* packed, const uint8_t* e8m0, int64_t rows, int64_t k, uint16_t* out,
                          hipStream_t s);
+struct LoraTerm;                         // what an adapter adds to a W4A16 product (lora_device.hpp)
 size_t product_workspace_bytes(int64_t tokens, int64_t out, int64_t k, bool mx);
 int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* wp, const uint8_t* wc,
-                        const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);
+                        const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s,
+                        const LoraTerm* lora = nullptr);
 int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens, int64_t k,
                        const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y, int64_t ldy,
                        void* workspace, hipStream_t s);
@@ -107,7 +109,7 @@ int launch_tile_mx(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t
                    int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s);
 int launch_tile_nv(const uint16_t* x, int64_t ldx, const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens,
                    int64_t k, const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y,
-                   int64_t ldy, void* workspace, hipStream_t s);
+                   int64_t ldy, void* workspace, hipStream_t s, const LoraTerm* lora = nullptr);
 // mixture-of-experts layer: limits of one call
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopK = 16;

@@ -1,0 +1,168 @@
+// Low-rank adapters of many requests at once beside a shared W4A16 projection:
+//
+//   y[t][o] = RN_bf16( w_scale2 sum_k x[t][k] v[o][k] + scale_a sum_r u[t][r] B_a[o][r] )
+//   u[t][r] = sum_k x[t][k] A_a[r][k],  a the token's adapter
+//
+// Two launches (and the product's own third where it splits the channels): u in
+// fp32 here, and the product, whose last step adds the term (matmul.hip,
+// matmul_tile.hip), so that nothing is rounded but y.
+//
+// u: a wave takes 16 or 64 tokens and a run of channels, and the adapters of its
+// tokens one after another on the 16x16x32 bf16 instruction, whose columns are the
+// tokens: each column of the result belongs to one token, which takes that of its
+// own adapter.  Where tokens follow in runs of a request that is one pass over x.
+// The four waves of a workgroup add up their channels in LDS; what other
+// workgroups have of the same tokens are the splits that the product adds up.
+#include "layer.hpp"
+#include "lora_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kCus = 256;
+constexpr int kMaxSplits = 8;
+
+struct InnerArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const int32_t* ids;
+  const uint16_t* a;          // [count][rank][k]
+  const float* scale;
+  float* u;                   // [splits][tokens][rank]
+  int64_t part;
+  int tokens, k, count, rank, splits;
+};
+
+__device__ __forceinline__ f32x4 mfma16_bf16(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// 16 NT tokens (x), a split of the channels (y), every gridDim.z-th of their
+// adapters (z).  RT tiles of 16 rows of A at a time.
+template <int NT, int RT>
+__global__ __launch_bounds__(256) void lora_inner_kernel(InnerArgs p) {
+  __shared__ __attribute__((aligned(16))) f32x4 part[4][NT * RT][64];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.x * 16 * NT;
+  // the wave's steps of 32 channels
+  const int steps = (p.k + 31) >> 5, parts = p.splits * 4, at = blockIdx.y * 4 + wave;
+  const int s0 = (int)((int64_t)steps * at / parts), s1 = (int)((int64_t)steps * (at + 1) / parts);
+  int id[NT];
+  const uint16_t* x[NT];
+  uint64_t live[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = t0 + 16 * n + l16;
+    id[n] = t < p.tokens ? p.ids[t] : -1;
+    if (id[n] < 0 || id[n] >= p.count) id[n] = -1;
+    live[n] = __ballot(id[n] >= 0);
+    x[n] = p.x + (int64_t)min(t, p.tokens - 1) * p.ldx + q * 8;
+  }
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int turn = 0;; ++turn) {
+    // the next adapter: that of the first token that has had none
+    int a = -1;
+#pragma unroll
+    for (int n = NT - 1; n >= 0; --n)
+      if (live[n]) a = __builtin_amdgcn_readlane(id[n], __builtin_ctzll(live[n]));
+    if (a < 0) break;
+    uint64_t has[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      has[n] = __ballot(id[n] == a);
+      live[n] &= ~has[n];
+    }
+    if (turn % (int)gridDim.z != (int)blockIdx.z) continue;
+    for (int r0 = 0; r0 < p.rank; r0 += 16 * RT) {
+      const uint16_t* rows[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)                   // (rows past the last: it again, their results are not stored)
+        rows[r] = p.a + ((int64_t)a * p.rank + min(r0 + 16 * r + l16, p.rank - 1)) * p.k + q * 8;
+      f32x4 acc[NT][RT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[n][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const auto step = [&](int s, bool in) {
+        uint4 w[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) w[r] = in ? *reinterpret_cast<const uint4*>(rows[r] + s * 32) : zero;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (!has[n]) continue;
+          const uint4 v = in ? *reinterpret_cast<const uint4*>(x[n] + s * 32) : zero;
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[n][r] = mfma16_bf16(w[r], v, acc[n][r]);
+        }
+      };
+      const int whole = min(s1, p.k >> 5);
+      int s = s0;
+      for (; s < whole; ++s) step(s, true);
+      if (s < s1) step(s, s * 32 + q * 8 < p.k);     // (k is a multiple of 16)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) part[wave][n * RT + r][lane] = acc[n][r];
+      __syncthreads();
+      const float scale = p.scale[a];
+      for (int i = threadIdx.x; i < NT * RT * 64; i += 256) {
+        const int l = i & 63, n = (i >> 6) / RT, r = r0 + 16 * ((i >> 6) % RT) + 4 * (l >> 4);
+        const int t = t0 + 16 * n + (l & 15);
+        if (r >= p.rank || t >= p.tokens || p.ids[t] != a) continue;
+        f32x4 v = part[0][i >> 6][l];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v += part[w][i >> 6][l];
+        *reinterpret_cast<f32x4*>(p.u + blockIdx.y * p.part + (int64_t)t * p.rank + r) = v * scale;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+struct InnerPlan { int tokens, splits, slots; };     // tokens of a workgroup, splits of the channels, of the adapters
+InnerPlan plan_inner(int64_t tokens, int64_t k) {
+  InnerPlan p;
+  p.tokens = tokens <= 1024 ? 16 : 64;
+  const int64_t groups = (tokens + p.tokens - 1) / p.tokens, steps = (k + 127) / 128;
+  const int64_t want = (2 * kCus + groups - 1) / groups;
+  p.splits = (int)(want < kMaxSplits ? want : kMaxSplits);
+  if (p.splits > steps) p.splits = (int)steps;
+  const int64_t slots = want / p.splits, most = tokens < 16 ? tokens : 16;
+  p.slots = (int)(slots < 1 ? 1 : slots < most ? slots : most);
+  return p;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t lora_workspace_bytes(int64_t tokens, int64_t out, int64_t k, int64_t rank) {
+  return align256(product_workspace_bytes(tokens, out, k, false)) + (size_t)plan_inner(tokens, k).splits * tokens * rank * 4;
+}
+
+int launch_w4a16_lora(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* wp, const uint8_t* wc,
+                      const float* ws2, int64_t out, const Adapters& ad, uint16_t* y, int64_t ldy, void* workspace,
+                      hipStream_t s) {
+  const InnerPlan plan = plan_inner(tokens, k);
+  float* u = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                      align256(product_workspace_bytes(tokens, out, k, false)));
+  const int64_t part = tokens * ad.rank;
+  const InnerArgs p{x, ldx, ad.ids, ad.a, ad.scale, u, part, (int)tokens, (int)k, ad.count, ad.rank, plan.splits};
+  const dim3 grid((unsigned)((tokens + plan.tokens - 1) / plan.tokens), plan.splits, plan.slots);
+  const auto run = [&](auto nt, auto rt) {
+    lora_inner_kernel<decltype(nt)::value, decltype(rt)::value><<<grid, 256, 0, s>>>(p);
+    return launch_status("lora_inner_kernel");
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  int st;
+  if (plan.tokens == 16) st = ad.rank <= 16 ? run(One{}, One{}) : run(One{}, Four{});
+  else st = ad.rank <= 16 ? run(Four{}, One{}) : run(Four{}, Four{});
+  if (st) return st;
+  const LoraTerm l{ad.ids, u, ad.b, ws2, part, ad.count, ad.rank, plan.splits};
+  return launch_matmul_w4a16(x, tokens, k, ldx, wp, wc, ws2, out, y, ldy, workspace, s, &l);
+}
+
+}  // namespace nvfp4

@@ -19,7 +19,7 @@
 // the time (52 to 55 vector instructions a KiB for up to four tokens).
 // Comparisons of variants below that do not say cold are of one set of weights.
 #include "common.hpp"
-#include "product_device.hpp"
+#include "lora_device.hpp"
 
 namespace nvfp4 {
 
@@ -72,10 +72,39 @@ __device__ __forceinline__ void store_rows(const ProductArgs& a, int row, int to
     if (row + e < a.out) dst[e] = to_bf16(tensor_scaled<KIND>(v[e], a));
 }
 
+// The same with an adapter's term.
+__device__ __forceinline__ void store_lora_rows(const ProductArgs& a, const LoraTerm& l, int row, int tok, f32x4 v) {
+  v *= *l.ws2;
+  const int id = l.ids[tok];
+  if (has_adapter(l, id)) {
+    const uint16_t* b = l.b + ((int64_t)id * a.out + row) * l.rank;
+    const int last = min(3, a.out - 1 - row);
+    for (int r = 0; r < l.rank; r += 8) {
+      float u[8];
+      load_u(l, tok, r, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 w = *reinterpret_cast<const uint4*>(b + min(e, last) * l.rank + r);
+        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[e] = __builtin_fmaf(u[2 * i], __uint_as_float(p[i] << 16), v[e]);
+          v[e] = __builtin_fmaf(u[2 * i + 1], __uint_as_float(p[i] & 0xFFFF0000u), v[e]);
+        }
+      }
+    }
+  }
+  uint16_t* dst = a.y + (int64_t)tok * a.ldy + row;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (row + e < a.out) dst[e] = to_bf16(v[e]);
+}
+
 // 4 NG tokens (the y coordinate's) against NVFP4 rows.  CU: waves that share a
 // CU, MW: waves of a workgroup, both at most.
-template <int KIND, bool ODD, int NG, int CU, int MW>
-__global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a) {
+// (with an adapter's term: few_tokens_kernel<..., LoraTerm>).
+template <int KIND, bool ODD, int NG, int CU, int MW, typename... Lora>
+__global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a, Lora... lora) {
   constexpr int TB = 4;
   __shared__ f32x4 part[MW * TB * NG * 16];
   constexpr int STAGE = KIND == kW4A16 ? 4096 : 1024;      // of a wave: tokens, then weights, change their order there
@@ -116,7 +145,9 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
   };
   auto done = [&](int t, int n, int q, int tj, f32x4 v) {
     const int row = t * 16 + q * 4, tok = tok0 + 4 * n + tj;
-    if (tok < a.tokens && row < a.out) store_rows<KIND>(a, row, tok, v);
+    if (tok >= a.tokens || row >= a.out) return;
+    if constexpr (sizeof...(Lora) > 0) (store_lora_rows(a, lora, row, tok, v), ...);
+    else store_rows<KIND>(a, row, tok, v);
   };
   stream_rows<ODD, NG, TB>(begin, end, a.k, quad_plan<1>(a.k, CU), group_row, x, part, lds_wave, rows_of, load_tokens,
                            take_tokens, done);
@@ -155,13 +186,13 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_mx_tokens_kernel(ProductA
                                  done);
 }
 
-template <int KIND, bool ODD, int NG, int CU>
-int run_few(const ProductArgs& a, hipStream_t s) {
+template <int KIND, bool ODD, int NG, int CU, typename... Lora>
+int run_few(const ProductArgs& a, hipStream_t s, const Lora&... lora) {
   const int waves = quad_plan<1>(a.k, CU).waves;
   const dim3 grid(few_grid((a.out + 15) / 16, waves, CU), (a.tokens + 4 * NG - 1) / (4 * NG));
-  if (waves <= 4) few_tokens_kernel<KIND, ODD, NG, CU, 4><<<grid, 64 * waves, 0, s>>>(a);
-  else if (CU == 8 || waves <= 8) few_tokens_kernel<KIND, ODD, NG, CU, 8><<<grid, 64 * waves, 0, s>>>(a);
-  else few_tokens_kernel<KIND, ODD, NG, CU, CU><<<grid, 64 * waves, 0, s>>>(a);
+  if (waves <= 4) few_tokens_kernel<KIND, ODD, NG, CU, 4, Lora...><<<grid, 64 * waves, 0, s>>>(a, lora...);
+  else if (CU == 8 || waves <= 8) few_tokens_kernel<KIND, ODD, NG, CU, 8, Lora...><<<grid, 64 * waves, 0, s>>>(a, lora...);
+  else few_tokens_kernel<KIND, ODD, NG, CU, CU, Lora...><<<grid, 64 * waves, 0, s>>>(a, lora...);
   return launch_status("few_tokens_kernel");
 }
 
@@ -175,8 +206,8 @@ int run_few_mx(const ProductArgs& a, hipStream_t s) {
   return launch_status("few_mx_tokens_kernel");
 }
 
-template <int KIND>
-int run(const ProductArgs& a, hipStream_t s) {
+template <int KIND, typename... Lora>
+int run(const ProductArgs& a, hipStream_t s, const Lora&... lora) {
   if constexpr (KIND == kMX) {
     // Two row tiles a step and 8 waves where those hold the channels, else two
     // quads a wave: 12288x4096, one token: 8.2 us against 9.5 with one tile and 16
@@ -190,10 +221,10 @@ int run(const ProductArgs& a, hipStream_t s) {
     // with 8 and 16 (two quads a wave and 12 waves: 1 more); sixteen 14.4 with 16
     // and 8 (as two workgroups of 8: half as much again).  k off 32 has few uses:
     // two sizes.
-    if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s) : run_few<KIND, true, 4, 8>(a, s);
-    if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s);
-    if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s);
-    return run_few<KIND, false, 4, 8>(a, s);
+    if (a.k % 32) return a.tokens <= 4 ? run_few<KIND, true, 1, 16>(a, s, lora...) : run_few<KIND, true, 4, 8>(a, s, lora...);
+    if (a.tokens <= 4) return run_few<KIND, false, 1, 16>(a, s, lora...);
+    if (a.tokens <= 8) return run_few<KIND, false, 2, 16>(a, s, lora...);
+    return run_few<KIND, false, 4, 8>(a, s, lora...);
   }
 }
 
@@ -220,12 +251,13 @@ size_t product_workspace_bytes(int64_t tokens, int64_t out, int64_t k, bool mx) 
 }
 
 int launch_matmul_w4a16(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx, const uint8_t* wp, const uint8_t* wc,
-                        const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s) {
+                        const float* ws2, int64_t out, uint16_t* y, int64_t ldy, void* workspace, hipStream_t s,
+                        const LoraTerm* lora) {
   if (use_tiles(tokens, out, k, false, ldx * 2))
-    return launch_tile_nv(x, ldx, nullptr, nullptr, nullptr, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s);
+    return launch_tile_nv(x, ldx, nullptr, nullptr, nullptr, tokens, k, wp, wc, ws2, out, y, ldy, workspace, s, lora);
   const ProductArgs a{reinterpret_cast<const uint8_t*>(x), nullptr, nullptr, wp, wc, ws2, ldx * 2, ldy, y, (int)tokens,
                       (int)out, (int)k};
-  return run<kW4A16>(a, s);
+  return lora ? run<kW4A16>(a, s, *lora) : run<kW4A16>(a, s);
 }
 
 int launch_matmul_w4a4(const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens, int64_t k,

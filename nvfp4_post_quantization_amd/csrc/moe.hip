@@ -144,17 +144,6 @@ __device__ __forceinline__ int place_of(int c, int j) {
   return (c & ~511) << 2 | ((c >> 3) & 3) << 9 | ((c >> 5) & 15) << 5 | j << 3 | (c & 7);
 }
 
-// v = a + b + c in bf16, 8 bits each, cut off and not rounded: a finite v stays
-// finite, and the differences are exact.  An infinity or NaN is in a alone.
-__device__ __forceinline__ void split(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
-  const uint32_t bits = __float_as_uint(v), top = bits & 0xFFFF0000u;
-  const float rest = (bits & 0x7F800000u) == 0x7F800000u ? 0.f : v - __uint_as_float(top);
-  const uint32_t middle = __float_as_uint(rest) & 0xFFFF0000u;
-  a = top >> 16;
-  b = middle >> 16;
-  c = __float_as_uint(rest - __uint_as_float(middle)) >> 16;
-}
-
 // h of 4 NG tokens (tok: the lane's of each four) of a job, for row tiles
 // t0 .. t1 - 1.  A tile's first two row groups are the gate rows of 8 channels,
 // the others their up rows, so that one pass over the tokens serves both.

@@ -1,0 +1,392 @@
+// Tokens sorted by expert and back.  A choice is a token and one of its top_k
+// places; the sorted rows are the choices whose id names an expert, by expert,
+// then by choice.
+//
+//   sort      order[row] = choice, place[choice] = row, offsets[expert]
+//   dispatch  xs[place[t][s]] = x[t]
+//   combine   y[t] = sum over s of w[t][s] ys[place[t][s]], s ascending
+//   gradient  dys[place[t][s]] = w[t][s] dy[t],  dw[t][s] = <dy[t], ys[place[t][s]]>;
+//             that of dispatch is combine without weights
+//
+// Rows move by token, not by row: a token is read (written) once and its top_k
+// rows are written (read), so that every byte crosses memory once.
+#include <type_traits>
+
+#include "layer.hpp"
+#include "product_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+// ---- sort --------------------------------------------------------------------
+//
+// A counting sort.  The choices are cut into as many chunks as workgroups, a
+// chunk into 16 runs, one a wave.  First launch: a count per chunk and expert.
+// Second: every workgroup adds up the counts (of all chunks for the experts'
+// first rows, of those before its own for its place in them), counts its runs,
+// and walks them 64 choices at a time; votes over the bits of the ids find the
+// lanes with the same expert, whose order gives the rows.  Counts are whole
+// numbers, so the result does not depend on who adds first.  One chunk needs no
+// first launch.
+constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
+constexpr int kSortChunk = 4096;         // choices of a workgroup, at least, where there are several
+constexpr int kSortAlone = 8192;         // up to this many one workgroup does it
+constexpr int kSortGroups = 256;
+
+struct SortArgs {
+  const int32_t* ids;
+  int32_t *order, *place, *offsets;
+  uint32_t* counts;                      // [groups][experts] where groups > 1
+  int64_t n;
+  int experts, groups;
+  TileList list;
+};
+
+__device__ __forceinline__ int64_t chunk_begin(const SortArgs& a, int g) { return a.n * g / a.groups; }
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  __shared__ uint32_t count[kMoeMaxExperts];
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t end = chunk_begin(a, blockIdx.x + 1);
+  for (int64_t i = chunk_begin(a, blockIdx.x) + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = a.ids[i];
+    if (e >= 0 && e < a.experts) atomicAdd(&count[e], 1u);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
+}
+
+// The sum of v over the threads before this one; all of it in `all`.  (part: one
+// word a wave; syncs.)
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t scan = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = __shfl_up(scan, d);
+    if (lane >= d) scan += o;
+  }
+  __syncthreads();
+  if (lane == 63) part[wave] = scan;
+  __syncthreads();
+  uint32_t before = scan - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    if (w < wave) before += part[w];
+    all += part[w];
+  }
+  return before;
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  __shared__ uint32_t next[kSortWaves * kMoeMaxExperts];         // [wave][expert]: counts, then rows
+  __shared__ uint32_t sum[2][kMoeMaxExperts];                    // all chunks', and those before this one
+  __shared__ uint32_t part[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts, g = blockIdx.x;
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) next[i] = 0;
+  if (tid < E) sum[0][tid] = sum[1][tid] = 0;
+  __syncthreads();
+  const int64_t begin = chunk_begin(a, g), end = chunk_begin(a, g + 1);
+  const int64_t run = ((end - begin + kSortThreads - 1) / kSortThreads) * 64;
+  const int64_t r0 = begin + wave * run, r1 = r0 + run < end ? r0 + run : end;
+  uint32_t* mine = next + wave * E;
+  for (int64_t i = r0 + lane; i < r1; i += 64) {
+    const int e = a.ids[i];
+    if (e >= 0 && e < E) atomicAdd(&mine[e], 1u);
+  }
+  if (a.groups > 1) {
+    // thread tid adds up expert tid % span, every (1024 / span)-th chunk
+    int span = 1;
+    while (span < E) span *= 2;
+    const int e = tid & (span - 1), step = kSortThreads / span;
+    if (e < E) {
+      uint32_t all = 0, before = 0;
+#pragma unroll 16
+      for (int c = tid / span; c < a.groups; c += step) {
+        const uint32_t v = a.counts[(int64_t)c * E + e];
+        all += v;
+        if (c < g) before += v;
+      }
+      atomicAdd(&sum[0][e], all);
+      atomicAdd(&sum[1][e], before);
+    }
+  }
+  __syncthreads();
+  uint32_t total = 0, rows;
+  if (tid < E) {
+    if (a.groups > 1) total = sum[0][tid];
+    else
+      for (int w = 0; w < kSortWaves; ++w) total += next[w * E + tid];
+  }
+  const uint32_t first = block_scan(total, part, rows);
+  if (tid < E) {
+    if (g == 0) a.offsets[tid] = (int32_t)first;
+    uint32_t row = first + sum[1][tid];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = next[w * E + tid];
+      next[w * E + tid] = row;
+      row += c;
+    }
+  }
+  if (g == 0 && tid == 0) a.offsets[E] = (int32_t)rows;
+  if (a.list.tiles && g == 0) {                                  // (the same way for all threads)
+    uint32_t tiles;
+    uint32_t at = block_scan((total + a.list.bm - 1) / a.list.bm, part, tiles);
+    for (uint32_t r = 0; r < total; r += a.list.bm, ++at)
+      a.list.tiles[at] = ExpertTile{tid, (int)(first + r), (int)min(total - r, (uint32_t)a.list.bm), 0};
+    if (tid == 0) *a.list.count = (int)tiles;
+  }
+  __syncthreads();
+  for (int64_t i = r0; i < r1; i += 64) {
+    const int64_t c = i + lane;
+    const int e = c < r1 ? a.ids[c] : -1;
+    const bool in = e >= 0 && e < E;
+    uint64_t same = __ballot(in);
+    for (int b = 0; (1 << b) < E; ++b) {
+      const uint64_t set = __ballot(e >> b & 1);
+      same &= e >> b & 1 ? set : ~set;
+    }
+    if (in) {
+      const uint32_t row = mine[e] + __popcll(same & ((1ull << lane) - 1));
+      if (same >> lane == 1) mine[e] = row + 1;                  // the last of them
+      a.order[row] = (int32_t)c;
+      a.place[c] = (int32_t)row;
+    } else if (c < r1) {
+      a.place[c] = -1;
+    }
+  }
+  for (int64_t r = rows + (int64_t)g * kSortThreads + tid; r < a.n; r += (int64_t)a.groups * kSortThreads) a.order[r] = -1;
+}
+
+// ---- rows --------------------------------------------------------------------
+
+constexpr int kRowThreads = 256;
+constexpr unsigned kRowGrid = 1 << 16;   // workgroups at most; more tokens go round by round
+
+// Threads of a token: a power of two, at most a workgroup.
+int row_threads(int64_t pieces) {
+  int n = 1;
+  while (n < kRowThreads && n < pieces) n *= 2;
+  return n;
+}
+unsigned row_grid(int64_t tokens, int threads) {
+  const int64_t per = kRowThreads / threads, want = (tokens + per - 1) / per;
+  return want < kRowGrid ? (unsigned)want : kRowGrid;
+}
+
+// rows of xs: n = tokens * top_k; places outside 0 .. n - 1 get nothing.
+template <typename V>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const uint8_t* x, int64_t tokens, int64_t pieces,
+                                                               int64_t ldx, const int32_t* place, int top_k, uint8_t* xs,
+                                                               int64_t ldxs, int threads) {
+  const int per = kRowThreads / threads, l = threadIdx.x % threads;
+  const int64_t n = tokens * top_k;
+  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / threads; t < tokens; t += (int64_t)gridDim.x * per) {
+    const V* src = reinterpret_cast<const V*>(x + t * ldx);
+    const int32_t* p = place + t * top_k;
+    for (int64_t i = l; i < pieces; i += threads) {
+      const V v = src[i];
+      for (int s = 0; s < top_k; ++s) {
+        const int64_t row = p[s];
+        if (row >= 0 && row < n) reinterpret_cast<V*>(xs + row * ldxs)[i] = v;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void add_piece(float (&acc)[8], const uint16_t* src, float w) {
+  const uint4 v = *reinterpret_cast<const uint4*>(src);
+  const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc[2 * e] = __builtin_fmaf(w, __uint_as_float(p[e] << 16), acc[2 * e]);
+    acc[2 * e + 1] = __builtin_fmaf(w, __uint_as_float(p[e] & 0xFFFF0000u), acc[2 * e + 1]);
+  }
+}
+__device__ __forceinline__ void add_piece(float (&acc)[8], const float* src, float w) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc[e] = __builtin_fmaf(w, a[e], acc[e]);
+    acc[4 + e] = __builtin_fmaf(w, b[e], acc[4 + e]);
+  }
+}
+__device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
+  uint32_t p[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = to_bf16(v[2 * e]) | (uint32_t)to_bf16(v[2 * e + 1]) << 16;
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+// Sums in fp32, one rounding.
+template <typename Y>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(const Y* ys, int64_t ldys, const int32_t* place,
+                                                              const float* weights, int64_t tokens, int top_k,
+                                                              int64_t pieces, uint16_t* y, int64_t ldy, int threads) {
+  const int per = kRowThreads / threads, l = threadIdx.x % threads;
+  const int64_t n = tokens * top_k;
+  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / threads; t < tokens; t += (int64_t)gridDim.x * per) {
+    const int32_t* p = place + t * top_k;
+    const float* w = weights + t * top_k;
+    for (int64_t i = l; i < pieces; i += threads) {
+      float acc[8] = {};
+#pragma unroll 4
+      for (int s = 0; s < top_k; ++s) {
+        const int64_t row = p[s];
+        if (row >= 0 && row < n) add_piece(acc, ys + row * ldys + i * 8, weights ? w[s] : 1.0f);
+      }
+      *reinterpret_cast<uint4*>(y + t * ldy + i * 8) = pack_bf16(acc);
+    }
+  }
+}
+
+// One token a workgroup (WAVES = 4) or a wave; K >= top_k sums of products.
+template <int K, int WAVES>
+__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* ys,
+                                                                   int64_t ldys, const int32_t* place,
+                                                                   const float* weights, int64_t tokens, int top_k,
+                                                                   int64_t pieces, uint16_t* dys, int64_t lddys,
+                                                                   float* dweights) {
+  __shared__ float part[4][K];
+  constexpr int PER = 4 / WAVES, THREADS = 64 * WAVES;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = threadIdx.x % THREADS;
+  const int64_t n = tokens * top_k;
+  for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < tokens; t0 += (int64_t)gridDim.x * PER) {
+    const int64_t t = t0 + wave / WAVES;
+    float dot[K];
+    int64_t row[K];
+    float w[K];
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+      dot[s] = 0.f;
+      row[s] = -1;
+      w[s] = 0.f;
+      if (s < top_k && t < tokens) {
+        const int64_t r = place[t * top_k + s];
+        if (r >= 0 && r < n) row[s] = r;
+        w[s] = weights[t * top_k + s];
+      }
+    }
+    if (t < tokens)
+      for (int64_t i = l; i < pieces; i += THREADS) {
+        const uint4 d = *reinterpret_cast<const uint4*>(dy + t * lddy + i * 8);
+        const uint32_t dp[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int s = 0; s < K; ++s) {
+          if (row[s] < 0) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(ys + row[s] * ldys + i * 8);
+          const uint32_t vp[4] = {v.x, v.y, v.z, v.w};
+          float g[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(dp[e] << 16), hi = __uint_as_float(dp[e] & 0xFFFF0000u);
+            dot[s] = __builtin_fmaf(lo, __uint_as_float(vp[e] << 16), dot[s]);
+            dot[s] = __builtin_fmaf(hi, __uint_as_float(vp[e] & 0xFFFF0000u), dot[s]);
+            g[2 * e] = w[s] * lo;
+            g[2 * e + 1] = w[s] * hi;
+          }
+          *reinterpret_cast<uint4*>(dys + row[s] * lddys + i * 8) = pack_bf16(g);
+        }
+      }
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+      if (s >= top_k) continue;
+      float v = dot[s];
+#pragma unroll
+      for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+      if (lane == 0) part[wave][s] = v;
+    }
+    __syncthreads();
+    if (l < top_k && t < tokens) {
+      float v = part[wave][l];
+#pragma unroll
+      for (int z = 1; z < WAVES; ++z) v += part[z][l];
+      dweights[t * top_k + l] = v;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename Y>
+int run_combine(const Y* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens, int top_k,
+                int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
+  const int threads = row_threads(cols / 8);
+  combine_kernel<Y><<<row_grid(tokens, threads), kRowThreads, 0, s>>>(ys, ldys, place, weights, tokens, top_k, cols / 8, y,
+                                                                     ldy, threads);
+  return launch_status("combine_kernel");
+}
+
+}  // namespace
+
+static int sort_groups(int64_t n) {
+  if (n <= kSortAlone) return 1;
+  const int64_t want = (n + kSortChunk - 1) / kSortChunk;
+  return (int)(want < kSortGroups ? want : kSortGroups);
+}
+
+size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts) {
+  const int g = sort_groups(choices);
+  return g > 1 ? (size_t)g * experts * 4 : 0;
+}
+
+int launch_moe_sort(const int32_t* ids, int64_t choices, int64_t experts, int32_t* order, int32_t* place,
+                    int32_t* offsets, void* workspace, const TileList& list, hipStream_t s) {
+  const SortArgs a{ids, order, place, offsets, static_cast<uint32_t*>(workspace), choices, (int)experts,
+                   sort_groups(choices), list};
+  if (a.groups > 1) {
+    sort_count_kernel<<<a.groups, kSortThreads, 0, s>>>(a);
+    const int st = launch_status("sort_count_kernel");
+    if (st) return st;
+  }
+  sort_place_kernel<<<a.groups, kSortThreads, 0, s>>>(a);
+  return launch_status("sort_place_kernel");
+}
+
+int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ldx, const int32_t* place, int top_k,
+                        void* xs, int64_t ldxs, hipStream_t s) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs) | (uint64_t)(row_bytes | ldx | ldxs);
+  const auto run = [&](auto v) {
+    using V = decltype(v);
+    const int64_t pieces = row_bytes / (int64_t)sizeof(V);
+    const int threads = row_threads(pieces);
+    dispatch_kernel<V><<<row_grid(tokens, threads), kRowThreads, 0, s>>>(
+        static_cast<const uint8_t*>(x), tokens, pieces, ldx, place, top_k, static_cast<uint8_t*>(xs), ldxs, threads);
+    return launch_status("dispatch_kernel");
+  };
+  if (all % 16 == 0) return run(uint4{});
+  if (all % 4 == 0) return run(uint32_t{});
+  return run(uint8_t{});
+}
+
+int launch_moe_combine(const uint16_t* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
+                       int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
+  return run_combine(ys, ldys, place, weights, tokens, top_k, cols, y, ldy, s);
+}
+int launch_moe_combine(const float* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
+                       int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
+  return run_combine(ys, ldys, place, weights, tokens, top_k, cols, y, ldy, s);
+}
+
+int launch_moe_combine_grad(const uint16_t* dy, int64_t lddy, const uint16_t* ys, int64_t ldys, const int32_t* place,
+                            const float* weights, int64_t tokens, int top_k, int64_t cols, uint16_t* dys, int64_t lddys,
+                            float* dweights, hipStream_t s) {
+  const int64_t pieces = cols / 8;
+  const auto run = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if (pieces > 64)
+      combine_grad_kernel<K, 4><<<row_grid(tokens, kRowThreads), kRowThreads, 0, s>>>(
+          dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys, lddys, dweights);
+    else
+      combine_grad_kernel<K, 1><<<row_grid(tokens, 64), kRowThreads, 0, s>>>(
+          dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys, lddys, dweights);
+    return launch_status("combine_grad_kernel");
+  };
+  if (top_k <= 4) return run(std::integral_constant<int, 4>{});
+  if (top_k <= 8) return run(std::integral_constant<int, 8>{});
+  return run(std::integral_constant<int, 16>{});
+}
+
+}  // namespace nvfp4

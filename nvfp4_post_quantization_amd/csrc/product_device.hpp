@@ -63,6 +63,17 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// v = a + b + c in bf16, 8 bits each, cut off and not rounded: a finite v stays
+// finite, and the differences are exact.  An infinity or NaN is in a alone.
+__device__ __forceinline__ void split(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint32_t bits = __float_as_uint(v), top = bits & 0xFFFF0000u;
+  const float rest = (bits & 0x7F800000u) == 0x7F800000u ? 0.f : v - __uint_as_float(top);
+  const uint32_t middle = __float_as_uint(rest) & 0xFFFF0000u;
+  a = top >> 16;
+  b = middle >> 16;
+  c = __float_as_uint(rest - __uint_as_float(middle)) >> 16;
+}
+
 // ---- a few tokens against many rows -----------------------------------------
 //
 // The weights are read once and everything else is small, so what matters is
