@@ -13,11 +13,12 @@ constexpr int64_t kMaxChoices = INT64_C(1) << 30;
 
 // A row tile of the expert layer: rows first .. first + rows - 1 are expert's.
 struct ExpertTile { int expert, first, rows, unused; };
-// Where the sort also writes the tiles of `bm` rows (none: NULL).
+// Where the sort also writes the tiles of up to `bm` rows (none: NULL), those of
+// more units first.
 struct TileList {
   ExpertTile* tiles;
   int* count;
-  int bm;
+  int bm, unit;
 };
 
 size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts);
@@ -25,11 +26,13 @@ int launch_moe_sort(const int32_t* ids, int64_t choices, int64_t experts, int32_
                     int32_t* offsets, void* workspace, const TileList& list, hipStream_t s);
 int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ldx, const int32_t* place, int top_k,
                         void* xs, int64_t ldxs, hipStream_t s);
-// ys: bf16 rows of ld elements, or float ones
 int launch_moe_combine(const uint16_t* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
                        int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s);
-int launch_moe_combine(const float* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
-                       int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s);
+// The same without weights of rows in fp16 with an exponent byte for every 32
+// columns: value = fp16 * 2^(byte - kHalfBias).
+constexpr int kHalfBias = 141;
+int launch_moe_combine_half(const uint16_t* ys, const uint8_t* exponents, const int32_t* place, int64_t tokens, int top_k,
+                            int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s);
 int launch_moe_combine_grad(const uint16_t* dy, int64_t lddy, const uint16_t* ys, int64_t ldys, const int32_t* place,
                             const float* weights, int64_t tokens, int top_k, int64_t cols, uint16_t* dys, int64_t lddys,
                             float* dweights, hipStream_t s);

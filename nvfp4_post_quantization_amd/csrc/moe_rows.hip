@@ -133,10 +133,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   }
   if (g == 0 && tid == 0) a.offsets[E] = (int32_t)rows;
   if (a.list.tiles && g == 0) {                                  // (the same way for all threads)
+    // whole tiles first, then the experts' last ones, those of most units first
+    const uint32_t bm = a.list.bm, whole = total / bm, rest = total % bm;
+    const uint32_t units = (rest + a.list.unit - 1) / a.list.unit;
     uint32_t tiles;
-    uint32_t at = block_scan((total + a.list.bm - 1) / a.list.bm, part, tiles);
-    for (uint32_t r = 0; r < total; r += a.list.bm, ++at)
-      a.list.tiles[at] = ExpertTile{tid, (int)(first + r), (int)min(total - r, (uint32_t)a.list.bm), 0};
+    uint32_t at = block_scan(whole, part, tiles);
+    for (uint32_t i = 0; i < whole; ++i) a.list.tiles[at + i] = ExpertTile{tid, (int)(first + i * bm), (int)bm, 0};
+    for (uint32_t u = bm / a.list.unit; u > 0; --u) {
+      uint32_t more;
+      at = tiles + block_scan(units == u ? 1 : 0, part, more);
+      if (units == u) a.list.tiles[at] = ExpertTile{tid, (int)(first + whole * bm), (int)rest, 0};
+      tiles += more;
+    }
     if (tid == 0) *a.list.count = (int)tiles;
   }
   __syncthreads();
@@ -164,56 +172,99 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 // ---- rows --------------------------------------------------------------------
 
 constexpr int kRowThreads = 256;
-constexpr unsigned kRowGrid = 1 << 16;   // workgroups at most; more tokens go round by round
+constexpr unsigned kRowGrid = 1 << 22;   // workgroups at most; more units go round by round
 
-// Threads of a token: a power of two, at most a workgroup.
-int row_threads(int64_t pieces) {
-  int n = 1;
-  while (n < kRowThreads && n < pieces) n *= 2;
-  return n;
+// A unit: a token and up to `threads` neighbouring pieces of its row, a thread each.
+struct Units {
+  int64_t count, chunks;                 // of all tokens, of one
+  int threads;
+};
+// Threads of a unit: the most that leave fewer than an eighth of them without a
+// piece (7168 bf16 columns, 896 pieces: 128, not 256).
+Units units_of(int64_t tokens, int64_t pieces) {
+  Units u{0, 0, kRowThreads};
+  for (; u.threads > 1; u.threads /= 2) {
+    const int64_t given = (pieces + u.threads - 1) / u.threads * u.threads;
+    if ((given - pieces) * 8 <= given) break;
+  }
+  u.chunks = (pieces + u.threads - 1) / u.threads;
+  u.count = tokens * u.chunks;
+  return u;
 }
-unsigned row_grid(int64_t tokens, int threads) {
-  const int64_t per = kRowThreads / threads, want = (tokens + per - 1) / per;
+unsigned unit_grid(const Units& u) {
+  const int64_t per = kRowThreads / u.threads, want = (u.count + per - 1) / per;
   return want < kRowGrid ? (unsigned)want : kRowGrid;
 }
+// f(token, piece) for the thread's units
+template <typename F>
+__device__ __forceinline__ void each_unit(const Units& u, int64_t pieces, F f) {
+  const int per = kRowThreads / u.threads, sub = threadIdx.x / u.threads, l = threadIdx.x % u.threads;
+  for (int64_t i = (int64_t)blockIdx.x * per + sub; i < u.count; i += (int64_t)gridDim.x * per) {
+    const int64_t t = u.count >> 32 ? i / u.chunks : (int64_t)((uint32_t)i / (uint32_t)u.chunks);
+    const int64_t piece = (i - t * u.chunks) * u.threads + l;
+    if (piece < pieces) f(t, piece);
+  }
+}
 
-// rows of xs: n = tokens * top_k; places outside 0 .. n - 1 get nothing.
-template <typename V>
-__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const uint8_t* x, int64_t tokens, int64_t pieces,
-                                                               int64_t ldx, const int32_t* place, int top_k, uint8_t* xs,
-                                                               int64_t ldxs, int threads) {
-  const int per = kRowThreads / threads, l = threadIdx.x % threads;
-  const int64_t n = tokens * top_k;
-  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / threads; t < tokens; t += (int64_t)gridDim.x * per) {
-    const V* src = reinterpret_cast<const V*>(x + t * ldx);
-    const int32_t* p = place + t * top_k;
-    for (int64_t i = l; i < pieces; i += threads) {
-      const V v = src[i];
-      for (int s = 0; s < top_k; ++s) {
-        const int64_t row = p[s];
-        if (row >= 0 && row < n) reinterpret_cast<V*>(xs + row * ldxs)[i] = v;
-      }
+// A token's rows among the n = tokens * top_k sorted ones; -1: none.
+template <int K>
+__device__ __forceinline__ void rows_of_token(const int32_t* place, int64_t t, int top_k, int64_t n, int64_t (&row)[K]) {
+#pragma unroll
+  for (int s = 0; s < K; ++s) {
+    const int64_t r = s < top_k ? place[t * top_k + s] : -1;
+    row[s] = r < n ? r : -1;
+  }
+}
+
+// The token's piece is read once and written to its rows.
+template <typename V, int K>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const uint8_t* x, Units u, int64_t pieces, int64_t ldx,
+                                                               const int32_t* place, int64_t n, int top_k, uint8_t* xs,
+                                                               int64_t ldxs) {
+  each_unit(u, pieces, [&](int64_t t, int64_t i) {
+    const V v = reinterpret_cast<const V*>(x + t * ldx)[i];
+    int64_t row[K];
+    rows_of_token(place, t, top_k, n, row);
+#pragma unroll
+    for (int s = 0; s < K; ++s)
+      if (row[s] >= 0) reinterpret_cast<V*>(xs + row[s] * ldxs)[i] = v;
+  });
+}
+
+// Rows that are added up, 8 columns a piece: bf16, or fp16 with a power of two for
+// every 32 columns (biased: value = fp16 * 2^(e - kHalfBias)).
+struct Bf16Rows {
+  const uint16_t* p;
+  int64_t ld;
+  struct Piece { uint4 v; };
+  __device__ __forceinline__ Piece load(int64_t row, int64_t i) const {
+    return Piece{*reinterpret_cast<const uint4*>(p + row * ld + i * 8)};
+  }
+  static __device__ __forceinline__ void add(float (&acc)[8], const Piece& x, float w) {
+    const uint32_t q[4] = {x.v.x, x.v.y, x.v.z, x.v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[2 * e] = __builtin_fmaf(w, __uint_as_float(q[e] << 16), acc[2 * e]);
+      acc[2 * e + 1] = __builtin_fmaf(w, __uint_as_float(q[e] & 0xFFFF0000u), acc[2 * e + 1]);
     }
   }
-}
+};
+struct HalfRows {
+  const uint16_t* p;
+  const uint8_t* e;
+  int64_t ld, lde;
+  struct Piece { uint4 v; int e; };
+  __device__ __forceinline__ Piece load(int64_t row, int64_t i) const {
+    return Piece{*reinterpret_cast<const uint4*>(p + row * ld + i * 8), e[row * lde + (i >> 2)]};
+  }
+  static __device__ __forceinline__ void add(float (&acc)[8], const Piece& x, float w) {
+    const float s = __builtin_amdgcn_ldexpf(w, x.e - kHalfBias);
+    const f16x8 h = __builtin_bit_cast(f16x8, x.v);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) acc[z] = __builtin_fmaf(s, (float)h[z], acc[z]);
+  }
+};
 
-__device__ __forceinline__ void add_piece(float (&acc)[8], const uint16_t* src, float w) {
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    acc[2 * e] = __builtin_fmaf(w, __uint_as_float(p[e] << 16), acc[2 * e]);
-    acc[2 * e + 1] = __builtin_fmaf(w, __uint_as_float(p[e] & 0xFFFF0000u), acc[2 * e + 1]);
-  }
-}
-__device__ __forceinline__ void add_piece(float (&acc)[8], const float* src, float w) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    acc[e] = __builtin_fmaf(w, a[e], acc[e]);
-    acc[4 + e] = __builtin_fmaf(w, b[e], acc[4 + e]);
-  }
-}
 __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
   uint32_t p[4];
 #pragma unroll
@@ -221,26 +272,38 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// Sums in fp32, one rounding.
-template <typename Y>
-__global__ __launch_bounds__(kRowThreads) void combine_kernel(const Y* ys, int64_t ldys, const int32_t* place,
-                                                              const float* weights, int64_t tokens, int top_k,
-                                                              int64_t pieces, uint16_t* y, int64_t ldy, int threads) {
-  const int per = kRowThreads / threads, l = threadIdx.x % threads;
-  const int64_t n = tokens * top_k;
-  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / threads; t < tokens; t += (int64_t)gridDim.x * per) {
-    const int32_t* p = place + t * top_k;
-    const float* w = weights + t * top_k;
-    for (int64_t i = l; i < pieces; i += threads) {
-      float acc[8] = {};
-#pragma unroll 4
-      for (int s = 0; s < top_k; ++s) {
-        const int64_t row = p[s];
-        if (row >= 0 && row < n) add_piece(acc, ys + row * ldys + i * 8, weights ? w[s] : 1.0f);
-      }
-      *reinterpret_cast<uint4*>(y + t * ldy + i * 8) = pack_bf16(acc);
+// Sums in fp32, one rounding.  All rows of a token are on their way before the
+// first is added.
+template <typename Rows, int K>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(Rows ys, Units u, int64_t pieces, const int32_t* place,
+                                                              const float* weights, int64_t n, int top_k, uint16_t* y,
+                                                              int64_t ldy) {
+  each_unit(u, pieces, [&](int64_t t, int64_t i) {
+    int64_t row[K];
+    float w[K];
+    typename Rows::Piece v[K];
+    rows_of_token(place, t, top_k, n, row);
+#pragma unroll
+    for (int s = 0; s < K; ++s) {
+      w[s] = weights && s < top_k ? weights[t * top_k + s] : 1.0f;
+      v[s] = ys.load(row[s] < 0 ? 0 : row[s], i);    // (there is a row 0; not added where it is not meant)
     }
-  }
+    float acc[8] = {};
+#pragma unroll
+    for (int s = 0; s < K; ++s)
+      if (row[s] >= 0) Rows::add(acc, v[s], w[s]);
+    *reinterpret_cast<uint4*>(y + t * ldy + i * 8) = pack_bf16(acc);
+  });
+}
+
+// f(K) for the least K of 1, 2, 4, 8, 16 that holds top_k
+template <typename F>
+int with_places(int top_k, F f) {
+  if (top_k <= 1) return f(std::integral_constant<int, 1>{});
+  if (top_k <= 2) return f(std::integral_constant<int, 2>{});
+  if (top_k <= 4) return f(std::integral_constant<int, 4>{});
+  if (top_k <= 8) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
 }
 
 // One token a workgroup (WAVES = 4) or a wave; K >= top_k sums of products.
@@ -259,16 +322,11 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(const uint16_
     float dot[K];
     int64_t row[K];
     float w[K];
+    rows_of_token(place, min(t, tokens - 1), top_k, n, row);
 #pragma unroll
     for (int s = 0; s < K; ++s) {
       dot[s] = 0.f;
-      row[s] = -1;
-      w[s] = 0.f;
-      if (s < top_k && t < tokens) {
-        const int64_t r = place[t * top_k + s];
-        if (r >= 0 && r < n) row[s] = r;
-        w[s] = weights[t * top_k + s];
-      }
+      w[s] = s < top_k && t < tokens ? weights[t * top_k + s] : 0.f;
     }
     if (t < tokens)
       for (int64_t i = l; i < pieces; i += THREADS) {
@@ -310,13 +368,16 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(const uint16_
   }
 }
 
-template <typename Y>
-int run_combine(const Y* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens, int top_k,
-                int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
-  const int threads = row_threads(cols / 8);
-  combine_kernel<Y><<<row_grid(tokens, threads), kRowThreads, 0, s>>>(ys, ldys, place, weights, tokens, top_k, cols / 8, y,
-                                                                     ldy, threads);
-  return launch_status("combine_kernel");
+template <typename Rows>
+int run_combine(const Rows& ys, const int32_t* place, const float* weights, int64_t tokens, int top_k, int64_t cols,
+                uint16_t* y, int64_t ldy, hipStream_t s) {
+  const int64_t pieces = cols / 8;
+  const Units u = units_of(tokens, pieces);
+  return with_places(top_k, [&](auto k) {
+    combine_kernel<Rows, decltype(k)::value><<<unit_grid(u), kRowThreads, 0, s>>>(ys, u, pieces, place, weights,
+                                                                                 tokens * top_k, top_k, y, ldy);
+    return launch_status("combine_kernel");
+  });
 }
 
 }  // namespace
@@ -351,10 +412,12 @@ int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_
   const auto run = [&](auto v) {
     using V = decltype(v);
     const int64_t pieces = row_bytes / (int64_t)sizeof(V);
-    const int threads = row_threads(pieces);
-    dispatch_kernel<V><<<row_grid(tokens, threads), kRowThreads, 0, s>>>(
-        static_cast<const uint8_t*>(x), tokens, pieces, ldx, place, top_k, static_cast<uint8_t*>(xs), ldxs, threads);
-    return launch_status("dispatch_kernel");
+    const Units u = units_of(tokens, pieces);
+    return with_places(top_k, [&](auto k) {
+      dispatch_kernel<V, decltype(k)::value><<<unit_grid(u), kRowThreads, 0, s>>>(
+          static_cast<const uint8_t*>(x), u, pieces, ldx, place, tokens * top_k, top_k, static_cast<uint8_t*>(xs), ldxs);
+      return launch_status("dispatch_kernel");
+    });
   };
   if (all % 16 == 0) return run(uint4{});
   if (all % 4 == 0) return run(uint32_t{});
@@ -363,30 +426,30 @@ int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_
 
 int launch_moe_combine(const uint16_t* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
                        int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
-  return run_combine(ys, ldys, place, weights, tokens, top_k, cols, y, ldy, s);
+  return run_combine(Bf16Rows{ys, ldys}, place, weights, tokens, top_k, cols, y, ldy, s);
 }
-int launch_moe_combine(const float* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
-                       int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
-  return run_combine(ys, ldys, place, weights, tokens, top_k, cols, y, ldy, s);
+int launch_moe_combine_half(const uint16_t* ys, const uint8_t* exponents, const int32_t* place, int64_t tokens, int top_k,
+                            int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
+  return run_combine(HalfRows{ys, exponents, cols, (cols + 31) / 32}, place, nullptr, tokens, top_k, cols, y, ldy, s);
 }
 
 int launch_moe_combine_grad(const uint16_t* dy, int64_t lddy, const uint16_t* ys, int64_t ldys, const int32_t* place,
                             const float* weights, int64_t tokens, int top_k, int64_t cols, uint16_t* dys, int64_t lddys,
                             float* dweights, hipStream_t s) {
   const int64_t pieces = cols / 8;
-  const auto run = [&](auto k) {
+  return with_places(top_k, [&](auto k) {
     constexpr int K = decltype(k)::value;
-    if (pieces > 64)
-      combine_grad_kernel<K, 4><<<row_grid(tokens, kRowThreads), kRowThreads, 0, s>>>(
-          dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys, lddys, dweights);
+    const int per = pieces > 64 ? 1 : 4;             // tokens of a workgroup
+    const int64_t want = (tokens + per - 1) / per;
+    const unsigned grid = want < kRowGrid ? (unsigned)want : kRowGrid;
+    if (per == 1)
+      combine_grad_kernel<K, 4><<<grid, kRowThreads, 0, s>>>(dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys,
+                                                             lddys, dweights);
     else
-      combine_grad_kernel<K, 1><<<row_grid(tokens, 64), kRowThreads, 0, s>>>(
-          dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys, lddys, dweights);
+      combine_grad_kernel<K, 1><<<grid, kRowThreads, 0, s>>>(dy, lddy, ys, ldys, place, weights, tokens, top_k, pieces, dys,
+                                                             lddys, dweights);
     return launch_status("combine_grad_kernel");
-  };
-  if (top_k <= 4) return run(std::integral_constant<int, 4>{});
-  if (top_k <= 8) return run(std::integral_constant<int, 8>{});
-  return run(std::integral_constant<int, 16>{});
+  });
 }
 
 }  // namespace nvfp4

@@ -57,10 +57,11 @@ def moe_combine_grad(dy, ys, place, weights):
     return dys, dw, mag
 
 
-def moe_forward_sorted(x, ids, weights, w13, w2, eps_sum, eps_h):
+def moe_forward_sorted(x, ids, weights, w13, w2, eps_sum, eps_h, eps_row):
     """(y, bound): product.moe_forward expert by expert, and how far off y may be
     before its own rounding where a sum of n products may be off by n eps_sum of
-    the sum of their magnitudes and silu * up by eps_h of its value.
+    the sum of their magnitudes, silu * up by eps_h of its value and an expert's
+    row by eps_row of its own (and 2^-28 of that of the row's largest value).
 
     silu' lies in [-0.1, 1.1]: an error d of gate moves silu by at most 1.1 d."""
     y, off = np.zeros_like(x), np.zeros_like(x)
@@ -76,9 +77,12 @@ def moe_forward_sorted(x, ids, weights, w13, w2, eps_sum, eps_h):
         h = silu(gate) * up
         dh = (1.1 * dg * (np.abs(up) + du) + np.abs(silu(gate)) * du)
         dh += eps_h * (np.abs(h) + dh)
-        np.add.at(y, t, w * (h @ w2[e].T))
+        row = h @ w2[e].T
+        np.add.at(y, t, w * row)
         mag = (np.abs(h) + dh) @ np.abs(w2[e]).T
-        np.add.at(off, t, np.abs(w) * (dh @ np.abs(w2[e]).T + (inter + ids.shape[1] + 3) * eps_sum * mag))
+        d = dh @ np.abs(w2[e]).T + (inter + ids.shape[1] + 3) * eps_sum * mag
+        d += eps_row * (np.abs(row) + d + 2.0 ** -28 * (np.abs(row) + d).max(1, keepdims=True))
+        np.add.at(off, t, np.abs(w) * d)
     return y, off
 
 
