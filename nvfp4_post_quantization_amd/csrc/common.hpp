@@ -110,6 +110,7 @@ int launch_tile_mx(const uint8_t* xp, const uint8_t* xe, int64_t tokens, int64_t
 int launch_tile_nv(const uint16_t* x, int64_t ldx, const uint8_t* xp, const uint8_t* xc, const float* xs2, int64_t tokens,
                    int64_t k, const uint8_t* wp, const uint8_t* wc, const float* ws2, int64_t out, uint16_t* y,
                    int64_t ldy, void* workspace, hipStream_t s, const LoraTerm* lora = nullptr);
+constexpr int kMaxRank = 256;            // of an adapter
 // mixture-of-experts layer: limits of one call
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopK = 16;

@@ -136,7 +136,7 @@ int nvfp4_moe_forward_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, 
 static int check_lora(int64_t tokens, int64_t out, int64_t k, int64_t rank, int64_t ldy) {
   const int st = check_product(tokens, out, k, 16, ldy);
   if (st) return st;
-  return rank < 8 || rank > 256 || rank % 8 ? NVFP4_ERR_BAD_INPUT : NVFP4_OK;
+  return rank < 8 || rank > kMaxRank || rank % 8 ? NVFP4_ERR_BAD_INPUT : NVFP4_OK;
 }
 
 size_t nvfp4_matmul_w4a16_lora_workspace_bytes(int64_t tokens, int64_t out_features, int64_t k, int64_t rank) {

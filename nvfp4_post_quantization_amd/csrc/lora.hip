@@ -11,7 +11,7 @@
 // tokens one after another on the 16x16x32 bf16 instruction, whose columns are the
 // tokens: each column of the result belongs to one token, which takes that of its
 // own adapter.  Where tokens follow in runs of a request that is one pass over x.
-// The four waves of a workgroup add up their channels in LDS; what other
+// The waves of a workgroup add up their channels in LDS; what other
 // workgroups have of the same tokens are the splits that the product adds up.
 #include "layer.hpp"
 #include "lora_device.hpp"
@@ -21,7 +21,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kCus = 256;
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 4, kFewSplits = 16;      // up to 16 tokens: the most
 
 struct InnerArgs {
   const uint16_t* x;
@@ -34,20 +34,20 @@ struct InnerArgs {
   int tokens, k, count, rank, splits;
 };
 
-__device__ __forceinline__ f32x4 mfma16_bf16(uint4 a, uint4 b, f32x4 c) {
+__device__ __forceinline__ f32x4 mfma16_bf16(i32x4 a, i32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // 16 NT tokens (x), a split of the channels (y), every gridDim.z-th of their
-// adapters (z).  RT tiles of 16 rows of A at a time.
-template <int NT, int RT>
-__global__ __launch_bounds__(256) void lora_inner_kernel(InnerArgs p) {
-  __shared__ __attribute__((aligned(16))) f32x4 part[4][NT * RT][64];
+// adapters (z).  RT tiles of 16 rows of A at a time, NB steps of 32 channels.
+template <int NT, int RT, int NB, int W>
+__global__ __launch_bounds__(64 * W) void lora_inner_kernel(InnerArgs p) {
+  __shared__ __attribute__((aligned(16))) f32x4 part[W][NT * RT][64];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = blockIdx.x * 16 * NT;
   // the wave's steps of 32 channels
-  const int steps = (p.k + 31) >> 5, parts = p.splits * 4, at = blockIdx.y * 4 + wave;
+  const int steps = (p.k + 31) >> 5, parts = p.splits * W, at = blockIdx.y * W + wave;
   const int s0 = (int)((int64_t)steps * at / parts), s1 = (int)((int64_t)steps * (at + 1) / parts);
   int id[NT];
   const uint16_t* x[NT];
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(InnerArgs p) {
     live[n] = __ballot(id[n] >= 0);
     x[n] = p.x + (int64_t)min(t, p.tokens - 1) * p.ldx + q * 8;
   }
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const i32x4 zero = {0, 0, 0, 0};
   for (int turn = 0;; ++turn) {
     // the next adapter: that of the first token that has had none
     int a = -1;
@@ -80,40 +80,57 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(InnerArgs p) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)                   // (rows past the last: it again, their results are not stored)
         rows[r] = p.a + ((int64_t)a * p.rank + min(r0 + 16 * r + l16, p.rank - 1)) * p.k + q * 8;
+      const float scale = p.scale[a];
       f32x4 acc[NT][RT];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < RT; ++r) acc[n][r] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const auto step = [&](int s, bool in) {
-        uint4 w[RT];
+      // NB steps are on their way at a time; the last ones, where k or the wave's steps
+      // end, load what there is and take zeros for the rest
+      const auto steps_from = [&](int s, auto all) {
+        i32x4 w[NB][RT], v[NB][NT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) w[r] = in ? *reinterpret_cast<const uint4*>(rows[r] + s * 32) : zero;
+        for (int i = 0; i < NB; ++i) {
+          const int c = (s + i) * 32, at = all ? c : min(c, p.k - 8 - q * 8);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (!has[n]) continue;
-          const uint4 v = in ? *reinterpret_cast<const uint4*>(x[n] + s * 32) : zero;
+          for (int r = 0; r < RT; ++r) w[i][r] = *reinterpret_cast<const i32x4*>(rows[r] + at);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) acc[n][r] = mfma16_bf16(w[r], v, acc[n][r]);
+          for (int n = 0; n < NT; ++n) v[i][n] = *reinterpret_cast<const i32x4*>(x[n] + at);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          if (!all) {
+            const bool in = s + i < s1 && (s + i) * 32 + q * 8 < p.k;        // (k is a multiple of 16)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) w[i][r] = in ? w[i][r] : zero;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) v[i][n] = in ? v[i][n] : zero;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (has[n])
+#pragma unroll
+              for (int r = 0; r < RT; ++r) acc[n][r] = mfma16_bf16(w[i][r], v[i][n], acc[n][r]);
         }
       };
-      const int whole = min(s1, p.k >> 5);
       int s = s0;
-      for (; s < whole; ++s) step(s, true);
-      if (s < s1) step(s, s * 32 + q * 8 < p.k);     // (k is a multiple of 16)
+      if constexpr (NT > 1)                          // (few steps a wave: one loop, for its code comes from memory too)
+        for (; s + NB <= min(s1, p.k >> 5); s += NB) steps_from(s, std::true_type{});
+#pragma unroll 1
+      for (; s < s1; s += NB) steps_from(s, std::false_type{});
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < RT; ++r) part[wave][n * RT + r][lane] = acc[n][r];
       __syncthreads();
-      const float scale = p.scale[a];
-      for (int i = threadIdx.x; i < NT * RT * 64; i += 256) {
+      for (int i = threadIdx.x; i < NT * RT * 64; i += 64 * W) {
         const int l = i & 63, n = (i >> 6) / RT, r = r0 + 16 * ((i >> 6) % RT) + 4 * (l >> 4);
         const int t = t0 + 16 * n + (l & 15);
         if (r >= p.rank || t >= p.tokens || p.ids[t] != a) continue;
         f32x4 v = part[0][i >> 6][l];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) v += part[w][i >> 6][l];
+        for (int w = 1; w < W; ++w) v += part[w][i >> 6][l];
         *reinterpret_cast<f32x4*>(p.u + blockIdx.y * p.part + (int64_t)t * p.rank + r) = v * scale;
       }
       __syncthreads();
@@ -121,16 +138,20 @@ __global__ __launch_bounds__(256) void lora_inner_kernel(InnerArgs p) {
   }
 }
 
-struct InnerPlan { int tokens, splits, slots; };     // tokens of a workgroup, splits of the channels, of the adapters
+// Tokens and waves of a workgroup, splits of the channels (each wave has two steps
+// or more), slots of a token group's adapters.
+struct InnerPlan { int tokens, waves, splits, slots; };
 InnerPlan plan_inner(int64_t tokens, int64_t k) {
   InnerPlan p;
   p.tokens = tokens <= 1024 ? 16 : 64;
-  const int64_t groups = (tokens + p.tokens - 1) / p.tokens, steps = (k + 127) / 128;
-  const int64_t want = (2 * kCus + groups - 1) / groups;
-  p.splits = (int)(want < kMaxSplits ? want : kMaxSplits);
-  if (p.splits > steps) p.splits = (int)steps;
-  const int64_t slots = want / p.splits, most = tokens < 16 ? tokens : 16;
-  p.slots = (int)(slots < 1 ? 1 : slots < most ? slots : most);
+  p.waves = tokens <= 1024 ? 8 : 4;
+  const int64_t groups = (tokens + p.tokens - 1) / p.tokens, want = (2 * kCus + groups - 1) / groups;
+  int64_t splits = k / (64 * p.waves);
+  if (splits > want) splits = want;
+  if (splits > (groups > 1 ? kMaxSplits : kFewSplits)) splits = groups > 1 ? kMaxSplits : kFewSplits;
+  p.splits = splits < 1 ? 1 : (int)splits;
+  const int64_t slots = want / p.splits, adapters = tokens < 16 ? tokens : 16;
+  p.slots = (int)(slots < 1 ? 1 : slots < adapters ? slots : adapters);
   return p;
 }
 
@@ -151,15 +172,14 @@ int launch_w4a16_lora(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx,
   const int64_t part = tokens * ad.rank;
   const InnerArgs p{x, ldx, ad.ids, ad.a, ad.scale, u, part, (int)tokens, (int)k, ad.count, ad.rank, plan.splits};
   const dim3 grid((unsigned)((tokens + plan.tokens - 1) / plan.tokens), plan.splits, plan.slots);
-  const auto run = [&](auto nt, auto rt) {
-    lora_inner_kernel<decltype(nt)::value, decltype(rt)::value><<<grid, 256, 0, s>>>(p);
-    return launch_status("lora_inner_kernel");
-  };
-  using One = std::integral_constant<int, 1>;
-  using Four = std::integral_constant<int, 4>;
-  int st;
-  if (plan.tokens == 16) st = ad.rank <= 16 ? run(One{}, One{}) : run(One{}, Four{});
-  else st = ad.rank <= 16 ? run(Four{}, One{}) : run(Four{}, Four{});
+  if (plan.tokens == 16) {
+    if (ad.rank <= 16) lora_inner_kernel<1, 1, 4, 8><<<grid, 512, 0, s>>>(p);
+    else lora_inner_kernel<1, 4, 4, 8><<<grid, 512, 0, s>>>(p);
+  } else {
+    if (ad.rank <= 16) lora_inner_kernel<4, 1, 4, 4><<<grid, 256, 0, s>>>(p);
+    else lora_inner_kernel<4, 4, 2, 4><<<grid, 256, 0, s>>>(p);
+  }
+  const int st = launch_status("lora_inner_kernel");
   if (st) return st;
   const LoraTerm l{ad.ids, u, ad.b, ws2, part, ad.count, ad.rank, plan.splits};
   return launch_matmul_w4a16(x, tokens, k, ldx, wp, wc, ws2, out, y, ldy, workspace, s, &l);

@@ -72,24 +72,44 @@ __device__ __forceinline__ void store_rows(const ProductArgs& a, int row, int to
     if (row + e < a.out) dst[e] = to_bf16(tensor_scaled<KIND>(v[e], a));
 }
 
-// The same with an adapter's term.
-__device__ __forceinline__ void store_lora_rows(const ProductArgs& a, const LoraTerm& l, int row, int tok, f32x4 v) {
-  v *= *l.ws2;
-  const int id = l.ids[tok];
+// u of `rows` tokens from tok0 on, in as many shares [share][row][rank] as fit and
+// splits there are, so that more threads have some of them to wait for (what reads
+// them comes after a barrier).
+__device__ __forceinline__ int u_shares(const LoraTerm& l) { return min(l.splits, kMaxRank / l.rank); }
+__device__ __forceinline__ void gather_u(const LoraTerm& l, int tok0, int rows, int tokens, float* u) {
+  const int shares = u_shares(l), all = rows * l.rank;
+  for (int i = threadIdx.x * 4; i < shares * all; i += blockDim.x * 4) {
+    const int share = i / all, c = i - share * all, at = c / l.rank, t = tok0 + at;
+    if (t < tokens) *reinterpret_cast<f32x4*>(u + i) = load_u(l, t, c - at * l.rank, share, shares);
+  }
+}
+
+// store_rows with a term of adapter id; u: the token's inner sums in LDS, of `rows`.
+__device__ __forceinline__ void store_lora_rows(const ProductArgs& a, const LoraTerm& l, float ws2, int id, const float* u,
+                                                int rows, int row, int tok, f32x4 v) {
+  v *= ws2;
   if (has_adapter(l, id)) {
     const uint16_t* b = l.b + ((int64_t)id * a.out + row) * l.rank;
-    const int last = min(3, a.out - 1 - row);
+    const int last = min(3, a.out - 1 - row), shares = u_shares(l);
+#pragma unroll 1
     for (int r = 0; r < l.rank; r += 8) {
-      float u[8];
-      load_u(l, tok, r, u);
+      uint4 w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint4*>(b + min(e, last) * l.rank + r);
+      f32x4 u0 = {0.f, 0.f, 0.f, 0.f}, u1 = u0;
+      const float* share = u + r;
+#pragma unroll 4
+      for (int z = 0; z < shares; ++z, share += rows * l.rank) {
+        u0 += *reinterpret_cast<const f32x4*>(share);
+        u1 += *reinterpret_cast<const f32x4*>(share + 4);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint4 w = *reinterpret_cast<const uint4*>(b + min(e, last) * l.rank + r);
-        const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t p[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[e] = __builtin_fmaf(u[2 * i], __uint_as_float(p[i] << 16), v[e]);
-          v[e] = __builtin_fmaf(u[2 * i + 1], __uint_as_float(p[i] & 0xFFFF0000u), v[e]);
+          v[e] = __builtin_fmaf(i < 2 ? u0[2 * i] : u1[2 * i - 4], __uint_as_float(p[i] << 16), v[e]);
+          v[e] = __builtin_fmaf(i < 2 ? u0[2 * i + 1] : u1[2 * i - 3], __uint_as_float(p[i] & 0xFFFF0000u), v[e]);
         }
       }
     }
@@ -99,16 +119,19 @@ __device__ __forceinline__ void store_lora_rows(const ProductArgs& a, const Lora
   for (int e = 0; e < 4; ++e)
     if (row + e < a.out) dst[e] = to_bf16(v[e]);
 }
-
 // 4 NG tokens (the y coordinate's) against NVFP4 rows.  CU: waves that share a
 // CU, MW: waves of a workgroup, both at most.
-// (with an adapter's term: few_tokens_kernel<..., LoraTerm>).
+// With a LoraTerm an adapter's term is added.  What that needs is asked for behind
+// the first weights: the tokens' u, and a word of every cache line of the rows of B
+// that the thread will want for its first results, which then are near.
 template <int KIND, bool ODD, int NG, int CU, int MW, typename... Lora>
 __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs a, Lora... lora) {
-  constexpr int TB = 4;
-  __shared__ f32x4 part[MW * TB * NG * 16];
+  constexpr int TB = 4, SLOTS = NG * 16;
+  constexpr bool LORA = sizeof...(Lora) > 0;
+  __shared__ f32x4 part[MW * TB * SLOTS];
   constexpr int STAGE = KIND == kW4A16 ? 4096 : 1024;      // of a wave: tokens, then weights, change their order there
   __shared__ __attribute__((aligned(16))) uint8_t stage[MW * STAGE];
+  __shared__ __attribute__((aligned(16))) float u[LORA ? 4 * NG * kMaxRank : 1];
   const int lane = threadIdx.x & 63;
   uint8_t* const lds_wave = stage + (threadIdx.x >> 6) * STAGE;
   const int tok0 = blockIdx.y * 4 * NG;
@@ -117,6 +140,17 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
   tile_run((a.out + 15) >> 4, begin, end);
   const uint32_t group_row[4] = {0, 4, 8, 12};
   Chunk x[1][NG];
+  // a thread's results are all of one token (its slots are 64 * waves apart, a
+  // multiple of SLOTS)
+  constexpr int LINES = 2;
+  int id = -1;
+  float ws2 = 0.f;
+  uint32_t near[LINES] = {};
+  if constexpr (LORA) {
+    const LoraTerm& l = (lora, ...);
+    id = l.ids[min(tok0 + (int)(threadIdx.x / 16 % NG * 4 + (threadIdx.x & 3)), a.tokens - 1)];
+    ws2 = *l.ws2;
+  }
   auto rows_of = [&](int t) {
     const int row = t * 16;
     const uint32_t rows = min(16, a.out - row);
@@ -136,21 +170,40 @@ __global__ __launch_bounds__(64 * MW, CU / 4) void few_tokens_kernel(ProductArgs
       }
     }
   };
+  bool first = true;
   auto take_tokens = [&]() {
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       if constexpr (KIND == kW4A16) pieces_to_chunk(x[0][n], lds_wave);
       else expand_chunk(x[0][n], packed[n].arranged(lds_wave));
     }
+    if constexpr (LORA) {
+      const LoraTerm& l = (lora, ...);
+      if (first) {
+        gather_u(l, tok0, 4 * NG, a.tokens, u);
+        const int row = (begin + (int)threadIdx.x / SLOTS) * 16 + (threadIdx.x >> 2 & 3) * 4;
+        if (has_adapter(l, id) && row < a.out)
+#pragma unroll
+          for (int z = 0; z < LINES; ++z)
+            if (z * 64 < 4 * l.rank)
+              near[z] = *reinterpret_cast<const uint32_t*>(
+                  l.b + min(((int64_t)id * a.out + row) * l.rank + z * 64, ((int64_t)(id + 1) * a.out) * l.rank - 2));
+      }
+      first = false;
+    }
   };
   auto done = [&](int t, int n, int q, int tj, f32x4 v) {
     const int row = t * 16 + q * 4, tok = tok0 + 4 * n + tj;
     if (tok >= a.tokens || row >= a.out) return;
-    if constexpr (sizeof...(Lora) > 0) (store_lora_rows(a, lora, row, tok, v), ...);
+    if constexpr (LORA) store_lora_rows(a, (lora, ...), ws2, id, u + (4 * n + tj) * (lora.rank, ...), 4 * NG, row, tok,
+                                          v);
     else store_rows<KIND>(a, row, tok, v);
   };
   stream_rows<ODD, NG, TB>(begin, end, a.k, quad_plan<1>(a.k, CU), group_row, x, part, lds_wave, rows_of, load_tokens,
                            take_tokens, done);
+  if constexpr (LORA)
+#pragma unroll
+    for (int z = 0; z < LINES; ++z) asm volatile("" ::"v"(near[z]));
 }
 
 // 16 NT tokens against MXFP4 rows.

@@ -112,7 +112,8 @@ __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_up_tile_kernel(SortedA
         bx, bw, a.hidden, 0, (a.hidden + 63) >> 6,
         [&](int r) { return (uint32_t)(order[min(r, t.rows - 1)] / a.top_k) * (uint32_t)a.ldx; },
         [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; }, scales,
-        lds, [&](const f32x16 (&acc)[TN][TM], int wm, int wn, int wave) {
+        lds, [&](const f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
+          if (!multiplies) return;
           const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
           const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + wn * TN * 16 + piece * 8;
           uint8_t* mine = lds + wave * 32 * PITCH;
@@ -190,7 +191,8 @@ __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_down_tile_kernel(Sorte
     nv_tile<false, TM, TN, F::WM, F::WN, F::NL, F::ahead(TM)>(
         bx, bw, a.inter, 0, (a.inter + 63) >> 6, [&](int r) { return (uint32_t)min(r, t.rows - 1) * ldh; },
         [&](int r) { return (uint32_t)min(r, rows_w - 1) * ldw; }, scales, lds,
-        [&](f32x16 (&acc)[TN][TM], int wm, int wn, int wave) {
+        [&](f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
+          if (!multiplies) return;
           const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
           const int piece = lane % LANES, row0 = lane / LANES, ob = o0 + wn * TN * 32, o = ob + piece * 8;
           uint8_t* mine = lds + wave * 32 * PITCH;

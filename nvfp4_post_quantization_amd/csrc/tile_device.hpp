@@ -342,8 +342,9 @@ __device__ __forceinline__ int loader_of() {
 //                  past the tile's last: any row, their results are not stored),
 //   scales         the weights' (made with where they go in lds: NBUF * STAGE)
 //   lds            NvTile::LDS bytes
-//   finish(acc, wm, wn, wave)  called by the waves that multiply, once the stages
-//                  are done with; acc[n][m] is what store_tiles takes
+//   finish(acc, wm, wn, wave, multiplies)  called by all waves once the stages are
+//                  done with; acc[n][m], of those that multiply, is what store_tiles
+//                  takes
 // Lane half h of an instruction takes channels 32 h + 8 j .. + 7 of the stage
 // at step j, so that a lane's weights of a stage are one 16-byte piece.
 template <bool F16, int TM, int TN, int WM, int WN, int NL, int AHEAD, typename Scales, typename XAt, typename WAt,
@@ -464,7 +465,7 @@ __device__ __forceinline__ void nv_tile(i32x4 bx, i32x4 bw, int k, int s_begin, 
     });
   }
   __syncthreads();                                                // the stages are done with
-  if (multiplies) finish(acc, wm, wn, wave);
+  finish(acc, wm, wn, wave, multiplies);
 }
 
 }  // namespace nvfp4
