@@ -11,19 +11,19 @@ namespace nvfp4 {
 // their byte offsets in int32 tables stay clear of 2^31.
 constexpr int64_t kMaxChoices = INT64_C(1) << 30;
 
-// A row tile of the expert layer: rows first .. first + rows - 1 are expert's.
-struct ExpertTile { int expert, first, rows, unused; };
-// Where the sort also writes the tiles of up to `bm` rows (none: NULL), those of
+// A band of the expert layer: rows first .. first + rows - 1 are expert's.
+struct ExpertBand { int expert, first, rows, unused; };
+// Where the sort also writes the bands of up to `rows` rows (none: NULL), those of
 // more units first.
-struct TileList {
-  ExpertTile* tiles;
+struct BandList {
+  ExpertBand* bands;
   int* count;
-  int bm, unit;
+  int rows, unit;
 };
 
 size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts);
 int launch_moe_sort(const int32_t* ids, int64_t choices, int64_t experts, int32_t* order, int32_t* place,
-                    int32_t* offsets, void* workspace, const TileList& list, hipStream_t s);
+                    int32_t* offsets, void* workspace, const BandList& list, hipStream_t s);
 int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ldx, const int32_t* place, int top_k,
                         void* xs, int64_t ldxs, hipStream_t s);
 int launch_moe_combine(const uint16_t* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,

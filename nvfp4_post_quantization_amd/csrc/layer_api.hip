@@ -37,7 +37,7 @@ int nvfp4_moe_sort(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t ex
   if (workspace_bytes < need) return NVFP4_ERR_WORKSPACE;
   if (need && !workspace) return NVFP4_ERR_NULL_ARG;
   if (need && !aligned4(workspace)) return NVFP4_ERR_MISALIGNED;
-  return launch_moe_sort(ids, rows, experts, order, place, offsets, workspace, TileList{},
+  return launch_moe_sort(ids, rows, experts, order, place, offsets, workspace, BandList{},
                          as_stream(stream));
 }
 

@@ -40,7 +40,7 @@ struct SortArgs {
   uint32_t* counts;                      // [groups][experts] where groups > 1
   int64_t n;
   int experts, groups;
-  TileList list;
+  BandList list;
 };
 
 __device__ __forceinline__ int64_t chunk_begin(const SortArgs& a, int g) { return a.n * g / a.groups; }
@@ -132,20 +132,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     }
   }
   if (g == 0 && tid == 0) a.offsets[E] = (int32_t)rows;
-  if (a.list.tiles && g == 0) {                                  // (the same way for all threads)
-    // whole tiles first, then the experts' last ones, those of most units first
-    const uint32_t bm = a.list.bm, whole = total / bm, rest = total % bm;
+  if (a.list.bands && g == 0) {                                  // (the same way for all threads)
+    // whole bands first, then the experts' last ones, those of most units first
+    const uint32_t most = a.list.rows, whole = total / most, rest = total % most;
     const uint32_t units = (rest + a.list.unit - 1) / a.list.unit;
-    uint32_t tiles;
-    uint32_t at = block_scan(whole, part, tiles);
-    for (uint32_t i = 0; i < whole; ++i) a.list.tiles[at + i] = ExpertTile{tid, (int)(first + i * bm), (int)bm, 0};
-    for (uint32_t u = bm / a.list.unit; u > 0; --u) {
+    uint32_t count;
+    uint32_t at = block_scan(whole, part, count);
+    for (uint32_t i = 0; i < whole; ++i) a.list.bands[at + i] = ExpertBand{tid, (int)(first + i * most), (int)most, 0};
+    for (uint32_t u = most / a.list.unit; u > 0; --u) {
       uint32_t more;
-      at = tiles + block_scan(units == u ? 1 : 0, part, more);
-      if (units == u) a.list.tiles[at] = ExpertTile{tid, (int)(first + whole * bm), (int)rest, 0};
-      tiles += more;
+      at = count + block_scan(units == u ? 1 : 0, part, more);
+      if (units == u) a.list.bands[at] = ExpertBand{tid, (int)(first + whole * most), (int)rest, 0};
+      count += more;
     }
-    if (tid == 0) *a.list.count = (int)tiles;
+    if (tid == 0) *a.list.count = (int)count;
   }
   __syncthreads();
   for (int64_t i = r0; i < r1; i += 64) {
@@ -216,8 +216,14 @@ __device__ __forceinline__ void rows_of_token(const int32_t* place, int64_t t, i
   }
 }
 
+// Rows that are more than the 256 MB MALL can hand on are kept out of it: dispatch of
+// 8192x8x7168 (940 MB) 212 us, so 190, and combine 202 and 195; of 8192x8x2048 (268
+// MB) 51 and 54, and 51 and 58.
+constexpr int64_t kPastMall = INT64_C(1) << 29;
+typedef uint32_t Word4 __attribute__((ext_vector_type(4)));
+
 // The token's piece is read once and written to its rows.
-template <typename V, int K>
+template <typename V, int K, bool PAST>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const uint8_t* x, Units u, int64_t pieces, int64_t ldx,
                                                                const int32_t* place, int64_t n, int top_k, uint8_t* xs,
                                                                int64_t ldxs) {
@@ -227,18 +233,24 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(const uint8_t* x,
     rows_of_token(place, t, top_k, n, row);
 #pragma unroll
     for (int s = 0; s < K; ++s)
-      if (row[s] >= 0) reinterpret_cast<V*>(xs + row[s] * ldxs)[i] = v;
+      if (row[s] >= 0) {
+        V* const to = reinterpret_cast<V*>(xs + row[s] * ldxs) + i;
+        if constexpr (PAST) __builtin_nontemporal_store(v, to);
+        else *to = v;
+      }
   });
 }
 
 // Rows that are added up, 8 columns a piece: bf16, or fp16 with a power of two for
 // every 32 columns (biased: value = fp16 * 2^(e - kHalfBias)).
+template <bool PAST>
 struct Bf16Rows {
   const uint16_t* p;
   int64_t ld;
-  struct Piece { uint4 v; };
+  struct Piece { Word4 v; };
   __device__ __forceinline__ Piece load(int64_t row, int64_t i) const {
-    return Piece{*reinterpret_cast<const uint4*>(p + row * ld + i * 8)};
+    const Word4* const at = reinterpret_cast<const Word4*>(p + row * ld + i * 8);
+    return Piece{PAST ? __builtin_nontemporal_load(at) : *at};
   }
   static __device__ __forceinline__ void add(float (&acc)[8], const Piece& x, float w) {
     const uint32_t q[4] = {x.v.x, x.v.y, x.v.z, x.v.w};
@@ -394,7 +406,7 @@ size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts) {
 }
 
 int launch_moe_sort(const int32_t* ids, int64_t choices, int64_t experts, int32_t* order, int32_t* place,
-                    int32_t* offsets, void* workspace, const TileList& list, hipStream_t s) {
+                    int32_t* offsets, void* workspace, const BandList& list, hipStream_t s) {
   const SortArgs a{ids, order, place, offsets, static_cast<uint32_t*>(workspace), choices, (int)experts,
                    sort_groups(choices), list};
   if (a.groups > 1) {
@@ -414,19 +426,26 @@ int launch_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_
     const int64_t pieces = row_bytes / (int64_t)sizeof(V);
     const Units u = units_of(tokens, pieces);
     return with_places(top_k, [&](auto k) {
-      dispatch_kernel<V, decltype(k)::value><<<unit_grid(u), kRowThreads, 0, s>>>(
-          static_cast<const uint8_t*>(x), u, pieces, ldx, place, tokens * top_k, top_k, static_cast<uint8_t*>(xs), ldxs);
-      return launch_status("dispatch_kernel");
+      const auto go = [&](auto kernel) {
+        kernel<<<unit_grid(u), kRowThreads, 0, s>>>(static_cast<const uint8_t*>(x), u, pieces, ldx, place, tokens * top_k,
+                                                    top_k, static_cast<uint8_t*>(xs), ldxs);
+        return launch_status("dispatch_kernel");
+      };
+      if constexpr (sizeof(V) == 16)
+        if (tokens * top_k > kPastMall / row_bytes) return go(dispatch_kernel<V, decltype(k)::value, true>);
+      return go(dispatch_kernel<V, decltype(k)::value, false>);
     });
   };
-  if (all % 16 == 0) return run(uint4{});
+  if (all % 16 == 0) return run(Word4{});
   if (all % 4 == 0) return run(uint32_t{});
   return run(uint8_t{});
 }
 
 int launch_moe_combine(const uint16_t* ys, int64_t ldys, const int32_t* place, const float* weights, int64_t tokens,
                        int top_k, int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {
-  return run_combine(Bf16Rows{ys, ldys}, place, weights, tokens, top_k, cols, y, ldy, s);
+  if (tokens * top_k > kPastMall / (cols * 2))
+    return run_combine(Bf16Rows<true>{ys, ldys}, place, weights, tokens, top_k, cols, y, ldy, s);
+  return run_combine(Bf16Rows<false>{ys, ldys}, place, weights, tokens, top_k, cols, y, ldy, s);
 }
 int launch_moe_combine_half(const uint16_t* ys, const uint8_t* exponents, const int32_t* place, int64_t tokens, int top_k,
                             int64_t cols, uint16_t* y, int64_t ldy, hipStream_t s) {

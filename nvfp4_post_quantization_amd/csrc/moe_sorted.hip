@@ -25,12 +25,13 @@ namespace nvfp4 {
 namespace {
 
 struct SortedArgs {
-  const uint8_t* x;                // bf16 rows of the tokens
-  int64_t ldx;                     // bytes
+  const uint16_t* x;               // fp16 rows of the tokens, [tokens][hidden]
+  const float* xs;                 // their powers of two: value = fp16 * xs
   uint32_t x_bytes;                // of all of them, below 2^31
   const int32_t* order;            // choice of a sorted row
-  const ExpertTile* tiles;
-  const int* count;                // of tiles
+  const ExpertBand* bands;
+  const int* count;                // of bands
+  int band_tiles;                  // row tiles of a band, at most
   const float* weights;            // by choice
   const uint8_t *p13, *c13, *p2, *c2;
   const float *s13, *s2;
@@ -42,19 +43,69 @@ struct SortedArgs {
   int lds13, lds2;                 // bytes of a row of scales
 };
 
-// Which row tile and run of output rows a workgroup takes: false past the last.
-// Consecutive workgroups go to the 8 XCDs in turn, row tiles do so too; an XCD takes
-// all output rows of one before its next.  The list has the longest tiles first, so
-// that the XCDs have as much to do and what is left at the end is short.
-__device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, ExpertTile& t, int& n) {
-  const uint32_t xcd = blockIdx.x & 7, i = blockIdx.x >> 3, at = i / tiles_n * 8 + xcd;
+// The largest finite magnitude of 8 bf16 values, or `top`.
+__device__ __forceinline__ float finite_max(const uint4& v, float top) {
+  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = __uint_as_float((e & 1 ? q[e >> 1] & 0x7FFF0000u : q[e >> 1] << 16 & 0x7FFF0000u));
+    top = a <= 3.40282347e38f ? fmaxf(top, a) : top;
+  }
+  return top;
+}
+
+// Rows of x in fp16 with a power of two each that puts the largest below 2^15: exact,
+// but for values 2^29 and more below that, which are rounded to its 2^-39.  fp16
+// weights take half the work of bf16 ones to make, which is most of what a tile of few
+// rows has to do: 100 tokens of 128 experts of 7168 x 2048 (first product) 600 us with
+// x in bf16.
+__global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64_t ldx, int64_t tokens, int pieces,
+                                                        uint16_t* y, float* scale) {
+  __shared__ float part[4];
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const uint4* src = reinterpret_cast<const uint4*>(x + t * ldx);
+    float top = 0.f;
+    for (int i = threadIdx.x; i < pieces; i += 256) top = finite_max(src[i], top);
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    const int e = max((int)(__float_as_uint(top) >> 23), 15);
+    const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);
+    for (int i = threadIdx.x; i < pieces; i += 256) {
+      const uint4 v = src[i];
+      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+      f16x8 h;
+#pragma unroll
+      for (int z = 0; z < 8; ++z)
+        h[z] = (_Float16)(__uint_as_float(z & 1 ? q[z >> 1] & 0xFFFF0000u : q[z >> 1] << 16) * f);
+      reinterpret_cast<f16x8*>(y + t * (int64_t)pieces * 8)[i] = h;
+    }
+    if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(1.0f, e - kHalfBias);
+    __syncthreads();                                 // before the next token's maximum
+  }
+}
+
+// A row tile and run of output rows.
+struct TileAt { int expert, first, rows, n; };
+// Those that a workgroup takes: false past the last.  Consecutive workgroups go to
+// the 8 XCDs in turn, and so do bands: what an XCD's CUs work on at one time is the
+// row tiles of one expert, up to band_tiles of them, against the same output rows, so
+// that its L2 hands each weight to all of them and each row of x to all output rows
+// (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product fetches 6 GB so,
+// 19 GB with every row tile on another XCD).  The list has the longest bands first:
+// the XCDs have as much to do, and what is left at the end is short.
+__device__ __forceinline__ bool expert_tile(const SortedArgs& a, int rows, int tiles_n, TileAt& t) {
+  const uint32_t xcd = blockIdx.x & 7, i = blockIdx.x >> 3, per = a.band_tiles * tiles_n;
+  const uint32_t at = i / per * 8 + xcd, m = i % per / tiles_n;
   if (at >= (uint32_t)*a.count) return false;
-  const ExpertTile v = a.tiles[at];
+  const ExpertBand v = a.bands[at];
   t.expert = __builtin_amdgcn_readfirstlane(v.expert);
-  t.first = __builtin_amdgcn_readfirstlane(v.first);
-  t.rows = __builtin_amdgcn_readfirstlane(v.rows);
-  n = __builtin_amdgcn_readfirstlane(i % tiles_n);
-  return true;
+  t.first = __builtin_amdgcn_readfirstlane(v.first + m * rows);
+  t.rows = __builtin_amdgcn_readfirstlane(min(v.rows - (int)m * rows, rows));
+  t.n = __builtin_amdgcn_readfirstlane(i % per % tiles_n);
+  return t.rows > 0;
 }
 
 // A form of the tile kernels: TN x 32 output rows a wave, WM x WN waves, NL that
@@ -90,11 +141,10 @@ template <typename F>
 __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_up_tile_kernel(SortedArgs a) {
   constexpr int TN = F::TN, CH = F::BN / 2;          // channels of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
-  ExpertTile t;
-  int n;
-  if (!expert_tile(a, (a.inter + CH - 1) / CH, t, n)) return;
-  const int ch0 = n * CH, left = a.inter - ch0;
-  const uint32_t ldw = (uint32_t)a.hidden >> 1;
+  TileAt t;
+  if (!expert_tile(a, F::ROWS, (a.inter + CH - 1) / CH, t)) return;
+  const int ch0 = t.n * CH, left = a.inter - ch0;
+  const uint32_t ldw = (uint32_t)a.hidden >> 1, ldx = (uint32_t)a.hidden * 2;
   const int64_t row = (int64_t)t.expert * 2 * a.inter + ch0;
   const int rows_w = 2 * a.inter - ch0;              // to the end of the expert's up rows
   const int32_t* order = a.order + t.first;
@@ -108,15 +158,19 @@ __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_up_tile_kernel(SortedA
     using T = typename F::template Tile<TM, true>;
     const typename T::Scales scales(a.c13 + row * a.lds13, rows_w * a.lds13, a.lds13, a.inter * a.lds13,
                                     lds_address(lds) + T::NBUF * T::STAGE, 0, loader_of<T::NW, F::NL>());
-    nv_tile<false, TM, TN, F::WM, F::WN, F::NL, F::ahead(TM)>(
+    nv_tile<true, TM, TN, F::WM, F::WN, F::NL, F::ahead(TM)>(
         bx, bw, a.hidden, 0, (a.hidden + 63) >> 6,
-        [&](int r) { return (uint32_t)(order[min(r, t.rows - 1)] / a.top_k) * (uint32_t)a.ldx; },
+        [&](int r) { return (uint32_t)(order[min(r, t.rows - 1)] / a.top_k) * ldx; },
         [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; }, scales,
         lds, [&](const f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
           if (!multiplies) return;
           const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
           const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + wn * TN * 16 + piece * 8;
           uint8_t* mine = lds + wave * 32 * PITCH;
+          float s[TM];
+#pragma unroll
+          for (int m = 0; m < TM; ++m)
+            s[m] = a.xs[order[min((wm * TM + m) * 32 + l32, t.rows - 1)] / a.top_k] * s13;
 #pragma unroll
           for (int m = 0; m < TM; ++m) {
             const int r0 = (wm * TM + m) * 32;
@@ -128,7 +182,7 @@ __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_up_tile_kernel(SortedA
                 uint32_t v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const float gate = acc[i][m][4 * g + e] * s13, up = acc[i][m][8 + 4 * g + e] * s13;
+                  const float gate = acc[i][m][4 * g + e] * s[m], up = acc[i][m][8 + 4 * g + e] * s[m];
                   v[e] = to_bf16(gate / (1.0f + expf(-gate)) * up);
                 }
                 *reinterpret_cast<uint2*>(mine + l32 * PITCH + 32 * i + 16 * g + 2 * sub) =
@@ -172,10 +226,9 @@ template <typename F>
 __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_down_tile_kernel(SortedArgs a) {
   constexpr int TN = F::TN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
-  ExpertTile t;
-  int n;
-  if (!expert_tile(a, (a.hidden + F::BN - 1) / F::BN, t, n)) return;
-  const int o0 = n * F::BN, rows_w = min(F::BN, a.hidden - o0);
+  TileAt t;
+  if (!expert_tile(a, F::ROWS, (a.hidden + F::BN - 1) / F::BN, t)) return;
+  const int o0 = t.n * F::BN, rows_w = min(F::BN, a.hidden - o0);
   const uint32_t ldw = (uint32_t)a.inter >> 1, ldh = (uint32_t)a.inter * 2;
   const int64_t row = (int64_t)t.expert * a.hidden + o0;
   const auto bx = make_buffer(a.h + (int64_t)t.first * a.inter, (uint32_t)t.rows * ldh);
@@ -196,15 +249,18 @@ __global__ __launch_bounds__(F::THREADS, F::OCC) void moe_down_tile_kernel(Sorte
           const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
           const int piece = lane % LANES, row0 = lane / LANES, ob = o0 + wn * TN * 32, o = ob + piece * 8;
           uint8_t* mine = lds + wave * 32 * PITCH;
+          float w[TM];
+#pragma unroll
+          for (int m = 0; m < TM; ++m)
+            w[m] = a.weights[a.order[t.first + min((wm * TM + m) * 32 + l32, t.rows - 1)]] * s2;
 #pragma unroll
           for (int m = 0; m < TM; ++m) {
             const int r0 = (wm * TM + m) * 32;
             if (r0 >= t.rows) break;
             const int at = t.first + min(r0 + l32, t.rows - 1);
-            const float w = a.weights[a.order[at]] * s2;
 #pragma unroll
             for (int i = 0; i < TN; ++i) {
-              const int e = half_exponent(acc[i][m], w);
+              const int e = half_exponent(acc[i][m], w[m]);
               const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);      // the block's largest below 2^15
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
@@ -244,8 +300,8 @@ __global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* src, int
 }
 
 template <typename F>
-int run_products(const SortedArgs& a, int64_t max_tiles, hipStream_t s) {
-  const auto grid = [&](int64_t runs) { return (unsigned)((max_tiles + 7) / 8 * 8 * runs); };
+int run_products(const SortedArgs& a, int64_t max_bands, hipStream_t s) {
+  const auto grid = [&](int64_t runs) { return (unsigned)((max_bands + 7) / 8 * 8 * a.band_tiles * runs); };
   moe_up_tile_kernel<F><<<grid((a.inter + F::BN / 2 - 1) / (F::BN / 2)), F::THREADS, 0, s>>>(a);
   const int st = launch_status("moe_up_tile_kernel");
   if (st) return st;
@@ -262,21 +318,25 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 struct Plan {
   int64_t tokens;                                    // of a pass, at most
   bool large;                                        // form of the tiles
-  int bm;                                            // their rows
-  int64_t max_tiles;                                 // row tiles of a pass, at most
+  int rows, band_tiles;                              // rows of a tile, row tiles of a band
+  int64_t max_bands;                                 // of a pass
   bool pad13, pad2;
-  size_t order, place, offsets, sort, tiles, count, c13, c2, h, ys, ye, bytes;
+  size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, h, ys, ye, bytes;
 };
 
 Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inter) {
   Plan p{};
+  // a pass's rows of x have 32-bit offsets
+  const int64_t most = ((INT64_C(1) << 31) - 1) / (hidden * 2);
   p.tokens = kPassRows / top_k;
+  if (p.tokens > most) p.tokens = most;
   if (p.tokens > tokens) p.tokens = tokens;
   const int64_t n = p.tokens * top_k, per = n / experts;
   p.large = per > 32;
-  p.bm = p.large ? Large::ROWS : Small::ROWS;
-  // a tile is full, or the last one of an expert that has rows
-  p.max_tiles = n / p.bm + (n < experts ? n : experts);
+  p.rows = p.large ? Large::ROWS : Small::ROWS;
+  p.band_tiles = p.large ? 2 : 1;
+  // a band is whole, or the last one of an expert that has rows
+  p.max_bands = n / (p.rows * p.band_tiles) + (n < experts ? n : experts);
   p.pad13 = hidden % 64 != 0;
   p.pad2 = inter % 64 != 0;
   size_t at = 0;
@@ -289,10 +349,12 @@ Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, 
   p.place = take(n * 4);
   p.offsets = take((experts + 1) * 4);
   p.sort = take(moe_sort_workspace_bytes(n, experts));
-  p.tiles = take(p.max_tiles * sizeof(ExpertTile));
+  p.bands = take(p.max_bands * sizeof(ExpertBand));
   p.count = take(4);
   p.c13 = take(p.pad13 ? experts * 2 * inter * ((hidden + 63) / 64 * 4) : 0);
   p.c2 = take(p.pad2 ? experts * hidden * ((inter + 63) / 64 * 4) : 0);
+  p.x = take(p.tokens * hidden * 2);
+  p.xs = take(p.tokens * 4);
   p.h = take(n * inter * 2);
   p.ys = take(n * hidden * 2);
   p.ye = take(n * ((hidden + 31) / 32));
@@ -320,14 +382,14 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   const Plan p = plan_layer(tokens, top_k, experts, hidden, inter);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   SortedArgs a{};
-  a.ldx = ldx * 2;
   int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
   int32_t* const place = reinterpret_cast<int32_t*>(base + p.place);
-  ExpertTile* const tiles = reinterpret_cast<ExpertTile*>(base + p.tiles);
-  int* const count = reinterpret_cast<int*>(base + p.count);
+  const BandList list{reinterpret_cast<ExpertBand*>(base + p.bands), reinterpret_cast<int*>(base + p.count),
+                      p.rows * p.band_tiles, p.rows};
   a.order = order;
-  a.tiles = tiles;
-  a.count = count;
+  a.bands = list.bands;
+  a.count = list.count;
+  a.band_tiles = p.band_tiles;
   a.p13 = w.p13;
   a.p2 = w.p2;
   a.s13 = w.s13;
@@ -346,18 +408,20 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   int st;
   if (p.pad13 && (st = pad_scales(w.c13, experts * 2 * inter, hidden, base + p.c13, s))) return st;
   if (p.pad2 && (st = pad_scales(w.c2, experts * hidden, inter, base + p.c2, s))) return st;
-  // a pass's rows of x have 32-bit offsets
-  int64_t pass = ((INT64_C(1) << 31) - 1 - hidden * 2) / (ldx * 2) + 1;
-  if (pass > p.tokens) pass = p.tokens;
-  for (int64_t t = 0; t < tokens; t += pass) {
-    const int64_t here = tokens - t < pass ? tokens - t : pass;
-    a.x = reinterpret_cast<const uint8_t*>(x + t * ldx);
-    a.x_bytes = (uint32_t)((here - 1) * a.ldx + hidden * 2);
+  a.x = reinterpret_cast<const uint16_t*>(base + p.x);
+  a.xs = reinterpret_cast<const float*>(base + p.xs);
+  for (int64_t t = 0; t < tokens; t += p.tokens) {
+    const int64_t here = tokens - t < p.tokens ? tokens - t : p.tokens;
+    a.x_bytes = (uint32_t)(here * hidden * 2);
+    half_rows_kernel<<<(unsigned)here, 256, 0, s>>>(x + t * ldx, ldx, here, (int)(hidden / 8),
+                                                    reinterpret_cast<uint16_t*>(base + p.x),
+                                                    reinterpret_cast<float*>(base + p.xs));
+    if ((st = launch_status("half_rows_kernel"))) return st;
     a.weights = weights + t * top_k;
     if ((st = launch_moe_sort(ids + t * top_k, here * top_k, experts, order, place,
-                              reinterpret_cast<int32_t*>(base + p.offsets), base + p.sort, TileList{tiles, count, p.bm, p.bm / (p.large ? Large::MOST : Small::MOST)}, s)))
+                              reinterpret_cast<int32_t*>(base + p.offsets), base + p.sort, list, s)))
       return st;
-    if ((st = p.large ? run_products<Large>(a, p.max_tiles, s) : run_products<Small>(a, p.max_tiles, s))) return st;
+    if ((st = p.large ? run_products<Large>(a, p.max_bands, s) : run_products<Small>(a, p.max_bands, s))) return st;
     if ((st = launch_moe_combine_half(a.ys, a.ye, place, here, top_k, hidden, y + t * ldy, ldy, s))) return st;
   }
   return NVFP4_OK;
