@@ -13,12 +13,16 @@ constexpr int64_t kMaxChoices = INT64_C(1) << 30;
 
 // A band of the expert layer: rows first .. first + rows - 1 are expert's.
 struct ExpertBand { int expert, first, rows, unused; };
-// Where the sort also writes the bands of up to `rows` rows (none: NULL), those of
-// more units first.
+// What the sort also writes for the expert layer (bands NULL: nothing): the bands of
+// up to `rows` rows, those of more units first, and by row its choice's weight and
+// its token's scale.
 struct BandList {
   ExpertBand* bands;
   int* count;
   int rows, unit;
+  const float *weights, *scales;
+  float *row_weight, *row_scale;
+  int top_k;
 };
 
 size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts);

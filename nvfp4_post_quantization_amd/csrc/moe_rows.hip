@@ -31,7 +31,7 @@ namespace {
 // first launch.
 constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
 constexpr int kSortChunk = 4096;         // choices of a workgroup, at least, where there are several
-constexpr int kSortAlone = 8192;         // up to this many one workgroup does it
+constexpr int kSortAlone = 4096;         // up to this many one workgroup does it
 constexpr int kSortGroups = 256;
 
 struct SortArgs {
@@ -148,20 +148,39 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     if (tid == 0) *a.list.count = (int)count;
   }
   __syncthreads();
+  // what a step needs from memory is on its way during the one before
+  struct Choice { int e; float weight, scale; };
+  const auto load = [&](int64_t c) {
+    Choice v{-1, 0.f, 0.f};
+    if (c < r1) {
+      v.e = a.ids[c];
+      if (a.list.bands) {
+        v.weight = a.list.weights[c];
+        v.scale = a.list.scales[c / a.list.top_k];
+      }
+    }
+    return v;
+  };
+  Choice ahead = load(r0 + lane);
   for (int64_t i = r0; i < r1; i += 64) {
     const int64_t c = i + lane;
-    const int e = c < r1 ? a.ids[c] : -1;
-    const bool in = e >= 0 && e < E;
+    const Choice v = ahead;
+    ahead = load(c + 64);
+    const bool in = v.e >= 0 && v.e < E;
     uint64_t same = __ballot(in);
     for (int b = 0; (1 << b) < E; ++b) {
-      const uint64_t set = __ballot(e >> b & 1);
-      same &= e >> b & 1 ? set : ~set;
+      const uint64_t set = __ballot(v.e >> b & 1);
+      same &= v.e >> b & 1 ? set : ~set;
     }
     if (in) {
-      const uint32_t row = mine[e] + __popcll(same & ((1ull << lane) - 1));
-      if (same >> lane == 1) mine[e] = row + 1;                  // the last of them
+      const uint32_t row = mine[v.e] + __popcll(same & ((1ull << lane) - 1));
+      if (same >> lane == 1) mine[v.e] = row + 1;                // the last of them
       a.order[row] = (int32_t)c;
       a.place[c] = (int32_t)row;
+      if (a.list.bands) {
+        a.list.row_weight[row] = v.weight;
+        a.list.row_scale[row] = v.scale;
+      }
     } else if (c < r1) {
       a.place[c] = -1;
     }

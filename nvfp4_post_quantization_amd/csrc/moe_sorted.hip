@@ -24,15 +24,16 @@ namespace nvfp4 {
 
 namespace {
 
+constexpr int kCus = 256;
+
 struct SortedArgs {
   const uint16_t* x;               // fp16 rows of the tokens, [tokens][hidden]
-  const float* xs;                 // their powers of two: value = fp16 * xs
   uint32_t x_bytes;                // of all of them, below 2^31
   const int32_t* order;            // choice of a sorted row
   const ExpertBand* bands;
   const int* count;                // of bands
-  int band_tiles;                  // row tiles of a band, at most
-  const float* weights;            // by choice
+  const float* row_weight;         // by row: the choice's weight,
+  const float* row_scale;          // the token's power of two: value = fp16 * scale
   const uint8_t *p13, *c13, *p2, *c2;
   const float *s13, *s2;
   uint16_t* h;                     // [rows][inter]
@@ -89,115 +90,91 @@ __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64
 
 // A row tile and run of output rows.
 struct TileAt { int expert, first, rows, n; };
-// Those that a workgroup takes: false past the last.  Consecutive workgroups go to
-// the 8 XCDs in turn, and so do bands: what an XCD's CUs work on at one time is the
-// row tiles of one expert, up to band_tiles of them, against the same output rows, so
-// that its L2 hands each weight to all of them and each row of x to all output rows
-// (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product fetches 6 GB so,
-// 19 GB with every row tile on another XCD).  The list has the longest bands first:
-// the XCDs have as much to do, and what is left at the end is short.
-__device__ __forceinline__ bool expert_tile(const SortedArgs& a, int rows, int tiles_n, TileAt& t) {
-  const uint32_t xcd = blockIdx.x & 7, i = blockIdx.x >> 3, per = a.band_tiles * tiles_n;
+// Those that a workgroup of the tile kernels takes: false past the last.  Consecutive
+// workgroups go to the 8 XCDs in turn, and so do bands, two row tiles of an expert; of
+// a band, all output rows of the first come before those of the second.  What an XCD's
+// CUs work on at one time is then one or two experts, whose weights its L2 hands to
+// both row tiles (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product
+// fetches 10 GB, 19 where each row tile is on another XCD, and the layer takes 5.68 ms
+// and 5.94).  The list has the longest bands first: the XCDs have as much to do, and
+// what is left at the end is short.
+constexpr int kBandTiles = 2;
+__device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, TileAt& t) {
+  constexpr int ROWS = 128;
+  const uint32_t xcd = blockIdx.x & 7, i = blockIdx.x >> 3, per = kBandTiles * tiles_n;
   const uint32_t at = i / per * 8 + xcd, m = i % per / tiles_n;
   if (at >= (uint32_t)*a.count) return false;
   const ExpertBand v = a.bands[at];
   t.expert = __builtin_amdgcn_readfirstlane(v.expert);
-  t.first = __builtin_amdgcn_readfirstlane(v.first + m * rows);
-  t.rows = __builtin_amdgcn_readfirstlane(min(v.rows - (int)m * rows, rows));
+  t.first = __builtin_amdgcn_readfirstlane(v.first + m * ROWS);
+  t.rows = __builtin_amdgcn_readfirstlane(min(v.rows - (int)m * ROWS, ROWS));
   t.n = __builtin_amdgcn_readfirstlane(i % per % tiles_n);
   return t.rows > 0;
 }
 
-// A form of the tile kernels: TN x 32 output rows a wave, WM x WN waves, NL that
-// only load, OCC waves a SIMD.  A row tile has up to 32 MOST WM rows; the workgroup
-// takes the least multiple of 32 WM that holds it, so that products of rows that are
-// not there are left out.  Few rows leave LDS for more stages ahead (A1, A2 of them
-// for one and two multiples, else 2), which weights that are used once need.
-template <int TN_, int WM_, int WN_, int NL_, int MOST_, int OCC_, int A1, int A2>
-struct Form {
-  static constexpr int TN = TN_, WM = WM_, WN = WN_, NL = NL_, MOST = MOST_, OCC = OCC_;
-  static constexpr int ROWS = 32 * MOST * WM, BN = 32 * TN * WN, THREADS = 64 * (WM * WN + NL);
-  static constexpr int ahead(int tm) { return tm == 1 ? A1 : tm == 2 ? A2 : 2; }
+// The tile kernels' form: 4 waves, 64 output rows each; a row tile has up to 128 rows,
+// and the workgroup takes the least multiple of 32 that holds it, so that products of
+// rows that are not there are left out.  Two workgroups share a CU (one of 256 x 256,
+// whose start and end nothing hides: 6.2 ms against 5.9 for 8192 tokens).
+constexpr int tile_ahead(int tm) { return tm == 1 ? 4 : 2; }                 // stages, as LDS allows
+struct Tiles {
+  static constexpr int TN = 2, WN = 4, ROWS = 128, BN = 32 * TN * WN, THREADS = 64 * WN;
   template <int TM, bool PAIRED>
-  using Tile = NvTile<TM, TN, WM, WN, NL, ahead(TM), PAIRED>;
-  static constexpr int most(int a, int b) { return a > b ? a : b; }
-  static constexpr int LDS = most(most(Tile<1, false>::LDS, Tile<2, false>::LDS),
-                                  MOST > 2 ? most(Tile<3, false>::LDS, Tile<4, false>::LDS) : 0);
+  using Tile = NvTile<TM, TN, 1, WN, 0, tile_ahead(TM), PAIRED>;
+  static constexpr int LDS = Tile<4, false>::LDS;    // the most that any takes
+  static_assert(Tile<1, false>::LDS <= LDS && Tile<2, false>::LDS <= LDS && Tile<3, false>::LDS <= LDS, "stages");
+  static_assert(WN * 32 * (64 * TN + 16) <= LDS && 2 * LDS <= 160 * 1024, "store staging; two workgroups a CU");
 };
-template <typename F, typename Body>
+template <typename Body>
 __device__ __forceinline__ void with_rows(int rows, Body f) {
-  constexpr int UNIT = 32 * F::WM;
-  if (rows <= UNIT) return f(std::integral_constant<int, 1>{});
-  if (F::MOST == 2 || rows <= 2 * UNIT) return f(std::integral_constant<int, 2>{});
-  if constexpr (F::MOST > 2) {
-    if (rows <= 3 * UNIT) return f(std::integral_constant<int, 3>{});
-    return f(std::integral_constant<int, 4>{});
-  }
+  if (rows <= 32) f(std::integral_constant<int, 1>{});
+  else if (rows <= 64) f(std::integral_constant<int, 2>{});
+  else if (rows <= 96) f(std::integral_constant<int, 3>{});
+  else f(std::integral_constant<int, 4>{});
 }
 
-// h of a row tile: of every 32 output rows of a tile, 16 are gate rows and 16 the
-// up rows of the same channels, so that a lane holds both.
-template <typename F>
-__global__ __launch_bounds__(F::THREADS, F::OCC) void moe_up_tile_kernel(SortedArgs a) {
-  constexpr int TN = F::TN, CH = F::BN / 2;          // channels of a tile
-  __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
-  TileAt t;
-  if (!expert_tile(a, F::ROWS, (a.inter + CH - 1) / CH, t)) return;
-  const int ch0 = t.n * CH, left = a.inter - ch0;
-  const uint32_t ldw = (uint32_t)a.hidden >> 1, ldx = (uint32_t)a.hidden * 2;
-  const int64_t row = (int64_t)t.expert * 2 * a.inter + ch0;
-  const int rows_w = 2 * a.inter - ch0;              // to the end of the expert's up rows
-  const int32_t* order = a.order + t.first;
-  const auto bx = make_buffer(a.x, a.x_bytes);
-  const auto bw = make_buffer(a.p13 + row * ldw, (uint32_t)rows_w * ldw);
-  const float s13 = a.s13[t.expert];
-  constexpr int PITCH = 32 * TN + 16, LANES = 2 * TN, ROWS = 64 / LANES;      // of a wave's h in lds
-  static_assert(F::WM * F::WN * 32 * PITCH <= F::LDS, "store staging");
-  with_rows<F>(t.rows, [&](auto tm) {
-    constexpr int TM = decltype(tm)::value;
-    using T = typename F::template Tile<TM, true>;
-    const typename T::Scales scales(a.c13 + row * a.lds13, rows_w * a.lds13, a.lds13, a.inter * a.lds13,
-                                    lds_address(lds) + T::NBUF * T::STAGE, 0, loader_of<T::NW, F::NL>());
-    nv_tile<true, TM, TN, F::WM, F::WN, F::NL, F::ahead(TM)>(
-        bx, bw, a.hidden, 0, (a.hidden + 63) >> 6,
-        [&](int r) { return (uint32_t)(order[min(r, t.rows - 1)] / a.top_k) * ldx; },
-        [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; }, scales,
-        lds, [&](const f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
-          if (!multiplies) return;
-          const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
-          const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + wn * TN * 16 + piece * 8;
-          uint8_t* mine = lds + wave * 32 * PITCH;
-          float s[TM];
+// by[first row + 32 m + the lane's] * s
+template <int TM>
+struct RowValues {
+  float v[TM];
+  __device__ __forceinline__ RowValues(const float* by, const TileAt& t, float s) {
 #pragma unroll
-          for (int m = 0; m < TM; ++m)
-            s[m] = a.xs[order[min((wm * TM + m) * 32 + l32, t.rows - 1)] / a.top_k] * s13;
+    for (int m = 0; m < TM; ++m) v[m] = by[t.first + min(32 * m + (int)(threadIdx.x & 31), t.rows - 1)] * s;
+  }
+  __device__ __forceinline__ explicit RowValues(float one) : v{one} {}
+};
+
+// A wave's part of h: 16 TN channels from ch0 on of the tile's rows (s: what their sums
+// are to be multiplied by), through `mine` in LDS so that whole runs are stored.
+template <int TN, int TM>
+__device__ __forceinline__ void put_h(const SortedArgs& a, const TileAt& t, const f32x16 (&acc)[TN][TM],
+                                      const RowValues<TM>& s, int ch0, uint8_t* mine) {
+  constexpr int PITCH = 32 * TN + 16, LANES = 2 * TN, ROWS = 64 / LANES;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
+  const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + piece * 8;
 #pragma unroll
-          for (int m = 0; m < TM; ++m) {
-            const int r0 = (wm * TM + m) * 32;
-            if (r0 >= t.rows) break;
+  for (int m = 0; m < TM; ++m) {
+    if (32 * m >= t.rows) break;
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                uint32_t v[4];
+      for (int g = 0; g < 2; ++g) {
+        uint32_t v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float gate = acc[i][m][4 * g + e] * s[m], up = acc[i][m][8 + 4 * g + e] * s[m];
-                  v[e] = to_bf16(gate / (1.0f + expf(-gate)) * up);
-                }
-                *reinterpret_cast<uint2*>(mine + l32 * PITCH + 32 * i + 16 * g + 2 * sub) =
-                    make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-              }
+        for (int e = 0; e < 4; ++e) {
+          const float gate = acc[i][m][4 * g + e] * s.v[m], up = acc[i][m][8 + 4 * g + e] * s.v[m];
+          v[e] = to_bf16(gate / (1.0f + expf(-gate)) * up);
+        }
+        *reinterpret_cast<uint2*>(mine + l32 * PITCH + 32 * i + 16 * g + 2 * sub) =
+            make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      }
 #pragma unroll
-            for (int r = 0; r < 32; r += ROWS) {
-              const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
-              const int at = r0 + r + row0;
-              if (at < t.rows && ch < a.inter)
-                *reinterpret_cast<uint4*>(a.h + (int64_t)(t.first + at) * a.inter + ch) = v;
-            }
-          }
-        });
-  });
+    for (int r = 0; r < 32; r += ROWS) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
+      const int at = 32 * m + r + row0;
+      if (at < t.rows && ch < a.inter) *reinterpret_cast<uint4*>(a.h + (int64_t)(t.first + at) * a.inter + ch) = v;
+    }
+  }
 }
 
 // v *= w; the biased exponent to store for the 32 columns of a token that this lane
@@ -221,68 +198,273 @@ __device__ __forceinline__ int half_exponent(f32x16& v, float w) {
   return max((int)(max(p, q) >> 23), 14);
 }
 
-// The rows of a row tile, with their weight and the tensor scale.
-template <typename F>
-__global__ __launch_bounds__(F::THREADS, F::OCC) void moe_down_tile_kernel(SortedArgs a) {
-  constexpr int TN = F::TN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
+// A wave's part of the rows: 32 TN outputs from o0 on (w as s).
+template <int TN, int TM>
+__device__ __forceinline__ void put_rows(const SortedArgs& a, const TileAt& t, f32x16 (&acc)[TN][TM],
+                                         const RowValues<TM>& w, int o0, uint8_t* mine) {
+  constexpr int PITCH = 64 * TN + 16, LANES = 4 * TN, ROWS = 64 / LANES;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
+  const int piece = lane % LANES, row0 = lane / LANES, o = o0 + piece * 8;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    if (32 * m >= t.rows) break;
+    const int at = t.first + min(32 * m + l32, t.rows - 1);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int e = half_exponent(acc[i][m], w.v[m]);
+      const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);      // the block's largest below 2^15
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t v[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) v[z] = __builtin_bit_cast(uint16_t, (_Float16)(acc[i][m][4 * g + z] * f));
+        *reinterpret_cast<uint2*>(mine + l32 * PITCH + 64 * i + 16 * g + 2 * sub) =
+            make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      }
+      if (sub == 0 && 32 * m + l32 < t.rows && o0 + 32 * i < a.hidden)
+        a.ye[(int64_t)at * a.lde + (o0 >> 5) + i] = (uint8_t)e;
+    }
+#pragma unroll
+    for (int r = 0; r < 32; r += ROWS) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
+      const int to = 32 * m + r + row0;
+      if (to < t.rows && o < a.hidden) *reinterpret_cast<uint4*>(a.ys + (int64_t)(t.first + to) * a.hidden + o) = v;
+    }
+  }
+}
+
+// h of a row tile: of every 32 output rows of a tile, 16 are gate rows and 16 the
+// up rows of the same channels, so that a lane holds both.
+__global__ __launch_bounds__(Tiles::THREADS, 2) void moe_up_tile_kernel(SortedArgs a) {
+  constexpr int TN = Tiles::TN, CH = Tiles::BN / 2;  // channels of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Tiles::LDS];
   TileAt t;
-  if (!expert_tile(a, F::ROWS, (a.hidden + F::BN - 1) / F::BN, t)) return;
-  const int o0 = t.n * F::BN, rows_w = min(F::BN, a.hidden - o0);
+  if (!expert_tile(a, (a.inter + CH - 1) / CH, t)) return;
+  const int ch0 = t.n * CH, left = a.inter - ch0;
+  const uint32_t ldw = (uint32_t)a.hidden >> 1, ldx = (uint32_t)a.hidden * 2;
+  const int64_t row = (int64_t)t.expert * 2 * a.inter + ch0;
+  const int rows_w = 2 * a.inter - ch0;              // to the end of the expert's up rows
+  const auto bx = make_buffer(a.x, a.x_bytes);
+  const auto bw = make_buffer(a.p13 + row * ldw, (uint32_t)rows_w * ldw);
+  with_rows(t.rows, [&](auto tm) {
+    constexpr int TM = decltype(tm)::value;
+    using T = Tiles::Tile<TM, true>;
+    const typename T::Scales scales(a.c13 + row * a.lds13, rows_w * a.lds13, a.lds13, a.inter * a.lds13,
+                           lds_address(lds) + T::NBUF * T::STAGE, 0, loader_of<T::NW, 0>());
+    nv_tile<true, TM, TN, 1, Tiles::WN, 0, tile_ahead(TM)>(
+        bx, bw, a.hidden, 0, (a.hidden + 63) >> 6,
+        [&](int r) { return (uint32_t)(a.order[t.first + min(r, t.rows - 1)] / a.top_k) * ldx; },
+        [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; }, scales,
+        lds, [&](const f32x16 (&acc)[TN][TM], int, int wn, int wave, bool) {
+          put_h<TN, TM>(a, t, acc, RowValues<TM>(a.row_scale, t, a.s13[t.expert]), ch0 + wn * TN * 16,
+                        lds + wave * 32 * (32 * TN + 16));
+        });
+  });
+}
+
+// The rows of a row tile.
+__global__ __launch_bounds__(Tiles::THREADS, 2) void moe_down_tile_kernel(SortedArgs a) {
+  constexpr int TN = Tiles::TN;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Tiles::LDS];
+  TileAt t;
+  if (!expert_tile(a, (a.hidden + Tiles::BN - 1) / Tiles::BN, t)) return;
+  const int o0 = t.n * Tiles::BN, rows_w = min(Tiles::BN, a.hidden - o0);
   const uint32_t ldw = (uint32_t)a.inter >> 1, ldh = (uint32_t)a.inter * 2;
   const int64_t row = (int64_t)t.expert * a.hidden + o0;
   const auto bx = make_buffer(a.h + (int64_t)t.first * a.inter, (uint32_t)t.rows * ldh);
   const auto bw = make_buffer(a.p2 + row * ldw, (uint32_t)rows_w * ldw);
-  const float s2 = a.s2[t.expert];
-  constexpr int PITCH = 64 * TN + 16, LANES = 4 * TN, ROWS = 64 / LANES;      // of a wave's rows in lds
-  static_assert(F::WM * F::WN * 32 * PITCH <= F::LDS, "store staging");
-  with_rows<F>(t.rows, [&](auto tm) {
+  with_rows(t.rows, [&](auto tm) {
     constexpr int TM = decltype(tm)::value;
-    using T = typename F::template Tile<TM, false>;
-    const typename T::Scales scales(a.c2 + row * a.lds2, rows_w * a.lds2, a.lds2, 0, lds_address(lds) + T::NBUF * T::STAGE,
-                                    0, loader_of<T::NW, F::NL>());
-    nv_tile<false, TM, TN, F::WM, F::WN, F::NL, F::ahead(TM)>(
+    using T = Tiles::Tile<TM, false>;
+    const typename T::Scales scales(a.c2 + row * a.lds2, rows_w * a.lds2, a.lds2, 0, lds_address(lds) + T::NBUF * T::STAGE, 0,
+                           loader_of<T::NW, 0>());
+    nv_tile<false, TM, TN, 1, Tiles::WN, 0, tile_ahead(TM)>(
         bx, bw, a.inter, 0, (a.inter + 63) >> 6, [&](int r) { return (uint32_t)min(r, t.rows - 1) * ldh; },
         [&](int r) { return (uint32_t)min(r, rows_w - 1) * ldw; }, scales, lds,
-        [&](f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
-          if (!multiplies) return;
-          const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
-          const int piece = lane % LANES, row0 = lane / LANES, ob = o0 + wn * TN * 32, o = ob + piece * 8;
-          uint8_t* mine = lds + wave * 32 * PITCH;
-          float w[TM];
-#pragma unroll
-          for (int m = 0; m < TM; ++m)
-            w[m] = a.weights[a.order[t.first + min((wm * TM + m) * 32 + l32, t.rows - 1)]] * s2;
-#pragma unroll
-          for (int m = 0; m < TM; ++m) {
-            const int r0 = (wm * TM + m) * 32;
-            if (r0 >= t.rows) break;
-            const int at = t.first + min(r0 + l32, t.rows - 1);
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-              const int e = half_exponent(acc[i][m], w[m]);
-              const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);      // the block's largest below 2^15
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                uint32_t v[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  v[z] = __builtin_bit_cast(uint16_t, (_Float16)(acc[i][m][4 * g + z] * f));
-                *reinterpret_cast<uint2*>(mine + l32 * PITCH + 64 * i + 16 * g + 2 * sub) =
-                    make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-              }
-              if (sub == 0 && r0 + l32 < t.rows && ob + 32 * i < a.hidden)
-                a.ye[(int64_t)at * a.lde + (ob >> 5) + i] = (uint8_t)e;
-            }
-#pragma unroll
-            for (int r = 0; r < 32; r += ROWS) {
-              const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
-              const int to = r0 + r + row0;
-              if (to < t.rows && o < a.hidden) *reinterpret_cast<uint4*>(a.ys + (int64_t)(t.first + to) * a.hidden + o) = v;
-            }
-          }
+        [&](f32x16 (&acc)[TN][TM], int, int wn, int wave, bool) {
+          put_rows<TN, TM>(a, t, acc, RowValues<TM>(a.row_weight, t, a.s2[t.expert]), o0 + wn * TN * 32,
+                           lds + wave * 32 * (64 * TN + 16));
         });
   });
+}
+
+// ---- few rows an expert ------------------------------------------------------
+//
+// Tiles of up to 32 rows x 256 output rows for experts with few tokens, where the
+// weights, read once, bound the layer.  A stage is 256 channels, so that a row of
+// packed weights or scales is asked for by whole cache lines (of the 64 channels of
+// the other forms, 32 bytes a row, each line is asked for four times) and waves meet
+// a quarter as often.  Eight waves load and multiply, 32 output rows each; one
+// workgroup a CU keeps three stages in LDS, two of them on their way, also from one
+// tile to the next: what the next tile is, is read through the scalar cache, so that
+// nothing waits for it behind the stages in flight.
+struct Stream {
+  static constexpr int ROWS = 32, BN = 256, WAVES = 16, THREADS = 64 * WAVES;
+  static constexpr int WB = BN * 128, XB = ROWS * 512, SB = BN * 16;
+  static constexpr int ROW = WB + XB + SB, STAGE = ROW + 256, BUFS = 3;        // at ROW: a value for each row
+  static constexpr int LDS = BUFS * STAGE;
+  // loads of a wave and stage: twice 8 rows of weights, 2 rows of x, and 64 rows of
+  // scales (waves 0 .. 3) or the rows' values
+  static constexpr int LOADS = 4;
+  // at a tile's end, in the last stage's place: the sums of half the waves, then what
+  // put_h and put_rows turn round
+  static constexpr int TURN = 8 * 4096;
+  static_assert(TURN + 8 * 32 * 80 <= ROW, "the end of a tile");
+};
+
+// (a conditional on the variables themselves would choose among their addresses,
+// which puts them in memory)
+__device__ __forceinline__ uint32_t beyond_if(bool cut, uint32_t offset) { return cut ? kBeyond : offset; }
+
+// A word that all lanes want, past the vector loads in flight.
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)uniform(reinterpret_cast<const uint8_t*>(p));
+}
+__device__ __forceinline__ float scalar_load(const float* p) {
+  return __uint_as_float((uint32_t)scalar_load(reinterpret_cast<const int32_t*>(p)));
+}
+
+// Tiles at, at + step, ...: the first product (UP: tokens in fp16, output rows in
+// pairs as above) or the second.
+template <bool UP>
+__global__ __launch_bounds__(Stream::THREADS, 4) void moe_stream_kernel(SortedArgs a) {
+  using S = Stream;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S::LDS];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds_base = lds_address(lds);
+  constexpr int COLS = UP ? S::BN / 2 : S::BN;                   // of the result, a tile
+  const int k = UP ? a.hidden : a.inter, cols = UP ? a.inter : a.hidden;
+  const int stages = (k + 255) >> 8, tiles_n = (cols + COLS - 1) / COLS;
+  const uint32_t ldw = (uint32_t)k >> 1, lds_s = UP ? a.lds13 : a.lds2;
+  // this workgroup's tiles: of its XCD's bands, in turn (see expert_tile)
+  const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+  const int bands = scalar_load(a.count);
+  const int tiles = (bands - xcd + 7) / 8 * tiles_n;
+  const auto tile = [&](int i) {
+    const int32_t* b = reinterpret_cast<const int32_t*>(a.bands + (i / tiles_n * 8 + xcd));
+    return TileAt{scalar_load(b), scalar_load(b + 1), scalar_load(b + 2), i % tiles_n};
+  };
+
+  // what is loaded: stage ls of tile lt
+  int lt = blockIdx.x >> 3, ls = 0;
+  i32x4 bx, bw, bs;                                              // bs: scales, or the rows' values
+  const bool has_scales = wave < 4;
+  uint32_t xo, wo0, wo1, so;
+  // channels of the lane's pieces (the same for all its loads)
+  const int xc = (l32 ^ ((2 * wave + half) & 15)) * 8;
+  const int wc = ((lane & 7) ^ swizzle128(wave * 8 + (lane >> 3))) * 32;
+  const auto aim = [&]() {
+    const bool none = lt >= tiles;                               // then loads bring zeros
+    const TileAt t = tile(none ? blockIdx.x >> 3 : lt);
+    const int c0 = t.n * COLS;
+    const int64_t row = (int64_t)t.expert * (UP ? 2 * a.inter : a.hidden) + c0;
+    const int rows_w = UP ? 2 * a.inter - c0 : min(S::BN, cols - c0);
+    const auto w_row = [&](int r) {
+      return UP ? min((r >> 5) * 16 + (r & 15), a.inter - 1 - c0) + ((r >> 4) & 1) * a.inter : min(r, rows_w - 1);
+    };
+    bx = UP ? make_buffer(a.x, a.x_bytes)
+            : make_buffer(a.h + (int64_t)t.first * k, (uint32_t)t.rows * (uint32_t)k * 2);
+    bw = make_buffer((UP ? a.p13 : a.p2) + row * ldw, (uint32_t)rows_w * ldw);
+    bs = has_scales ? make_buffer((UP ? a.c13 : a.c2) + row * lds_s, (uint32_t)rows_w * lds_s)
+                    : make_buffer((UP ? a.row_scale : a.row_weight) + t.first, (uint32_t)t.rows * 4);
+    const auto x_row = [&](int r) {                              // rows r and, for the upper lanes, r + 1
+      const int even = min(r, t.rows - 1), odd = min(r + 1, t.rows - 1);
+      if constexpr (!UP) return half ? odd : even;
+      const int32_t* order = a.order + t.first;
+      const int c0 = scalar_load(order + even) / a.top_k, c1 = scalar_load(order + odd) / a.top_k;
+      return half ? c1 : c0;
+    };
+    const auto w_off = [&](int i) { return (uint32_t)w_row((i * S::WAVES + wave) * 8 + (lane >> 3)) * ldw + wc / 2; };
+    xo = beyond_if(none, (uint32_t)x_row(2 * wave) * (uint32_t)k * 2 + xc * 2);
+    wo0 = beyond_if(none, w_off(0));
+    wo1 = beyond_if(none, w_off(1));
+    so = beyond_if(none, has_scales ? (uint32_t)w_row(wave * 64 + lane) * lds_s : lane * 4);
+  };
+  const auto load_stage = [&](int buf) {
+    const uint32_t dst = lds_base + buf * S::STAGE + wave * 1024;
+    const bool cut = ls == stages - 1;                           // pieces past k: zeros
+    const bool wcut = cut && ls * 256 + wc >= k;
+    constexpr int W = S::WAVES * 1024;
+    load_lds16<0>(bw, dst, beyond_if(wcut, wo0), ls * 128);
+    load_lds16<W>(bw, dst, beyond_if(wcut, wo1), ls * 128);
+    load_lds16<S::WB>(bx, dst, beyond_if(cut && ls * 256 + xc >= k, xo), ls * 512);
+    if (has_scales) load_lds16<S::WB + S::XB>(bs, dst, so, ls * 16);
+    else load_lds4<S::ROW>(bs, lds_base + buf * S::STAGE, so, 0);
+    if (lt < tiles && ++ls == stages) {
+      ls = 0;
+      lt += step;
+      aim();
+    }
+  };
+
+  const int wn = wave & 7, q0 = wave >> 3 << 1;                  // output rows, quarters q0 and q0 + 1 of a stage
+  const int w_at = (wn * 32 + l32) * 128, x_at = S::WB + l32 * 512, s_at = S::WB + S::XB + (wn * 32 + l32) * 16 + q0 * 4;
+  if (lt >= tiles) return;
+  aim();
+  load_stage(0);
+  load_stage(1);
+  int buf = 0;
+  bool landed = false;
+  for (int i = blockIdx.x >> 3; i < tiles; i += step) {
+    const TileAt t = tile(i);
+    f32x16 acc[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[z][e] = 0.0f;
+    for (int g = 0; g < stages; ++g) {
+      if (!landed) wait_loads<S::LOADS>();
+      landed = false;
+      lds_barrier();                                             // the stage is there, and the one before it read
+      load_stage(buf == 0 ? 2 : buf - 1);
+      const uint8_t* b = lds + buf * S::STAGE;
+      const uint2 codes = *reinterpret_cast<const uint2*>(b + s_at);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {                              // 64 channels
+        const int q = q0 + z;
+        if (g * 256 + q * 64 >= k) break;
+        const uint4 w = *reinterpret_cast<const uint4*>(b + w_at + (((2 * q + half) ^ swizzle128(l32)) << 4));
+        const uint32_t nib[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t c = (z ? codes.y : codes.x) >> (16 * half);
+        const float s[2] = {e4m3_f32<0>(c), e4m3_f32<1>(c)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = *reinterpret_cast<const uint4*>(b + x_at + (((8 * q + 4 * half + j) ^ (l32 & 15)) << 4));
+          const uint4 v = UP ? fp4x8_f16(nib[j], splat_f16(s[j >> 1])) : fp4x8_bf16(nib[j], s[j >> 1]);
+          acc[j & 1] = mfma32_16<UP>(v, x, acc[j & 1]);
+        }
+      }
+      buf = buf == 2 ? 0 : buf + 1;
+    }
+    // The next stage is awaited here: behind the stores it would be awaited with them.
+    wait_loads<S::LOADS>();
+    landed = true;
+    lds_barrier();                                               // the last stage's buffer is free
+    f32x16 sum[1][1];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[0][0][e] = acc[0][e] + acc[1][e];
+    uint8_t* const last = lds + (buf == 0 ? 2 : buf - 1) * S::STAGE;
+    f32x4* const halves = reinterpret_cast<f32x4*>(last + wn * 4096) + lane;
+    if (q0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        halves[64 * g] = f32x4{sum[0][0][4 * g], sum[0][0][4 * g + 1], sum[0][0][4 * g + 2], sum[0][0][4 * g + 3]};
+    }
+    lds_barrier();
+    if (q0) continue;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 v = halves[64 * g];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][0][4 * g + e] += v[e];
+    }
+    const RowValues<1> v(reinterpret_cast<const float*>(last + S::ROW)[l32] * scalar_load((UP ? a.s13 : a.s2) + t.expert));
+    uint8_t* const mine = last + S::TURN + wn * 32 * 80;
+    if constexpr (UP) put_h<1, 1>(a, t, sum, v, t.n * COLS + wn * 16, mine);
+    else put_rows<1, 1>(a, t, sum, v, t.n * COLS + wn * 32, mine);
+  }
+  wait_loads<0>();                                               // what is still on its way to LDS
 }
 
 // Rows of scales to rows of whole words, zero past nb.
@@ -299,31 +481,38 @@ __global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* src, int
   }
 }
 
-template <typename F>
-int run_products(const SortedArgs& a, int64_t max_bands, hipStream_t s) {
-  const auto grid = [&](int64_t runs) { return (unsigned)((max_bands + 7) / 8 * 8 * a.band_tiles * runs); };
-  moe_up_tile_kernel<F><<<grid((a.inter + F::BN / 2 - 1) / (F::BN / 2)), F::THREADS, 0, s>>>(a);
+int run_tiles(const SortedArgs& a, int64_t max_bands, hipStream_t s) {
+  const auto grid = [&](int64_t runs) { return (unsigned)((max_bands + 7) / 8 * 8 * kBandTiles * runs); };
+  moe_up_tile_kernel<<<grid((a.inter + Tiles::BN / 2 - 1) / (Tiles::BN / 2)), Tiles::THREADS, 0, s>>>(a);
   const int st = launch_status("moe_up_tile_kernel");
   if (st) return st;
-  moe_down_tile_kernel<F><<<grid((a.hidden + F::BN - 1) / F::BN), F::THREADS, 0, s>>>(a);
+  moe_down_tile_kernel<<<grid((a.hidden + Tiles::BN - 1) / Tiles::BN), Tiles::THREADS, 0, s>>>(a);
   return launch_status("moe_down_tile_kernel");
 }
-using Small = Form<1, 1, 4, 4, 4, 4, 6, 4>;
-using Large = Form<2, 1, 4, 0, 4, 2, 4, 2>;
-
+int run_stream(const SortedArgs& a, hipStream_t s) {
+  moe_stream_kernel<true><<<kCus, Stream::THREADS, 0, s>>>(a);
+  const int st = launch_status("moe_stream_kernel");
+  if (st) return st;
+  moe_stream_kernel<false><<<kCus, Stream::THREADS, 0, s>>>(a);
+  return launch_status("moe_stream_kernel");
+}
 constexpr int64_t kPassRows = INT64_C(1) << 17;      // choices of one pass, at most
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Plan {
   int64_t tokens;                                    // of a pass, at most
-  bool large;                                        // form of the tiles
-  int rows, band_tiles;                              // rows of a tile, row tiles of a band
+  bool few;                                          // rows an expert: the stream kernel
   int64_t max_bands;                                 // of a pass
   bool pad13, pad2;
-  size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, h, ys, ye, bytes;
+  size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, row_weight, row_scale, h, ys, ye, bytes;
 };
 
+int band_rows(const Plan& p) { return p.few ? Stream::ROWS : kBandTiles * Tiles::ROWS; }
+
+// Few rows an expert, us with the stream kernel and in tiles (7168 x 2048, 8 of 128):
+//   rows      6        9        16       22         32         44
+//        692, 847  748, 891  898, 932  1018, 1013  1182, 1051  1372, 1120
 Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inter) {
   Plan p{};
   // a pass's rows of x have 32-bit offsets
@@ -332,11 +521,9 @@ Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, 
   if (p.tokens > most) p.tokens = most;
   if (p.tokens > tokens) p.tokens = tokens;
   const int64_t n = p.tokens * top_k, per = n / experts;
-  p.large = per > 32;
-  p.rows = p.large ? Large::ROWS : Small::ROWS;
-  p.band_tiles = p.large ? 2 : 1;
+  p.few = per <= 20;
   // a band is whole, or the last one of an expert that has rows
-  p.max_bands = n / (p.rows * p.band_tiles) + (n < experts ? n : experts);
+  p.max_bands = n / band_rows(p) + (n < experts ? n : experts);
   p.pad13 = hidden % 64 != 0;
   p.pad2 = inter % 64 != 0;
   size_t at = 0;
@@ -355,6 +542,8 @@ Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, 
   p.c2 = take(p.pad2 ? experts * hidden * ((inter + 63) / 64 * 4) : 0);
   p.x = take(p.tokens * hidden * 2);
   p.xs = take(p.tokens * 4);
+  p.row_weight = take(n * 4);
+  p.row_scale = take(n * 4);
   p.h = take(n * inter * 2);
   p.ys = take(n * hidden * 2);
   p.ye = take(n * ((hidden + 31) / 32));
@@ -384,12 +573,20 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   SortedArgs a{};
   int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
   int32_t* const place = reinterpret_cast<int32_t*>(base + p.place);
-  const BandList list{reinterpret_cast<ExpertBand*>(base + p.bands), reinterpret_cast<int*>(base + p.count),
-                      p.rows * p.band_tiles, p.rows};
+  BandList list{};
+  list.bands = reinterpret_cast<ExpertBand*>(base + p.bands);
+  list.count = reinterpret_cast<int*>(base + p.count);
+  list.rows = band_rows(p);
+  list.unit = p.few ? Stream::ROWS : Tiles::ROWS;
+  list.scales = reinterpret_cast<const float*>(base + p.xs);
+  list.row_weight = reinterpret_cast<float*>(base + p.row_weight);
+  list.row_scale = reinterpret_cast<float*>(base + p.row_scale);
+  list.top_k = top_k;
   a.order = order;
   a.bands = list.bands;
   a.count = list.count;
-  a.band_tiles = p.band_tiles;
+  a.row_weight = list.row_weight;
+  a.row_scale = list.row_scale;
   a.p13 = w.p13;
   a.p2 = w.p2;
   a.s13 = w.s13;
@@ -409,7 +606,6 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   if (p.pad13 && (st = pad_scales(w.c13, experts * 2 * inter, hidden, base + p.c13, s))) return st;
   if (p.pad2 && (st = pad_scales(w.c2, experts * hidden, inter, base + p.c2, s))) return st;
   a.x = reinterpret_cast<const uint16_t*>(base + p.x);
-  a.xs = reinterpret_cast<const float*>(base + p.xs);
   for (int64_t t = 0; t < tokens; t += p.tokens) {
     const int64_t here = tokens - t < p.tokens ? tokens - t : p.tokens;
     a.x_bytes = (uint32_t)(here * hidden * 2);
@@ -417,11 +613,12 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
                                                     reinterpret_cast<uint16_t*>(base + p.x),
                                                     reinterpret_cast<float*>(base + p.xs));
     if ((st = launch_status("half_rows_kernel"))) return st;
-    a.weights = weights + t * top_k;
+    list.weights = weights + t * top_k;
     if ((st = launch_moe_sort(ids + t * top_k, here * top_k, experts, order, place,
                               reinterpret_cast<int32_t*>(base + p.offsets), base + p.sort, list, s)))
       return st;
-    if ((st = p.large ? run_products<Large>(a, p.max_bands, s) : run_products<Small>(a, p.max_bands, s))) return st;
+    st = p.few ? run_stream(a, s) : run_tiles(a, p.max_bands, s);
+    if (st) return st;
     if ((st = launch_moe_combine_half(a.ys, a.ye, place, here, top_k, hidden, y + t * ldy, ldy, s))) return st;
   }
   return NVFP4_OK;
