@@ -28,19 +28,44 @@ __device__ __forceinline__ f32x4 load_u(const LoraTerm& l, int64_t t, int r, int
   return v;
 }
 
-// acc (as store_tiles takes it) *= the tensor scale, and the term is added where
-// `add` (the same for a workgroup; all its waves call this).  The u of the tile's BM
-// tokens go to LDS, 64 ranks at a time, as the operands that they become.  A wave
-// then takes the (adapter, 16 ranks) pairs of its tokens, several at a time, so that
-// one wait serves their rows of B.  A token takes the sums of its own adapter alone,
-// so that another's infinities do not reach it; 32 tokens of one adapter need no
-// choice.
-template <int TN, int TM, int BM, int LDS>
+// Whether eight bf16 values are all finite.
+__device__ __forceinline__ bool all_finite(const i32x4& v) {
+  bool ok = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = (uint32_t)v[e];
+    ok &= (x & 0x7F800000u) != 0x7F800000u && (x & 0x7F80u) != 0x7F80u;
+  }
+  return ok;
+}
+
+// acc (as store_tiles takes it) *= the tensor scale, and the term is added (all waves
+// of the workgroup call this).  The u of the tile's BM tokens go to LDS, 64 ranks at a
+// time, as the operands that they become.  A wave takes the (adapter, 16 ranks) pairs
+// of its tokens one after another, the next two pairs' rows of B on their way; where
+// the channels are split, each split takes its share of the pairs.  Tokens of other
+// adapters have zeros for u, or, where B holds an infinity or NaN, sums of their own
+// that leave them out.
+//
+// It runs once a tile, so that its instructions come from memory more often than not:
+// loops stay rolled up.  61 tokens of 64 adapters of 4096x12288, rank 16, take 46 us,
+// 59 with four pairs at a time unrolled and the splits' shares of the channels alone;
+// 8192 tokens of 12288x4096, rank 64, 768 us, 682 of them without the adapters and 31
+// of them u.
+template <int TN, int TM, int BM, int LDS, int THREADS>
 __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out, f32x16 (&acc)[TN][TM], bool multiplies,
-                                         int o0, int tile0, int row0, bool add, uint8_t* lds) {
-  constexpr int PITCH = 144, PART = BM * PITCH, ITEMS = 4;     // 64 bf16 and 16 bytes: rows in all banks
-  static_assert(3 * PART <= LDS, "u in LDS");
+                                         int o0, int tile0, int row0, int split_at, int splits, uint8_t* lds) {
+  constexpr int PITCH = 144, PART = BM * PITCH;                  // 64 bf16 and 16 bytes: rows in all banks
+  static_assert(3 * PART <= LDS && BM * 8 % THREADS == 0, "u in LDS");
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  int id[TM];
+  bool any = false;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int t = tile0 + row0 + 32 * m + l32, v = l.ids[min(t, tokens - 1)];
+    id[m] = t >= tokens ? -2 : has_adapter(l, v) ? v : -1;       // -2: no token, whose results nobody takes
+    any |= id[m] >= 0;
+  }
   const float ws2 = *l.ws2;
 #pragma unroll
   for (int n = 0; n < TN; ++n)
@@ -48,106 +73,116 @@ __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out,
     for (int m = 0; m < TM; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[n][m][e] *= ws2;
-  if (!add) return;
-  bool any = false;
-#pragma unroll
-  for (int r = 0; r < BM; r += 64) {
-    const int t = tile0 + r + lane;
-    any |= r + lane < BM && t < tokens && has_adapter(l, l.ids[t]);
-  }
-  if (!__ballot(any)) return;                        // (the same for all waves)
-  int id[TM];
-#pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    const int t = tile0 + row0 + 32 * m + l32;
-    id[m] = t < tokens ? l.ids[t] : -2;              // -2: no token, whose results nobody takes
-    if (id[m] != -2 && !has_adapter(l, id[m])) id[m] = -1;
-  }
+  if (!__syncthreads_or(any)) return;
+#pragma unroll 1
   for (int c0 = 0; c0 < l.rank; c0 += 64) {
-    const int ranks = min(64, l.rank - c0);          // a multiple of 8
+    const int ranks = min(64, l.rank - c0);                      // a multiple of 8
     if (c0) __syncthreads();
-    for (int i = threadIdx.x; i < BM * 8; i += blockDim.x) {
-      const int row = i >> 3, r = (i & 7) * 8, t = tile0 + row;
-      uint32_t p[3][8] = {};
-      if (r < ranks && t < tokens && has_adapter(l, l.ids[t])) {
-        const f32x4 a = load_u(l, t, c0 + r), b = load_u(l, t, c0 + r + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          split(a[e], p[0][e], p[1][e], p[2][e]);
-          split(b[e], p[0][4 + e], p[1][4 + e], p[2][4 + e]);
-        }
-      }
-#pragma unroll
-      for (int z = 0; z < 3; ++z)
-        *reinterpret_cast<uint4*>(lds + z * PART + row * PITCH + r * 2) = make_uint4(
-            p[z][0] | p[z][1] << 16, p[z][2] | p[z][3] << 16, p[z][4] | p[z][5] << 16, p[z][6] | p[z][7] << 16);
-    }
-    __syncthreads();
-    if (!multiplies) continue;
     uint64_t live[TM];
 #pragma unroll
     for (int m = 0; m < TM; ++m) live[m] = __ballot(id[m] >= 0);
-    int a = -1, r = ranks;                           // the pair that was last
-    for (bool more = true; more;) {
-      int item_a[ITEMS], item_r[ITEMS];
-      uint4 w[ITEMS][TN];
+    // pairs: adapter a (-1: no more), ranks from r on
+    struct Pair { int a, r; i32x4 w[TN]; };
+    int a = multiplies ? 0 : -1, r = ranks, count = -1;
+    const auto next_pair = [&]() {
+      Pair p;
+      if (a >= 0) {
+        do {
+          ++count;
+          r += 16;
+          if (r >= ranks) {                                      // on to the adapter of the first token that has had none
+            r = 0;
+            a = -1;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        r += 16;
-        if (r >= ranks) {                            // on to the adapter of the first token that has had none
-          r = 0;
-          a = -1;
+            for (int m = TM - 1; m >= 0; --m)
+              if (live[m]) a = __builtin_amdgcn_readlane(id[m], __builtin_ctzll(live[m]));
 #pragma unroll
-          for (int m = TM - 1; m >= 0; --m)
-            if (live[m]) a = __builtin_amdgcn_readlane(id[m], __builtin_ctzll(live[m]));
-#pragma unroll
-          for (int m = 0; m < TM; ++m) live[m] &= ~__ballot(id[m] == a);
-        }
-        item_a[i] = a;
-        item_r[i] = r;
-        if (a < 0) r = ranks;                        // there is none any more
-#pragma unroll
-        for (int n = 0; n < TN; ++n) {
-          w[i][n] = make_uint4(0, 0, 0, 0);
-          if (a >= 0 && r + 8 * half < ranks)
-            w[i][n] = *reinterpret_cast<const uint4*>(
-                l.b + ((int64_t)a * out + min(o0 + 32 * n + l32, out - 1)) * l.rank + c0 + r + 8 * half);
-        }
+            for (int m = 0; m < TM; ++m) live[m] &= ~__ballot(id[m] == a);
+          }
+        } while (a >= 0 && count % splits != split_at);
       }
-      more = a >= 0;
+      p.a = a;
+      p.r = r;
+      // (past the last rank, and for no pair: some row, which is not used)
+      const int rank = min(c0 + r + 8 * half, l.rank - 8);
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        if (item_a[i] < 0) break;
+      for (int n = 0; n < TN; ++n)
+        p.w[n] = *reinterpret_cast<const i32x4*>(l.b + ((int64_t)max(a, 0) * out + min(o0 + 32 * n + l32, out - 1)) * l.rank +
+                                                 rank);
+      return p;
+    };
+    Pair next = next_pair(), after = next_pair();
+    // u, 8 ranks of a token at a time; zeros for a token without an adapter
+#pragma unroll 1
+    for (int at = threadIdx.x; at < BM * 8; at += THREADS) {
+      const int t = tile0 + (at >> 3), k = (at & 7) * 8, row = min(t, tokens - 1);
+      const bool have = t < tokens && k < ranks && has_adapter(l, l.ids[row]);
+      const float* src = l.u + (int64_t)row * l.rank + c0 + (k < ranks ? k : 0);
+      f32x4 u[2] = {*reinterpret_cast<const f32x4*>(src), *reinterpret_cast<const f32x4*>(src + 4)};
+#pragma unroll 1
+      for (int s = 1; s < l.splits; ++s) {
+        src += l.part;
+        u[0] += *reinterpret_cast<const f32x4*>(src);
+        u[1] += *reinterpret_cast<const f32x4*>(src + 4);
+      }
+      uint32_t p[3][8];
 #pragma unroll
-        for (int m = 0; m < TM; ++m) {
-          const bool mine = id[m] == item_a[i];
-          if (!__ballot(mine)) continue;
-          uint4 u[3];
+      for (int e = 0; e < 8; ++e) split(have ? u[e >> 2][e & 3] : 0.f, p[0][e], p[1][e], p[2][e]);
+#pragma unroll
+      for (int z = 0; z < 3; ++z)
+        *reinterpret_cast<uint4*>(lds + z * PART + (at >> 3) * PITCH + k * 2) = make_uint4(
+            p[z][0] | p[z][1] << 16, p[z][2] | p[z][3] << 16, p[z][4] | p[z][5] << 16, p[z][6] | p[z][7] << 16);
+    }
+    __syncthreads();
+#pragma unroll 1
+    while (next.a >= 0) {
+      const Pair now = next;
+      next = after;
+      after = next_pair();
+      // past the last rank: zeros, not another rank's values against u's zeros
+      const bool in = now.r + 8 * half < ranks;
+      i32x4 b[TN];
+      bool finite = true;
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        b[n] = in ? now.w[n] : i32x4{0, 0, 0, 0};
+        finite &= all_finite(b[n]);
+      }
+      finite = !__ballot(!finite);
+      const uint8_t* u = lds + (row0 + l32) * PITCH + (now.r + 8 * half) * 2;
+#pragma unroll
+      for (int m = 0; m < TM; ++m) {
+        const bool mine = id[m] == now.a;
+        if (!__ballot(mine)) continue;
+        i32x4 x[3];
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+          x[z] = *reinterpret_cast<const i32x4*>(u + z * PART + m * 32 * PITCH);
+          x[z] = mine ? x[z] : i32x4{0, 0, 0, 0};
+        }
+        if (__builtin_expect(finite || !__ballot(!mine && id[m] != -2), 1)) {
 #pragma unroll
           for (int z = 0; z < 3; ++z)
-            u[z] = *reinterpret_cast<const uint4*>(lds + z * PART + (row0 + 32 * m + l32) * PITCH + (item_r[i] + 8 * half) * 2);
-          if (!__ballot(!mine && id[m] != -2)) {
 #pragma unroll
             for (int n = 0; n < TN; ++n)
+              acc[n][m] = mfma32_16<false>(__builtin_bit_cast(uint4, b[n]), __builtin_bit_cast(uint4, x[z]), acc[n][m]);
+        } else {
 #pragma unroll
-              for (int z = 0; z < 3; ++z) acc[n][m] = mfma32_16<false>(w[i][n], u[z], acc[n][m]);
-          } else {
+          for (int n = 0; n < TN; ++n) {
+            f32x16 sum;
 #pragma unroll
-            for (int n = 0; n < TN; ++n) {
-              f32x16 sum;
+            for (int e = 0; e < 16; ++e) sum[e] = 0.f;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+            for (int z = 0; z < 3; ++z)
+              sum = mfma32_16<false>(__builtin_bit_cast(uint4, b[n]), __builtin_bit_cast(uint4, x[z]), sum);
 #pragma unroll
-              for (int z = 0; z < 3; ++z) sum = mfma32_16<false>(w[i][n], u[z], sum);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) acc[n][m][e] += mine ? sum[e] : 0.f;
-            }
+            for (int e = 0; e < 16; ++e) acc[n][m][e] += mine ? sum[e] : 0.f;
           }
         }
       }
     }
   }
-  __syncthreads();                                   // the results go through LDS next
+  __syncthreads();                                               // the results go through LDS next
 }
 
 }  // namespace nvfp4

@@ -198,7 +198,8 @@ __global__ __launch_bounds__(64 * (WM * WN + NL), NL && AHEAD == 2 ? 4 : 2) void
       [&](int row) { return (uint32_t)(min(row, rows_w - 1) * a.ldw); }, scales, lds,
       [&](f32x16 (&acc)[TN][TM], int wm, int wn, int wave, bool multiplies) {
         const int o = o0 + wn * TN * 32, t = t0 + wm * TM * 32;
-        (add_lora<TN, TM, T::BM, T::LDS>(lora, a.tokens, a.out, acc, multiplies, o, t0, wm * TM * 32, pos.split == 0, lds),
+        (add_lora<TN, TM, T::BM, T::LDS, T::THREADS>(lora, a.tokens, a.out, acc, multiplies, o, t0, wm * TM * 32, pos.split, a.splits,
+                                         lds),
          ...);
         if (!multiplies) return;
         store_tiles<TN, TM>(a, acc, o, t, pos.split, lds + wave * 32 * (64 * TN + 16));
