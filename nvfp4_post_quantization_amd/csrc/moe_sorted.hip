@@ -6,17 +6,24 @@
 //          weight(t, e) * W2_e ( silu(W1_e x[t]) * (W3_e x[t]) )
 //
 // The choices are sorted by expert, so that an expert's tokens are rows of row
-// tiles of its own, which the sort lists.  Two launches of the tile kernels that
-// multiply 16-bit rows by packed NVFP4 weights go over that list: the first reads
-// the tokens where they are and makes h = silu(gate) * up, the second makes
-// weight * s2 * W2 h, a row for every choice, and a last launch adds the rows of
-// each token.  The number of row tiles is known on the device only; the grids are
-// for the most there can be, and workgroups past the last tile end at once.
+// tiles of its own, which the sort lists.  Two launches that multiply 16-bit rows by
+// packed NVFP4 weights go over that list: the first reads the tokens where they are
+// and makes h = silu(gate) * up, the second makes weight * s2 * W2 h, a row for
+// every choice, and a last launch adds the rows of each token.  Where experts have
+// few rows these are streams of the weights (persistent workgroups), where they
+// have many, matrix tiles; their number is known on the device only, so the tiles'
+// grids are for the most there can be, and workgroups past the last end at once.
 //
-// Rounded on the way: h to bf16, which halves what moves and lets bf16 matrix
+// Rounded on the way: x to fp16 with a power of two a token (exact, but for values
+// far below the largest); h to bf16, which halves what moves and lets bf16 matrix
 // instructions take it (an error the size of the final rounding's); the rows to the
 // 11 bits of fp16, with a power of two of their own for every 32 columns, for a third
 // error of that size would show.
+//
+// 8 of 128 experts of 7168 x 2048: 100 tokens 0.68 ms (weights and rows that cross
+// memory at 4.7 TB/s: bound by that), 1023 tokens 1.30 ms (bound by neither; the
+// expansion of weights and the matrix products of 64 rows in turn), 8192 tokens 5.7
+// ms (1.01 PFLOP/s, the clocks of the matrix units under full power).
 #include "layer.hpp"
 #include "tile_device.hpp"
 

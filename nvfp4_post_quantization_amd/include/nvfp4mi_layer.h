@@ -83,8 +83,9 @@ NVFP4_CHECKED int nvfp4_moe_combine(const uint16_t* ys, int64_t ldys, const int3
  * Rows of dys to which no choice goes are left as they were; dweights of a place
  * outside 0 .. tokens*top_k-1 is 0.
  *
- * dy [tokens][lddy], ys [tokens * top_k][ldys], dys [tokens * top_k][lddys] (not
- * ys): bf16, as in nvfp4_moe_combine.  dweights [tokens][top_k] float.
+ * dy [tokens][lddy], ys [tokens * top_k][ldys], dys [tokens * top_k][lddys] (no
+ * memory of dy or ys): bf16, as in nvfp4_moe_combine.  place: no row twice.
+ * dweights [tokens][top_k] float.
  * Errors: as nvfp4_moe_combine.
  */
 NVFP4_CHECKED int nvfp4_moe_combine_grad(const uint16_t* dy, int64_t lddy, const uint16_t* ys, int64_t ldys,
@@ -95,12 +96,16 @@ NVFP4_CHECKED int nvfp4_moe_combine_grad(const uint16_t* dy, int64_t lddy, const
  * nvfp4_moe_forward for any number of tokens: the same layer and arguments,
  *   y[t] = RN_bf16( sum_s weights[t][s] W2_e ( silu(W1_e x[t]) * (W3_e x[t]) ) ).
  * Up to 64 tokens it is that function's streaming kernels; beyond, the tokens are
- * sorted by expert, silu(..)*(..) is rounded to bf16, everything else stays in
- * fp32 (the sum over s ascending).  An id outside 0..experts-1 adds nothing; a
+ * sorted by expert.  Sums are in fp32 (that over s ascending); three things are
+ * rounded before y: x enters as fp16 with a power of two for each token, which is
+ * exact but for values 2^29 and more below the token's largest (off by 2^-39 of that
+ * at most); silu(..)*(..) to bf16; and an expert's row, weight included, to fp16 with
+ * a power of two for every 32 columns.  An id outside 0..experts-1 adds nothing; a
  * token without any gets zeros; an expert that a token names twice counts twice.
  *
- * Arguments as nvfp4_moe_forward; tokens * top_k at most 2^30; hidden and inter
- * multiples of 16, at most 2^17, their product below 2^31.
+ * Arguments as nvfp4_moe_forward (rows of x and y 16-byte aligned); tokens * top_k
+ * at most 2^30; hidden and inter multiples of 16, at most 2^17, their product below
+ * 2^31.
  * workspace  256-byte aligned, at least nvfp4_moe_forward_sorted_workspace_bytes(...)
  *            bytes (more than 131072 choices go pass by pass, which bounds it).
  * Errors: NULL_ARG, BAD_SHAPE, BAD_INPUT (top_k, experts), MISALIGNED, WORKSPACE,

@@ -1,0 +1,315 @@
+"""Router, sort, rows, expert layer and adapters together, as a program uses them:
+chained, for calibration and for training, captured and replayed, on two streams,
+with workspaces of exactly their size, and with no tokens at all."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_post_quantization_amd as nq
+import oracle as O
+from oracle import formats as F
+from oracle import layer as L
+from oracle import nvfp4 as N
+from oracle.product import silu
+
+import test_gpu_layer_experts as experts_test
+import test_gpu_layer_lora as lora_test
+from _gpu import DEV, host, need_gpu, note, rel_frobenius, to_dev_bf16, to_dev_f32, to_host_bits
+
+pytestmark = pytest.mark.gpu
+
+HALF, EPS = 2.0 ** -8, 2.0 ** -23
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def _vals(t):
+    return F.bf16_bits_to_f64(to_host_bits(t))
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _by_hand(x, ids, wt, c):
+    """(y, ys, place): the layer of Case c from its parts, products expert by expert."""
+    order, place, offsets = nq.moe_sort(ids, c.experts)
+    xs = nq.moe_dispatch(x, place)
+    ys = torch.zeros_like(xs)
+    p13, c13, s13, p2, c2, s2 = c.dev
+    first = host(offsets)
+    for e in range(c.experts):
+        rows = slice(int(first[e]), int(first[e + 1]))
+        if rows.start == rows.stop:
+            continue
+        gate, up = (nq.matmul_w4a16(xs[rows], p13[e, i], c13[e, i], s13[e:e + 1]).float() for i in (0, 1))
+        h = (gate / (1 + torch.exp(-gate)) * up).to(torch.bfloat16)
+        nq.matmul_w4a16(h, p2[e, 0], c2[e, 0], s2[e:e + 1], out=ys[rows])
+    return nq.moe_combine(ys, place, wt), ys, place
+
+
+def _hand_bound(x, ids, wt, w13, w2):
+    """(y, bound before y's rounding) where gate, up, silu * up and the experts'
+    rows are each rounded to bf16; sums of n products are off by n EPS of the
+    magnitudes, silu' lies in [-0.1, 1.1], silu is good to 2^-20."""
+    y, off = np.zeros_like(x), np.zeros_like(x)
+    for e in range(w13.shape[0]):
+        t, s = np.nonzero(ids == e)
+        xe, w = x[t], wt[t, s, None]
+        def product(a, da, m):
+            r = a @ m.T
+            d = da @ np.abs(m).T + (a.shape[1] + 3) * EPS * ((np.abs(a) + da) @ np.abs(m).T)
+            return r, d + HALF * (np.abs(r) + d)
+        gate, dg = product(xe, 0 * xe, w13[e, 0])
+        up, du = product(xe, 0 * xe, w13[e, 1])
+        h = silu(gate) * up
+        dh = 1.1 * dg * (np.abs(up) + du) + np.abs(silu(gate)) * du
+        dh += (HALF + 2.0 ** -20) * (np.abs(h) + dh)
+        row, dr = product(h, dh, w2[e])
+        np.add.at(y, t, w * row)
+        np.add.at(off, t, np.abs(w) * (dr + (ids.shape[1] + 1) * EPS * (np.abs(row) + dr)))
+    return y, off
+
+
+@pytest.mark.parametrize("tokens", [90, 500])
+def test_projection_router_and_layer(tokens):
+    """x -> projection with adapters -> router -> expert layer, at once and from its
+    parts; then the gradients of the way there and back."""
+    note(f"projection, router and layer, {tokens} tokens")
+    experts, top_k, hidden, inter = 12, 3, 256, 80
+    proj = lora_test.Case(tokens, tokens, hidden, 512, 5, 16)
+    c = experts_test.Case(tokens + 1, tokens, hidden, inter, experts, top_k)
+    x = nq.matmul_w4a16_lora(to_dev_bf16(proj.x), *proj.args())
+    proj.check(x)
+    logits = torch.randn((tokens, experts), generator=_gen(1), device=DEV)
+    logits[5] = float("-inf")                                        # a token without an expert
+    logits[7, 1:] = float("-inf")                                    # and one with a single one
+    ids, wt = nq.moe_route(logits, top_k)
+    c.x, c.ids, c.wt = to_host_bits(x), host(ids), host(wt)
+    y = nq.moe_forward_sorted(x, ids, wt, *c.dev)
+    c.check(y)
+    assert not y[5].any()
+    hand, ys, place = _by_hand(x, ids, wt, c)
+    p13, c13, s13, p2, c2, s2 = c.w
+    ref, off = _hand_bound(_vals(x), c.ids, c.wt.astype(np.float64), O.nvfp4_values(p13, c13, s13),
+                           O.nvfp4_values(p2, c2, s2)[:, 0])
+    assert np.all(np.abs(_vals(hand) - ref) <= HALF * np.abs(ref) + off * (1 + HALF) + 2.0 ** -120)
+    # the gradients, on the rows that there are
+    dy = torch.randn((tokens, hidden), generator=_gen(2), device=DEV).to(torch.bfloat16)
+    dys, dw = nq.moe_combine_grad(dy, ys, place, wt)
+    want, dw_ref, mag = L.moe_combine_grad(_vals(dy), _vals(ys), host(place), c.wt.astype(np.float64))
+    rows = ~np.isnan(want[:, 0])
+    got = _vals(dys)[rows]
+    assert np.all(np.abs(got - want[rows]) <= (HALF + 2 * EPS) * np.abs(want[rows]) + 2.0 ** -134)
+    assert np.all(np.abs(host(dw) - dw_ref) <= hidden * EPS * mag)
+    dx = nq.moe_dispatch_grad(dys, place)
+    full = np.zeros_like(want)
+    full[rows] = got
+    ref, mag = L.moe_combine(full, host(place))
+    assert np.all(np.abs(_vals(dx) - ref) <= HALF * np.abs(ref) + top_k * EPS * mag * (1 + HALF) + 2.0 ** -134)
+
+
+def test_calibration_of_experts():
+    """Each expert's Hessian from its own tokens, and quantized rows moved as they are."""
+    note("calibration of experts")
+    tokens, top_k, experts, hidden = 700, 2, 6, 96
+    rng = np.random.default_rng(3)
+    bits = F.f64_to_bf16_bits(rng.standard_normal((tokens, hidden)))
+    ids = rng.integers(-1, experts - 1, (tokens, top_k)).astype(np.int32)         # the last expert has none
+    x = to_dev_bf16(bits)
+    order, place, offsets = nq.moe_sort(torch.from_numpy(ids).to(DEV), experts)
+    xs = nq.moe_dispatch(x, place)
+    H = torch.zeros((experts, hidden // 16, 16, 16), dtype=torch.float32, device=DEV)
+    first = host(offsets)
+    assert first[-2] == first[-1] == (ids >= 0).sum()
+    for e in range(experts - 1):
+        nq.hessian_accum(xs[first[e]:first[e + 1]], H[e])
+        t, _ = np.nonzero(ids == e)
+        assert rel_frobenius(host(H[e]), N.hessian(bits[t])).max() <= 1e-5
+    s2, _ = nq.compute_scale2(x)
+    rows = host(order)[:first[-1]] // top_k
+    for q in nq.quantize_dynamic(x, s2):
+        moved = nq.moe_dispatch(q, place)
+        assert np.array_equal(host(moved)[:first[-1]], host(q)[rows])
+
+
+class Step:
+    """Everything once, into buffers of its own."""
+
+    def __init__(self, tokens, top_k, experts, seed):
+        hidden, inter = 192, 96
+        self.c = experts_test.Case(seed, tokens, hidden, inter, experts, top_k)
+        self.p = lora_test.Case(seed, tokens, hidden, 272, 6, 24)
+        self.weights = self.p.args()
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.zeros(shape, dtype=dtype, device=DEV)
+        n, i32, f32, u8 = tokens * top_k, torch.int32, torch.float32, torch.uint8
+        self.h = empty(tokens, hidden)
+        self.route = empty(tokens, top_k, dtype=i32), empty(tokens, top_k, dtype=f32)
+        self.sort = empty(n, dtype=i32), empty(tokens, top_k, dtype=i32), empty(experts + 1, dtype=i32)
+        self.xs, self.back, self.dys, self.dx = empty(n, hidden), empty(tokens, hidden), empty(n, hidden), empty(tokens, hidden)
+        self.dw, self.y = empty(tokens, top_k, dtype=f32), empty(tokens, hidden)
+        self.ws = [empty(b, dtype=u8) for b in (nq.matmul_lora_workspace_bytes(*self.p.dims),
+                                                max(nq.moe_sort_workspace_bytes(tokens, top_k, experts), 1),
+                                                nq.moe_sorted_workspace_bytes(tokens, top_k, experts, hidden, inter))]
+
+    def run(self, x, logits):
+        nq.matmul_w4a16_lora(x, *self.weights, out=self.h, workspace=self.ws[0])
+        ids, wt = nq.moe_route(logits, self.c.top_k, out=self.route)
+        _, place, _ = nq.moe_sort(ids, self.c.experts, out=self.sort, workspace=self.ws[1])
+        nq.moe_dispatch(self.h, place, out=self.xs)
+        nq.moe_combine(self.xs, place, wt, out=self.back)
+        nq.moe_combine_grad(self.h, self.xs, place, wt, out=(self.dys, self.dw))
+        nq.moe_dispatch_grad(self.dys, place, out=self.dx)
+        nq.moe_forward_sorted(self.h, ids, wt, *self.c.dev, out=self.y, workspace=self.ws[2])
+
+    def results(self):
+        return [*self.route, *self.sort, self.h, self.xs, self.back, self.dys, self.dx, self.dw, self.y]
+
+    def inputs(self, seed):
+        g = _gen(seed)
+        logits = torch.randn((self.c.tokens, self.c.experts), generator=g, device=DEV)
+        logits[::7] = float("-inf")
+        return torch.randn((self.c.tokens, 272), generator=g, device=DEV).to(torch.bfloat16), logits
+
+
+# streamed, many experts, and tiles with several workgroups of the sort
+STEPS = [(40, 2, 8), (100, 4, 40), (700, 8, 16)]
+
+
+@pytest.mark.parametrize("tokens,top_k,experts", STEPS)
+def test_captured(tokens, top_k, experts):
+    note(f"captured step, {tokens}x{top_k} of {experts}")
+    inputs, want = [], []
+    for seed in range(3):
+        s = Step(tokens, top_k, experts, 9)
+        inputs.append(s.inputs(seed))
+        s.run(*inputs[-1])
+        want.append([r.clone() for r in s.results()])
+    s, eager = Step(tokens, top_k, experts, 9), Step(tokens, top_k, experts, 9)
+    x, logits = (v.clone() for v in inputs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run(x, logits)
+    for i in (1, 2, 0, 0, 1):
+        x.copy_(inputs[i][0])
+        logits.copy_(inputs[i][1])
+        for r in (*s.results(), *eager.results()):                   # (rows behind the last: zeros in `want`)
+            r.zero_()
+        for w in s.ws:
+            w.fill_(0xFF)
+        graph.replay()
+        eager.run(*inputs[i])                                        # eager work beside and between replays
+        torch.cuda.synchronize()
+        for a, b, r in zip(s.results(), eager.results(), want[i]):
+            assert torch.equal(a, r) and torch.equal(b, r)
+
+
+def test_two_streams():
+    note("two streams")
+    steps = [Step(60, 4, 16, 1), Step(600, 8, 16, 2)]
+    inputs = [s.inputs(5) for s in steps]
+    want = []
+    for s, i in zip(steps, inputs):
+        s.run(*i)
+        want.append([r.clone() for r in s.results()])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for s, i, stream in zip(steps, inputs, streams):
+            with torch.cuda.stream(stream):
+                for r in s.results():
+                    r.zero_()
+                s.run(*i)
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        assert all(torch.equal(a, b) for a, b in zip(s.results(), w))
+
+
+class Guarded:
+    """A workspace of exactly `size` bytes between bytes that stay."""
+
+    def __init__(self, size):
+        self.all = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.ws = self.all[256:256 + size]
+
+    def check(self):
+        assert (self.all[:256] == 0xA5).all() and (self.all[256 + self.ws.numel():] == 0xA5).all()
+
+
+@pytest.mark.parametrize("tokens,top_k,experts", [(65, 16, 7), (700, 8, 16), (300, 3, 1024), (9000, 16, 40)])
+def test_workspaces_are_enough(tokens, top_k, experts):
+    note(f"workspaces, {tokens}x{top_k} of {experts}")
+    c = experts_test.Case(3, tokens, 80, 48, experts, top_k)
+    ws = Guarded(nq.moe_sorted_workspace_bytes(tokens, top_k, experts, 80, 48))
+    y = c.run(ws=ws.ws)
+    ws.check()
+    assert torch.equal(y, c.run())
+    size = nq.moe_sort_workspace_bytes(tokens, top_k, experts)
+    if size:
+        ws, ids = Guarded(size), torch.from_numpy(c.ids).to(DEV)
+        got = nq.moe_sort(ids, experts, workspace=ws.ws)
+        ws.check()
+        assert all(torch.equal(a, b) for a, b in zip(got, nq.moe_sort(ids, experts)))
+
+
+@pytest.mark.parametrize("tokens,rank", [(1, 8), (5, 256), (16, 24), (61, 72), (500, 16), (1100, 136)])
+def test_adapter_workspaces_are_enough(tokens, rank):
+    note(f"adapter workspace, {tokens} tokens, rank {rank}")
+    c = lora_test.Case(4, tokens, 144, 1040, 5, rank)
+    ws = Guarded(nq.matmul_lora_workspace_bytes(*c.dims))
+    y = c.run(ws=ws.ws)
+    ws.check()
+    assert torch.equal(y, c.run())
+
+
+@pytest.mark.parametrize("tokens", [70, 700])
+def test_values_far_below_their_token_s_largest(tokens):
+    """x enters as fp16 with a power of two a token that puts the largest value into
+    2^14 .. 2^15: what that rounds is known, and is at most 2^-39 of the largest."""
+    note(f"layer, small values, {tokens} tokens")
+    c = experts_test.Case(8, tokens, 272, 48, 8, 2)
+    rng = np.random.default_rng(9)
+    x = F.bf16_bits_to_f64(c.x) * 2.0 ** -rng.integers(0, 44, c.x.shape).astype(np.float64)
+    x[:, 200:] = 0
+    x[3] *= 2.0 ** 30
+    x[4] *= 2.0 ** -20
+    x[5] = 0
+    c.x = F.f64_to_bf16_bits(x)
+    x = F.bf16_bits_to_f64(c.x)
+    top = np.abs(x).max(1, keepdims=True)
+    unit = np.exp2(np.floor(np.log2(np.where(top > 0, top, 1.0))) - 14)
+    rounded = (x / unit).astype(np.float16).astype(np.float64) * unit
+    assert np.all(np.abs(rounded - x) <= 2.0 ** -39 * top) and (rounded != x).any()
+    assert np.all((rounded == x) | (np.abs(x) < 2.0 ** -29 * top))
+    w = [O.nvfp4_values(*c.w[:3]), O.nvfp4_values(*c.w[3:])[:, 0]]
+    with np.errstate(over="ignore"):
+        ref, off = L.moe_forward_sorted(rounded, c.ids, c.wt.astype(np.float64), *w, EPS, HALF + 32 * EPS, 2.0 ** -11)
+    got = _vals(c.run())
+    assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + off * (1 + HALF) + 2.0 ** -120)
+
+
+def test_no_tokens():
+    note("no tokens")
+    def none(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device=DEV)
+    c = experts_test.Case(1, 1, 64, 32, 4, 2)
+    p = lora_test.Case(1, 1, 48, 64, 2, 8)
+    ids, wt = none(0, 2, dtype=torch.int32), none(0, 2, dtype=torch.float32)
+    _, place, offsets = nq.moe_sort(ids, 4)
+    assert host(offsets).tolist() == [0] * 5
+    assert nq.moe_dispatch(none(0, 64), place).shape == (0, 64)
+    assert nq.moe_combine(none(0, 64), place, wt).shape == (0, 64)
+    assert nq.moe_dispatch_grad(none(0, 64), place).shape == (0, 64)
+    dys, dw = nq.moe_combine_grad(none(0, 64), none(0, 64), place, wt)
+    assert dys.shape == (0, 64) and dw.shape == (0, 2)
+    assert nq.moe_forward_sorted(none(0, 64), ids, wt, *c.dev).shape == (0, 64)
+    weights = p.args()
+    weights[3] = none(0, dtype=torch.int32)
+    assert nq.matmul_w4a16_lora(none(0, 64), *weights).shape == (0, 48)
+    torch.cuda.synchronize()
