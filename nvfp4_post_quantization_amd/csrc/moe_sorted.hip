@@ -119,19 +119,161 @@ __device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, Ti
   return t.rows > 0;
 }
 
+// (a conditional on the variables themselves would choose among their addresses,
+// which puts them in memory)
+__device__ __forceinline__ uint32_t beyond_if(bool cut, uint32_t offset) { return cut ? kBeyond : offset; }
+
 // The tile kernels' form: 4 waves, 64 output rows each; a row tile has up to 128 rows,
 // and the workgroup takes the least multiple of 32 that holds it, so that products of
 // rows that are not there are left out.  Two workgroups share a CU (one of 256 x 256,
 // whose start and end nothing hides: 6.2 ms against 5.9 for 8192 tokens).
-constexpr int tile_ahead(int tm) { return tm == 1 ? 4 : 2; }                 // stages, as LDS allows
+//
+// A stage is 64 channels.  What bounds the tiles of few rows is how many pieces of
+// cache lines are asked for, so weights come two stages at a time, 64 bytes a row
+// (every second stage), and scales eight stages at a time, 32 bytes a row (an eighth
+// of the rows with every stage).  Two of each are kept in LDS, and two stages of x.
 struct Tiles {
-  static constexpr int TN = 2, WN = 4, ROWS = 128, BN = 32 * TN * WN, THREADS = 64 * WN;
-  template <int TM, bool PAIRED>
-  using Tile = NvTile<TM, TN, 1, WN, 0, tile_ahead(TM), PAIRED>;
-  static constexpr int LDS = Tile<4, false>::LDS;    // the most that any takes
-  static_assert(Tile<1, false>::LDS <= LDS && Tile<2, false>::LDS <= LDS && Tile<3, false>::LDS <= LDS, "stages");
-  static_assert(WN * 32 * (64 * TN + 16) <= LDS && 2 * LDS <= 160 * 1024, "store staging; two workgroups a CU");
+  static constexpr int TN = 2, WAVES = 4, ROWS = 128, BN = 32 * TN * WAVES, THREADS = 64 * WAVES;
+  static constexpr int PAIR = BN * 64, GROUP = BN * 32;          // weights of two stages, scales of eight
+  static constexpr int WL = PAIR / 1024 / WAVES;                 // loads of a wave
+  static constexpr int LDS = 2 * (4 * 4096 + PAIR + GROUP);
 };
+static_assert(Tiles::WAVES * 32 * (64 * Tiles::TN + 16) <= Tiles::LDS && 2 * Tiles::LDS <= 160 * 1024,
+              "store staging; two workgroups a CU");
+
+// One tile of 32 TM rows: acc[n][m] as store_tiles takes it, to finish(acc, wave).
+//   bx, bw, bs     buffers of the rows, the packed weights and their scales (stride bytes
+//                  a row, scale_bytes in all)
+//   x_at(row), w_at(row)   the bytes in them at which the tile's rows begin
+//   PAIRED         of 32 rows of the tile the first 16 and the others are as many rows of
+//                  two matrices, whose scales are `pair` bytes apart
+// Lane half h of an instruction takes channels 32 h + 8 j .. + 7 of the stage at step
+// j, so that a lane's weights of a stage are one 16-byte piece.
+template <bool F16, bool PAIRED, int TM, typename XAt, typename WAt, typename Finish>
+__device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XAt x_at, WAt w_at, int stride,
+                                         uint32_t scale_bytes, int pair, uint8_t* lds, Finish finish) {
+  constexpr int TN = Tiles::TN, WAVES = Tiles::WAVES, WL = Tiles::WL;
+  constexpr int XB = TM * 4096, W_AT = 2 * XB, S_AT = W_AT + 2 * Tiles::PAIR;
+  static_assert(S_AT + 2 * Tiles::GROUP <= Tiles::LDS, "stages");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31, end = (k + 63) >> 6;
+  const uint32_t lds_wave = lds_address(lds) + wave * 1024;
+  // loads of x: 8 rows each; of weights: 16 rows
+  uint32_t xo[TM], wo[WL];
+  const int xpiece = (lane & 7) ^ swizzle128(wave * 8 + (lane >> 3));
+  const int wpiece = (lane & 3) ^ swizzle64(lane >> 2);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) xo[i] = x_at((wave + i * WAVES) * 8 + (lane >> 3)) + xpiece * 16;
+#pragma unroll
+  for (int i = 0; i < WL; ++i) wo[i] = w_at((wave + i * WAVES) * 16 + (lane >> 2)) + wpiece * 16;
+  // Of scales: 8 rows, block 4 e + wave of the tile's; word w of a row lies at place w ^
+  // (row >> 3 & 7), so that 32 rows' words lie in as many banks.
+  const int word = (lane & 7) ^ wave;
+  const uint32_t so = (uint32_t)((PAIRED ? (wave & 1) * 8 : wave * 8) + (lane >> 3)) * stride +
+                      (PAIRED ? (wave >> 1) * pair : 0) + word * 4;
+  const int odd = word & 4 ? -16 : 16;
+
+  const auto load_x = [&](int s, auto whole) {
+    const bool cut = !whole && s * 64 + xpiece * 8 >= k;
+    const uint32_t dst = lds_wave + (s & 1) * XB;
+    each<TM>([&](auto i) { load_lds16<i * WAVES * 1024>(bx, dst, beyond_if(cut, xo[i]), s * 128); });
+  };
+  const auto load_w = [&](int p) {                               // (past k: zeros)
+    const bool cut = p * 128 + wpiece * 32 >= k;
+    const uint32_t dst = lds_wave + (p & 1) * Tiles::PAIR;
+    each<WL>([&](auto i) { load_lds16<W_AT + i * WAVES * 1024>(bw, dst, beyond_if(cut, wo[i]), p * 64); });
+  };
+  // (words past a row's end: read, not used; a scalar offset is held to the buffer's
+  // size, which keeps the bounds check right)
+  const auto load_scales = [&](int i) {                          // eighth i & 7 of group i >> 3
+    const int g = i >> 3, e = i & 7;
+    const uint32_t base = (uint32_t)(g * 32 + e * (PAIRED ? 16 : 32) * stride);
+    load_lds4<S_AT>(bs, lds_address(lds) + (g & 1) * Tiles::GROUP + (e * WAVES + wave) * 256, so + (e & 1 ? odd : 0),
+                    (int)min(base, scale_bytes));
+  };
+
+  uint4 xr[2][TM], wr[TN], wr_next[TN];
+  uint32_t wsr[TN], wsr_next[TN];
+  const int x_row = l32 * 128, w_row = (wave * TN * 32 + l32);
+  const auto read_x = [&](int set, int j, int s) {
+    const uint8_t* b = lds + (s & 1) * XB + x_row + (((4 * half + j) ^ swizzle128(l32)) << 4);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xr[set][i] = *reinterpret_cast<const uint4*>(b + i * 4096);
+  };
+  const auto read_w = [&](int s) {
+    const uint8_t* b = lds + W_AT + (s >> 1 & 1) * Tiles::PAIR + w_row * 64 + (((2 * (s & 1) + half) ^ swizzle64(l32)) << 4);
+    const uint8_t* c = lds + S_AT + (s >> 3 & 1) * Tiles::GROUP + w_row * 32;
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+      wr_next[n] = *reinterpret_cast<const uint4*>(b + n * 2048);
+      wsr_next[n] = *reinterpret_cast<const uint32_t*>(c + n * 1024 + (((s & 7) ^ (4 * n) ^ (l32 >> 3)) << 2));
+    }
+  };
+  static_assert(TN == 2, "a wave's rows start at a multiple of 64");
+
+  f32x16 acc[TN][TM];
+#pragma unroll
+  for (int n = 0; n < TN; ++n)
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
+
+  // The eighth that is loaded with the end of stage s is s + 9: it is there a stage on,
+  // the last of a group before the group's first stage is read; the group before the
+  // last one has been read when the first is loaded.
+#pragma unroll
+  for (int i = 0; i < 9; ++i) load_scales(i);
+  load_x(0, std::false_type{});
+  load_w(0);
+  if (end > 1) {
+    load_x(1, std::false_type{});
+    load_w(1);
+    wait_loads<TM + WL>();
+  } else {
+    wait_loads<0>();
+  }
+  stage_barrier();
+  read_w(0);
+  read_x(0, 0, 0);
+  run_stages<2>(0, end, k >> 6, [&](int s, auto way) {
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+      wr[n] = wr_next[n];
+      wsr[n] = wsr_next[n] >> (16 * half);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < 3) {
+        read_x((j + 1) & 1, j + 1, s);
+      } else if constexpr (way != kLast) {
+        // Stage s + 1 is to be there (the pair of weights behind its x may be on its
+        // way), and all that is read of stage s in registers: s + 2 takes its place.
+        if (way == kDrain || (s & 1)) wait_loads<0>();
+        else wait_loads<WL>();
+        lds_barrier();
+        if constexpr (way != kDrain) {
+          load_x(s + 2, std::bool_constant<way == kWhole>{});
+          load_scales(s + 9);
+          if (s & 1) load_w((s + 3) >> 1);
+        }
+        read_w(s + 1);
+        read_x(0, 0, s + 1);
+      }
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        const uint32_t nib = j == 0 ? wr[n].x : j == 1 ? wr[n].y : j == 2 ? wr[n].z : wr[n].w;
+        const float c = j < 2 ? e4m3_f32<0>(wsr[n]) : e4m3_f32<1>(wsr[n]);
+        const uint4 w = F16 ? fp4x8_f16(nib, splat_f16(c)) : fp4x8_bf16(nib, c);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_16<F16>(w, xr[j & 1][m], acc[n][m]);
+      }
+    }
+  });
+  __syncthreads();                                               // the stages are done with
+  finish(acc, wave);
+}
+
 template <typename Body>
 __device__ __forceinline__ void with_rows(int rows, Body f) {
   if (rows <= 32) f(std::integral_constant<int, 1>{});
@@ -253,17 +395,15 @@ __global__ __launch_bounds__(Tiles::THREADS, 2) void moe_up_tile_kernel(SortedAr
   const int rows_w = 2 * a.inter - ch0;              // to the end of the expert's up rows
   const auto bx = make_buffer(a.x, a.x_bytes);
   const auto bw = make_buffer(a.p13 + row * ldw, (uint32_t)rows_w * ldw);
+  const uint32_t bytes_s = (uint32_t)rows_w * a.lds13;
+  const auto bs = make_buffer(a.c13 + row * a.lds13, bytes_s);
   with_rows(t.rows, [&](auto tm) {
     constexpr int TM = decltype(tm)::value;
-    using T = Tiles::Tile<TM, true>;
-    const typename T::Scales scales(a.c13 + row * a.lds13, rows_w * a.lds13, a.lds13, a.inter * a.lds13,
-                           lds_address(lds) + T::NBUF * T::STAGE, 0, loader_of<T::NW, 0>());
-    nv_tile<true, TM, TN, 1, Tiles::WN, 0, tile_ahead(TM)>(
-        bx, bw, a.hidden, 0, (a.hidden + 63) >> 6,
-        [&](int r) { return (uint32_t)(a.order[t.first + min(r, t.rows - 1)] / a.top_k) * ldx; },
-        [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; }, scales,
-        lds, [&](const f32x16 (&acc)[TN][TM], int, int wn, int wave, bool) {
-          put_h<TN, TM>(a, t, acc, RowValues<TM>(a.row_scale, t, a.s13[t.expert]), ch0 + wn * TN * 16,
+    run_tile<true, true, TM>(
+        bx, bw, bs, a.hidden, [&](int r) { return (uint32_t)(a.order[t.first + min(r, t.rows - 1)] / a.top_k) * ldx; },
+        [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; },
+        a.lds13, bytes_s, a.inter * a.lds13, lds, [&](const f32x16 (&acc)[TN][TM], int wave) {
+          put_h<TN, TM>(a, t, acc, RowValues<TM>(a.row_scale, t, a.s13[t.expert]), ch0 + wave * TN * 16,
                         lds + wave * 32 * (32 * TN + 16));
         });
   });
@@ -280,16 +420,15 @@ __global__ __launch_bounds__(Tiles::THREADS, 2) void moe_down_tile_kernel(Sorted
   const int64_t row = (int64_t)t.expert * a.hidden + o0;
   const auto bx = make_buffer(a.h + (int64_t)t.first * a.inter, (uint32_t)t.rows * ldh);
   const auto bw = make_buffer(a.p2 + row * ldw, (uint32_t)rows_w * ldw);
+  const uint32_t bytes_s = (uint32_t)rows_w * a.lds2;
+  const auto bs = make_buffer(a.c2 + row * a.lds2, bytes_s);
   with_rows(t.rows, [&](auto tm) {
     constexpr int TM = decltype(tm)::value;
-    using T = Tiles::Tile<TM, false>;
-    const typename T::Scales scales(a.c2 + row * a.lds2, rows_w * a.lds2, a.lds2, 0, lds_address(lds) + T::NBUF * T::STAGE, 0,
-                           loader_of<T::NW, 0>());
-    nv_tile<false, TM, TN, 1, Tiles::WN, 0, tile_ahead(TM)>(
-        bx, bw, a.inter, 0, (a.inter + 63) >> 6, [&](int r) { return (uint32_t)min(r, t.rows - 1) * ldh; },
-        [&](int r) { return (uint32_t)min(r, rows_w - 1) * ldw; }, scales, lds,
-        [&](f32x16 (&acc)[TN][TM], int, int wn, int wave, bool) {
-          put_rows<TN, TM>(a, t, acc, RowValues<TM>(a.row_weight, t, a.s2[t.expert]), o0 + wn * TN * 32,
+    run_tile<false, false, TM>(
+        bx, bw, bs, a.inter, [&](int r) { return (uint32_t)min(r, t.rows - 1) * ldh; },
+        [&](int r) { return (uint32_t)min(r, rows_w - 1) * ldw; }, a.lds2, bytes_s, 0, lds,
+        [&](f32x16 (&acc)[TN][TM], int wave) {
+          put_rows<TN, TM>(a, t, acc, RowValues<TM>(a.row_weight, t, a.s2[t.expert]), o0 + wave * TN * 32,
                            lds + wave * 32 * (64 * TN + 16));
         });
   });
@@ -318,10 +457,6 @@ struct Stream {
   static constexpr int TURN = 8 * 4096;
   static_assert(TURN + 8 * 32 * 80 <= ROW, "the end of a tile");
 };
-
-// (a conditional on the variables themselves would choose among their addresses,
-// which puts them in memory)
-__device__ __forceinline__ uint32_t beyond_if(bool cut, uint32_t offset) { return cut ? kBeyond : offset; }
 
 // A word that all lanes want, past the vector loads in flight.
 __device__ __forceinline__ int scalar_load(const int32_t* p) {
