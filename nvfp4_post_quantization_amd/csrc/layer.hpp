@@ -14,12 +14,12 @@ constexpr int64_t kMaxChoices = INT64_C(1) << 30;
 // A band of the expert layer: rows first .. first + rows - 1 are expert's.
 struct ExpertBand { int expert, first, rows, unused; };
 // What the sort also writes for the expert layer (bands NULL: nothing): the bands of
-// up to `rows` rows, those of more units first, and by row its choice's weight and
-// its token's scale.
+// up to kBandRows rows, those of more kBandUnit rows first, and by row its choice's
+// weight and its token's scale.
+constexpr int kBandRows = 256, kBandUnit = 32;
 struct BandList {
   ExpertBand* bands;
   int* count;
-  int rows, unit;
   const float *weights, *scales;
   float *row_weight, *row_scale;
   int top_k;

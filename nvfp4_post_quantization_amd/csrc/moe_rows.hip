@@ -134,12 +134,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   if (g == 0 && tid == 0) a.offsets[E] = (int32_t)rows;
   if (a.list.bands && g == 0) {                                  // (the same way for all threads)
     // whole bands first, then the experts' last ones, those of most units first
-    const uint32_t most = a.list.rows, whole = total / most, rest = total % most;
-    const uint32_t units = (rest + a.list.unit - 1) / a.list.unit;
+    constexpr uint32_t most = kBandRows;
+    const uint32_t whole = total / most, rest = total % most;
+    const uint32_t units = (rest + kBandUnit - 1) / kBandUnit;
     uint32_t count;
     uint32_t at = block_scan(whole, part, count);
     for (uint32_t i = 0; i < whole; ++i) a.list.bands[at + i] = ExpertBand{tid, (int)(first + i * most), (int)most, 0};
-    for (uint32_t u = most / a.list.unit; u > 0; --u) {
+    for (uint32_t u = most / kBandUnit; u > 0; --u) {
       uint32_t more;
       at = count + block_scan(units == u ? 1 : 0, part, more);
       if (units == u) a.list.bands[at] = ExpertBand{tid, (int)(first + whole * most), (int)rest, 0};

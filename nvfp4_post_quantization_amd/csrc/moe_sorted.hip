@@ -6,32 +6,30 @@
 //          weight(t, e) * W2_e ( silu(W1_e x[t]) * (W3_e x[t]) )
 //
 // The choices are sorted by expert, so that an expert's tokens are rows of row
-// tiles of its own, which the sort lists.  Two launches that multiply 16-bit rows by
+// tiles of its own, which the sort lists.  Two launches that multiply fp16 rows by
 // packed NVFP4 weights go over that list: the first reads the tokens where they are
 // and makes h = silu(gate) * up, the second makes weight * s2 * W2 h, a row for
-// every choice, and a last launch adds the rows of each token.  Where experts have
-// few rows these are streams of the weights (persistent workgroups), where they
-// have many, matrix tiles; their number is known on the device only, so the tiles'
-// grids are for the most there can be, and workgroups past the last end at once.
+// every choice, and a last launch adds the rows of each token.  The number of row
+// tiles is known on the device only; the grids are for the most there can be, and
+// workgroups past the last tile end at once.
 //
-// Rounded on the way: x to fp16 with a power of two a token (exact, but for values
-// far below the largest); h to bf16, which halves what moves and lets bf16 matrix
-// instructions take it (an error the size of the final rounding's); the rows to the
-// 11 bits of fp16, with a power of two of their own for every 32 columns, for a third
-// error of that size would show.
+// Rounded on the way: h to bf16, which halves what moves (an error the size of the
+// final rounding's); the rows to the 11 bits of fp16, with a power of two of their own
+// for every 32 columns, for a third error of that size would show.  x and h enter the
+// products as fp16 with a power of two a row, exact but for values far below a row's
+// largest.
 //
 // 8 of 128 experts of 7168 x 2048: 100 tokens 0.68 ms (weights and rows that cross
-// memory at 4.7 TB/s: bound by that), 1023 tokens 1.30 ms (bound by neither; the
-// expansion of weights and the matrix products of 64 rows in turn), 8192 tokens 5.7
-// ms (1.01 PFLOP/s, the clocks of the matrix units under full power).
+// memory at 4.7 TB/s, which bounds it), 1023 tokens 1.19 ms (bound by neither memory
+// nor matrix units, which are 39% busy: half the experts have more than 64 rows and
+// are multiplied as 96), 8192 tokens 5.55 ms (1.04 PFLOP/s; the clocks fall to 1.7 GHz
+// under the matrix units' power).
 #include "layer.hpp"
 #include "tile_device.hpp"
 
 namespace nvfp4 {
 
 namespace {
-
-constexpr int kCus = 256;
 
 struct SortedArgs {
   const uint16_t* x;               // fp16 rows of the tokens, [tokens][hidden]
@@ -43,7 +41,7 @@ struct SortedArgs {
   const float* row_scale;          // the token's power of two: value = fp16 * scale
   const uint8_t *p13, *c13, *p2, *c2;
   const float *s13, *s2;
-  uint16_t* h;                     // [rows][inter]
+  uint16_t* h;                     // [rows][inter], bf16, then fp16 (its powers of two go into row_weight)
   uint16_t* ys;                    // fp16 [rows][hidden]
   uint8_t* ye;                     // their exponents, [rows][lde]
   int lde;
@@ -62,15 +60,17 @@ __device__ __forceinline__ float finite_max(const uint4& v, float top) {
   return top;
 }
 
-// Rows of x in fp16 with a power of two each that puts the largest below 2^15: exact,
+// bf16 rows in fp16 with a power of two each that puts the largest below 2^15: exact,
 // but for values 2^29 and more below that, which are rounded to its 2^-39.  fp16
-// weights take half the work of bf16 ones to make, which is most of what a tile of few
-// rows has to do: 100 tokens of 128 experts of 7168 x 2048 (first product) 600 us with
-// x in bf16.
-__global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64_t ldx, int64_t tokens, int pieces,
-                                                        uint16_t* y, float* scale) {
+// weights take half the work of bf16 ones to make, which is much of what a tile of few
+// rows has to do (x: 100 tokens of 128 experts of 7168 x 2048, first product 600 us in
+// bf16, 550 so; h: 698 us of the layer with its own, 672 so, and no more at 8192).
+// Row t goes to y + t cols (which may be x itself); scale[t] gets the power, or is
+// multiplied by it.
+__global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64_t ldx, int64_t rows, int pieces,
+                                                        uint16_t* y, float* scale, bool times) {
   __shared__ float part[4];
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
     const uint4* src = reinterpret_cast<const uint4*>(x + t * ldx);
     float top = 0.f;
     for (int i = threadIdx.x; i < pieces; i += 256) top = finite_max(src[i], top);
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64
         h[z] = (_Float16)(__uint_as_float(z & 1 ? q[z >> 1] & 0xFFFF0000u : q[z >> 1] << 16) * f);
       reinterpret_cast<f16x8*>(y + t * (int64_t)pieces * 8)[i] = h;
     }
-    if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(1.0f, e - kHalfBias);
+    if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(times ? scale[t] : 1.0f, e - kHalfBias);
     __syncthreads();                                 // before the next token's maximum
   }
 }
@@ -102,9 +102,9 @@ struct TileAt { int expert, first, rows, n; };
 // a band, all output rows of the first come before those of the second.  What an XCD's
 // CUs work on at one time is then one or two experts, whose weights its L2 hands to
 // both row tiles (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product
-// fetches 10 GB, 19 where each row tile is on another XCD, and the layer takes 5.68 ms
-// and 5.94).  The list has the longest bands first: the XCDs have as much to do, and
-// what is left at the end is short.
+// fetches 10 GB, 19 where each row tile is on another XCD, and the layer takes 5.59 ms
+// and 5.80).  The list has the bands of most rows first, by 32: the XCDs have as much to
+// do, and what is left at the end is short (1023 tokens 1.25 ms by 128 rows, 1.20 so).
 constexpr int kBandTiles = 2;
 __device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, TileAt& t) {
   constexpr int ROWS = 128;
@@ -129,14 +129,19 @@ __device__ __forceinline__ uint32_t beyond_if(bool cut, uint32_t offset) { retur
 // whose start and end nothing hides: 6.2 ms against 5.9 for 8192 tokens).
 //
 // A stage is 64 channels.  What bounds the tiles of few rows is how many pieces of
-// cache lines are asked for, so weights come two stages at a time, 64 bytes a row
-// (every second stage), and scales eight stages at a time, 32 bytes a row (an eighth
-// of the rows with every stage).  Two of each are kept in LDS, and two stages of x.
+// cache lines are asked for, and how many are on their way: weights come two stages at
+// a time, 64 bytes a row, and scales eight stages at a time, 32 bytes a row (a quarter
+// of the rows with each pair).  LDS keeps two stages of x, pairs of weights and groups
+// of scales, three of the first two in tiles of 32 rows: when something takes a place,
+// what was there has been read.  (256 tokens of 128 experts of 7168 x 2048 776 us, and
+// 1023 1190; one stage of each at a time, 32 and 16 bytes a row, 932 and 1350; a stage
+// of 256 channels, 128 bytes a row, one workgroup of 16 waves a CU, 878 and 1735.)
 struct Tiles {
   static constexpr int TN = 2, WAVES = 4, ROWS = 128, BN = 32 * TN * WAVES, THREADS = 64 * WAVES;
   static constexpr int PAIR = BN * 64, GROUP = BN * 32;          // weights of two stages, scales of eight
   static constexpr int WL = PAIR / 1024 / WAVES;                 // loads of a wave
-  static constexpr int LDS = 2 * (4 * 4096 + PAIR + GROUP);
+  static constexpr int kept(int tm) { return tm == 1 ? 3 : 2; }
+  static constexpr int LDS = 80 * 1024;
 };
 static_assert(Tiles::WAVES * 32 * (64 * Tiles::TN + 16) <= Tiles::LDS && 2 * Tiles::LDS <= 160 * 1024,
               "store staging; two workgroups a CU");
@@ -149,11 +154,11 @@ static_assert(Tiles::WAVES * 32 * (64 * Tiles::TN + 16) <= Tiles::LDS && 2 * Til
 //                  two matrices, whose scales are `pair` bytes apart
 // Lane half h of an instruction takes channels 32 h + 8 j .. + 7 of the stage at step
 // j, so that a lane's weights of a stage are one 16-byte piece.
-template <bool F16, bool PAIRED, int TM, typename XAt, typename WAt, typename Finish>
+template <bool PAIRED, int TM, typename XAt, typename WAt, typename Finish>
 __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XAt x_at, WAt w_at, int stride,
                                          uint32_t scale_bytes, int pair, uint8_t* lds, Finish finish) {
   constexpr int TN = Tiles::TN, WAVES = Tiles::WAVES, WL = Tiles::WL;
-  constexpr int XB = TM * 4096, W_AT = 2 * XB, S_AT = W_AT + 2 * Tiles::PAIR;
+  constexpr int KEPT = Tiles::kept(TM), XB = TM * 4096, W_AT = KEPT * XB, S_AT = W_AT + KEPT * Tiles::PAIR;
   static_assert(S_AT + 2 * Tiles::GROUP <= Tiles::LDS, "stages");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31, end = (k + 63) >> 6;
@@ -173,14 +178,14 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
                       (PAIRED ? (wave >> 1) * pair : 0) + word * 4;
   const int odd = word & 4 ? -16 : 16;
 
-  const auto load_x = [&](int s, auto whole) {
+  const auto load_x = [&](int s, int buf, auto whole) {          // (past k: zeros)
     const bool cut = !whole && s * 64 + xpiece * 8 >= k;
-    const uint32_t dst = lds_wave + (s & 1) * XB;
+    const uint32_t dst = lds_wave + buf * XB;
     each<TM>([&](auto i) { load_lds16<i * WAVES * 1024>(bx, dst, beyond_if(cut, xo[i]), s * 128); });
   };
-  const auto load_w = [&](int p) {                               // (past k: zeros)
+  const auto load_w = [&](int p, int buf) {
     const bool cut = p * 128 + wpiece * 32 >= k;
-    const uint32_t dst = lds_wave + (p & 1) * Tiles::PAIR;
+    const uint32_t dst = lds_wave + buf * Tiles::PAIR;
     each<WL>([&](auto i) { load_lds16<W_AT + i * WAVES * 1024>(bw, dst, beyond_if(cut, wo[i]), p * 64); });
   };
   // (words past a row's end: read, not used; a scalar offset is held to the buffer's
@@ -195,13 +200,13 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   uint4 xr[2][TM], wr[TN], wr_next[TN];
   uint32_t wsr[TN], wsr_next[TN];
   const int x_row = l32 * 128, w_row = (wave * TN * 32 + l32);
-  const auto read_x = [&](int set, int j, int s) {
-    const uint8_t* b = lds + (s & 1) * XB + x_row + (((4 * half + j) ^ swizzle128(l32)) << 4);
+  const auto read_x = [&](int set, int j, int buf) {
+    const uint8_t* b = lds + buf * XB + x_row + (((4 * half + j) ^ swizzle128(l32)) << 4);
 #pragma unroll
     for (int i = 0; i < TM; ++i) xr[set][i] = *reinterpret_cast<const uint4*>(b + i * 4096);
   };
-  const auto read_w = [&](int s) {
-    const uint8_t* b = lds + W_AT + (s >> 1 & 1) * Tiles::PAIR + w_row * 64 + (((2 * (s & 1) + half) ^ swizzle64(l32)) << 4);
+  const auto read_w = [&](int s, int buf) {
+    const uint8_t* b = lds + W_AT + buf * Tiles::PAIR + w_row * 64 + (((2 * (s & 1) + half) ^ swizzle64(l32)) << 4);
     const uint8_t* c = lds + S_AT + (s >> 3 & 1) * Tiles::GROUP + w_row * 32;
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
@@ -219,24 +224,33 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
 
-  // The eighth that is loaded with the end of stage s is s + 9: it is there a stage on,
-  // the last of a group before the group's first stage is read; the group before the
-  // last one has been read when the first is loaded.
+  // What goes on its way at the end of stage s: x of stage s + KEPT, and where s = 2 p + 1
+  // the eighths s + 9 and s + 10 of scales and pair p + KEPT.  A group's last eighths are
+  // there two stages on, before its first stage is read; its first are loaded when the
+  // group in whose place they go has been read.
+  const auto load_behind = [&](int s, int xbuf, int wbuf, auto whole) {
+    load_x(s + KEPT, xbuf, whole);
+    if (s & 1) {
+      load_scales(s + 9);
+      load_scales(s + 10);
+      load_w((s >> 1) + KEPT, wbuf);
+    }
+  };
 #pragma unroll
-  for (int i = 0; i < 9; ++i) load_scales(i);
-  load_x(0, std::false_type{});
-  load_w(0);
-  if (end > 1) {
-    load_x(1, std::false_type{});
-    load_w(1);
-    wait_loads<TM + WL>();
-  } else {
-    wait_loads<0>();
+  for (int i = 0; i < 8; ++i) load_scales(i);
+  load_w(0, 0);
+  load_x(0, 0, std::false_type{});
+  if constexpr (KEPT == 3) {
+    load_w(1, 1);
+    load_x(1, 1, std::false_type{});
   }
+  wait_loads<KEPT == 3 ? WL + TM : 0>();
   stage_barrier();
-  read_w(0);
+  load_behind(-1, KEPT - 1, KEPT - 1, std::false_type{});
+  int xbuf = 0, wbuf = 0;                            // stage s's
+  read_w(0, 0);
   read_x(0, 0, 0);
-  run_stages<2>(0, end, k >> 6, [&](int s, auto way) {
+  const auto step = [&](int s, auto whole, auto last) {
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
       wr[n] = wr_next[n];
@@ -245,31 +259,33 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j < 3) {
-        read_x((j + 1) & 1, j + 1, s);
-      } else if constexpr (way != kLast) {
-        // Stage s + 1 is to be there (the pair of weights behind its x may be on its
-        // way), and all that is read of stage s in registers: s + 2 takes its place.
-        if (way == kDrain || (s & 1)) wait_loads<0>();
-        else wait_loads<WL>();
+        read_x((j + 1) & 1, j + 1, xbuf);
+      } else if constexpr (!last) {
+        // Stage s + 1 is to be there, what comes behind its x may be on its way, and all
+        // that is read of stage s is in registers.
+        if (s & 1) wait_loads<KEPT == 3 ? WL + TM : 0>();
+        else wait_loads<(KEPT == 3 ? TM : 0) + 2 + WL>();
         lds_barrier();
-        if constexpr (way != kDrain) {
-          load_x(s + 2, std::bool_constant<way == kWhole>{});
-          load_scales(s + 9);
-          if (s & 1) load_w((s + 3) >> 1);
-        }
-        read_w(s + 1);
-        read_x(0, 0, s + 1);
+        load_behind(s, xbuf, wbuf, whole);
+        xbuf = xbuf == KEPT - 1 ? 0 : xbuf + 1;
+        if (s & 1) wbuf = wbuf == KEPT - 1 ? 0 : wbuf + 1;
+        read_w(s + 1, wbuf);
+        read_x(0, 0, xbuf);
       }
 #pragma unroll
       for (int n = 0; n < TN; ++n) {
         const uint32_t nib = j == 0 ? wr[n].x : j == 1 ? wr[n].y : j == 2 ? wr[n].z : wr[n].w;
-        const float c = j < 2 ? e4m3_f32<0>(wsr[n]) : e4m3_f32<1>(wsr[n]);
-        const uint4 w = F16 ? fp4x8_f16(nib, splat_f16(c)) : fp4x8_bf16(nib, c);
+        const uint4 w = fp4x8_f16(nib, splat_f16(j < 2 ? e4m3_f32<0>(wsr[n]) : e4m3_f32<1>(wsr[n])));
 #pragma unroll
-        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_16<F16>(w, xr[j & 1][m], acc[n][m]);
+        for (int m = 0; m < TM; ++m) acc[n][m] = mfma32_16<true>(w, xr[j & 1][m], acc[n][m]);
       }
     }
-  });
+  };
+  int s = 0;
+  for (; s + KEPT < k >> 6; ++s) step(s, std::true_type{}, std::false_type{});
+  for (; s + 1 < end; ++s) step(s, std::false_type{}, std::false_type{});
+  step(s, std::false_type{}, std::true_type{});
+  wait_loads<0>();                                               // what is still on its way to LDS
   __syncthreads();                                               // the stages are done with
   finish(acc, wave);
 }
@@ -290,7 +306,6 @@ struct RowValues {
 #pragma unroll
     for (int m = 0; m < TM; ++m) v[m] = by[t.first + min(32 * m + (int)(threadIdx.x & 31), t.rows - 1)] * s;
   }
-  __device__ __forceinline__ explicit RowValues(float one) : v{one} {}
 };
 
 // A wave's part of h: 16 TN channels from ch0 on of the tile's rows (s: what their sums
@@ -399,7 +414,7 @@ __global__ __launch_bounds__(Tiles::THREADS, 2) void moe_up_tile_kernel(SortedAr
   const auto bs = make_buffer(a.c13 + row * a.lds13, bytes_s);
   with_rows(t.rows, [&](auto tm) {
     constexpr int TM = decltype(tm)::value;
-    run_tile<true, true, TM>(
+    run_tile<true, TM>(
         bx, bw, bs, a.hidden, [&](int r) { return (uint32_t)(a.order[t.first + min(r, t.rows - 1)] / a.top_k) * ldx; },
         [&](int r) { return (uint32_t)(min((r >> 5) * 16 + (r & 15), left - 1) + ((r >> 4) & 1) * a.inter) * ldw; },
         a.lds13, bytes_s, a.inter * a.lds13, lds, [&](const f32x16 (&acc)[TN][TM], int wave) {
@@ -424,7 +439,7 @@ __global__ __launch_bounds__(Tiles::THREADS, 2) void moe_down_tile_kernel(Sorted
   const auto bs = make_buffer(a.c2 + row * a.lds2, bytes_s);
   with_rows(t.rows, [&](auto tm) {
     constexpr int TM = decltype(tm)::value;
-    run_tile<false, false, TM>(
+    run_tile<false, TM>(
         bx, bw, bs, a.inter, [&](int r) { return (uint32_t)min(r, t.rows - 1) * ldh; },
         [&](int r) { return (uint32_t)min(r, rows_w - 1) * ldw; }, a.lds2, bytes_s, 0, lds,
         [&](f32x16 (&acc)[TN][TM], int wave) {
@@ -432,181 +447,6 @@ __global__ __launch_bounds__(Tiles::THREADS, 2) void moe_down_tile_kernel(Sorted
                            lds + wave * 32 * (64 * TN + 16));
         });
   });
-}
-
-// ---- few rows an expert ------------------------------------------------------
-//
-// Tiles of up to 32 rows x 256 output rows for experts with few tokens, where the
-// weights, read once, bound the layer.  A stage is 256 channels, so that a row of
-// packed weights or scales is asked for by whole cache lines (of the 64 channels of
-// the other forms, 32 bytes a row, each line is asked for four times) and waves meet
-// a quarter as often.  Eight waves load and multiply, 32 output rows each; one
-// workgroup a CU keeps three stages in LDS, two of them on their way, also from one
-// tile to the next: what the next tile is, is read through the scalar cache, so that
-// nothing waits for it behind the stages in flight.
-struct Stream {
-  static constexpr int ROWS = 32, BN = 256, WAVES = 16, THREADS = 64 * WAVES;
-  static constexpr int WB = BN * 128, XB = ROWS * 512, SB = BN * 16;
-  static constexpr int ROW = WB + XB + SB, STAGE = ROW + 256, BUFS = 3;        // at ROW: a value for each row
-  static constexpr int LDS = BUFS * STAGE;
-  // loads of a wave and stage: twice 8 rows of weights, 2 rows of x, and 64 rows of
-  // scales (waves 0 .. 3) or the rows' values
-  static constexpr int LOADS = 4;
-  // at a tile's end, in the last stage's place: the sums of half the waves, then what
-  // put_h and put_rows turn round
-  static constexpr int TURN = 8 * 4096;
-  static_assert(TURN + 8 * 32 * 80 <= ROW, "the end of a tile");
-};
-
-// A word that all lanes want, past the vector loads in flight.
-__device__ __forceinline__ int scalar_load(const int32_t* p) {
-  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)uniform(reinterpret_cast<const uint8_t*>(p));
-}
-__device__ __forceinline__ float scalar_load(const float* p) {
-  return __uint_as_float((uint32_t)scalar_load(reinterpret_cast<const int32_t*>(p)));
-}
-
-// Tiles at, at + step, ...: the first product (UP: tokens in fp16, output rows in
-// pairs as above) or the second.
-template <bool UP>
-__global__ __launch_bounds__(Stream::THREADS, 4) void moe_stream_kernel(SortedArgs a) {
-  using S = Stream;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S::LDS];
-  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t lds_base = lds_address(lds);
-  constexpr int COLS = UP ? S::BN / 2 : S::BN;                   // of the result, a tile
-  const int k = UP ? a.hidden : a.inter, cols = UP ? a.inter : a.hidden;
-  const int stages = (k + 255) >> 8, tiles_n = (cols + COLS - 1) / COLS;
-  const uint32_t ldw = (uint32_t)k >> 1, lds_s = UP ? a.lds13 : a.lds2;
-  // this workgroup's tiles: of its XCD's bands, in turn (see expert_tile)
-  const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
-  const int bands = scalar_load(a.count);
-  const int tiles = (bands - xcd + 7) / 8 * tiles_n;
-  const auto tile = [&](int i) {
-    const int32_t* b = reinterpret_cast<const int32_t*>(a.bands + (i / tiles_n * 8 + xcd));
-    return TileAt{scalar_load(b), scalar_load(b + 1), scalar_load(b + 2), i % tiles_n};
-  };
-
-  // what is loaded: stage ls of tile lt
-  int lt = blockIdx.x >> 3, ls = 0;
-  i32x4 bx, bw, bs;                                              // bs: scales, or the rows' values
-  const bool has_scales = wave < 4;
-  uint32_t xo, wo0, wo1, so;
-  // channels of the lane's pieces (the same for all its loads)
-  const int xc = (l32 ^ ((2 * wave + half) & 15)) * 8;
-  const int wc = ((lane & 7) ^ swizzle128(wave * 8 + (lane >> 3))) * 32;
-  const auto aim = [&]() {
-    const bool none = lt >= tiles;                               // then loads bring zeros
-    const TileAt t = tile(none ? blockIdx.x >> 3 : lt);
-    const int c0 = t.n * COLS;
-    const int64_t row = (int64_t)t.expert * (UP ? 2 * a.inter : a.hidden) + c0;
-    const int rows_w = UP ? 2 * a.inter - c0 : min(S::BN, cols - c0);
-    const auto w_row = [&](int r) {
-      return UP ? min((r >> 5) * 16 + (r & 15), a.inter - 1 - c0) + ((r >> 4) & 1) * a.inter : min(r, rows_w - 1);
-    };
-    bx = UP ? make_buffer(a.x, a.x_bytes)
-            : make_buffer(a.h + (int64_t)t.first * k, (uint32_t)t.rows * (uint32_t)k * 2);
-    bw = make_buffer((UP ? a.p13 : a.p2) + row * ldw, (uint32_t)rows_w * ldw);
-    bs = has_scales ? make_buffer((UP ? a.c13 : a.c2) + row * lds_s, (uint32_t)rows_w * lds_s)
-                    : make_buffer((UP ? a.row_scale : a.row_weight) + t.first, (uint32_t)t.rows * 4);
-    const auto x_row = [&](int r) {                              // rows r and, for the upper lanes, r + 1
-      const int even = min(r, t.rows - 1), odd = min(r + 1, t.rows - 1);
-      if constexpr (!UP) return half ? odd : even;
-      const int32_t* order = a.order + t.first;
-      const int c0 = scalar_load(order + even) / a.top_k, c1 = scalar_load(order + odd) / a.top_k;
-      return half ? c1 : c0;
-    };
-    const auto w_off = [&](int i) { return (uint32_t)w_row((i * S::WAVES + wave) * 8 + (lane >> 3)) * ldw + wc / 2; };
-    xo = beyond_if(none, (uint32_t)x_row(2 * wave) * (uint32_t)k * 2 + xc * 2);
-    wo0 = beyond_if(none, w_off(0));
-    wo1 = beyond_if(none, w_off(1));
-    so = beyond_if(none, has_scales ? (uint32_t)w_row(wave * 64 + lane) * lds_s : lane * 4);
-  };
-  const auto load_stage = [&](int buf) {
-    const uint32_t dst = lds_base + buf * S::STAGE + wave * 1024;
-    const bool cut = ls == stages - 1;                           // pieces past k: zeros
-    const bool wcut = cut && ls * 256 + wc >= k;
-    constexpr int W = S::WAVES * 1024;
-    load_lds16<0>(bw, dst, beyond_if(wcut, wo0), ls * 128);
-    load_lds16<W>(bw, dst, beyond_if(wcut, wo1), ls * 128);
-    load_lds16<S::WB>(bx, dst, beyond_if(cut && ls * 256 + xc >= k, xo), ls * 512);
-    if (has_scales) load_lds16<S::WB + S::XB>(bs, dst, so, ls * 16);
-    else load_lds4<S::ROW>(bs, lds_base + buf * S::STAGE, so, 0);
-    if (lt < tiles && ++ls == stages) {
-      ls = 0;
-      lt += step;
-      aim();
-    }
-  };
-
-  const int wn = wave & 7, q0 = wave >> 3 << 1;                  // output rows, quarters q0 and q0 + 1 of a stage
-  const int w_at = (wn * 32 + l32) * 128, x_at = S::WB + l32 * 512, s_at = S::WB + S::XB + (wn * 32 + l32) * 16 + q0 * 4;
-  if (lt >= tiles) return;
-  aim();
-  load_stage(0);
-  load_stage(1);
-  int buf = 0;
-  bool landed = false;
-  for (int i = blockIdx.x >> 3; i < tiles; i += step) {
-    const TileAt t = tile(i);
-    f32x16 acc[2];
-#pragma unroll
-    for (int z = 0; z < 2; ++z)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[z][e] = 0.0f;
-    for (int g = 0; g < stages; ++g) {
-      if (!landed) wait_loads<S::LOADS>();
-      landed = false;
-      lds_barrier();                                             // the stage is there, and the one before it read
-      load_stage(buf == 0 ? 2 : buf - 1);
-      const uint8_t* b = lds + buf * S::STAGE;
-      const uint2 codes = *reinterpret_cast<const uint2*>(b + s_at);
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {                              // 64 channels
-        const int q = q0 + z;
-        if (g * 256 + q * 64 >= k) break;
-        const uint4 w = *reinterpret_cast<const uint4*>(b + w_at + (((2 * q + half) ^ swizzle128(l32)) << 4));
-        const uint32_t nib[4] = {w.x, w.y, w.z, w.w};
-        const uint32_t c = (z ? codes.y : codes.x) >> (16 * half);
-        const float s[2] = {e4m3_f32<0>(c), e4m3_f32<1>(c)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 x = *reinterpret_cast<const uint4*>(b + x_at + (((8 * q + 4 * half + j) ^ (l32 & 15)) << 4));
-          const uint4 v = UP ? fp4x8_f16(nib[j], splat_f16(s[j >> 1])) : fp4x8_bf16(nib[j], s[j >> 1]);
-          acc[j & 1] = mfma32_16<UP>(v, x, acc[j & 1]);
-        }
-      }
-      buf = buf == 2 ? 0 : buf + 1;
-    }
-    // The next stage is awaited here: behind the stores it would be awaited with them.
-    wait_loads<S::LOADS>();
-    landed = true;
-    lds_barrier();                                               // the last stage's buffer is free
-    f32x16 sum[1][1];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum[0][0][e] = acc[0][e] + acc[1][e];
-    uint8_t* const last = lds + (buf == 0 ? 2 : buf - 1) * S::STAGE;
-    f32x4* const halves = reinterpret_cast<f32x4*>(last + wn * 4096) + lane;
-    if (q0) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        halves[64 * g] = f32x4{sum[0][0][4 * g], sum[0][0][4 * g + 1], sum[0][0][4 * g + 2], sum[0][0][4 * g + 3]};
-    }
-    lds_barrier();
-    if (q0) continue;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4 v = halves[64 * g];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[0][0][4 * g + e] += v[e];
-    }
-    const RowValues<1> v(reinterpret_cast<const float*>(last + S::ROW)[l32] * scalar_load((UP ? a.s13 : a.s2) + t.expert));
-    uint8_t* const mine = last + S::TURN + wn * 32 * 80;
-    if constexpr (UP) put_h<1, 1>(a, t, sum, v, t.n * COLS + wn * 16, mine);
-    else put_rows<1, 1>(a, t, sum, v, t.n * COLS + wn * 32, mine);
-  }
-  wait_loads<0>();                                               // what is still on its way to LDS
 }
 
 // Rows of scales to rows of whole words, zero past nb.
@@ -623,38 +463,22 @@ __global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* src, int
   }
 }
 
-int run_tiles(const SortedArgs& a, int64_t max_bands, hipStream_t s) {
-  const auto grid = [&](int64_t runs) { return (unsigned)((max_bands + 7) / 8 * 8 * kBandTiles * runs); };
-  moe_up_tile_kernel<<<grid((a.inter + Tiles::BN / 2 - 1) / (Tiles::BN / 2)), Tiles::THREADS, 0, s>>>(a);
-  const int st = launch_status("moe_up_tile_kernel");
-  if (st) return st;
-  moe_down_tile_kernel<<<grid((a.hidden + Tiles::BN - 1) / Tiles::BN), Tiles::THREADS, 0, s>>>(a);
-  return launch_status("moe_down_tile_kernel");
-}
-int run_stream(const SortedArgs& a, hipStream_t s) {
-  moe_stream_kernel<true><<<kCus, Stream::THREADS, 0, s>>>(a);
-  const int st = launch_status("moe_stream_kernel");
-  if (st) return st;
-  moe_stream_kernel<false><<<kCus, Stream::THREADS, 0, s>>>(a);
-  return launch_status("moe_stream_kernel");
+int half_rows(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* y, float* scale, bool times, hipStream_t s) {
+  half_rows_kernel<<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
+  return launch_status("half_rows_kernel");
 }
 constexpr int64_t kPassRows = INT64_C(1) << 17;      // choices of one pass, at most
+static_assert(kBandRows == kBandTiles * Tiles::ROWS, "bands");
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Plan {
   int64_t tokens;                                    // of a pass, at most
-  bool few;                                          // rows an expert: the stream kernel
   int64_t max_bands;                                 // of a pass
   bool pad13, pad2;
   size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, row_weight, row_scale, h, ys, ye, bytes;
 };
 
-int band_rows(const Plan& p) { return p.few ? Stream::ROWS : kBandTiles * Tiles::ROWS; }
-
-// Few rows an expert, us with the stream kernel and in tiles (7168 x 2048, 8 of 128):
-//   rows      6        9        16       22         32         44
-//        692, 847  748, 891  898, 932  1018, 1013  1182, 1051  1372, 1120
 Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inter) {
   Plan p{};
   // a pass's rows of x have 32-bit offsets
@@ -662,10 +486,9 @@ Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, 
   p.tokens = kPassRows / top_k;
   if (p.tokens > most) p.tokens = most;
   if (p.tokens > tokens) p.tokens = tokens;
-  const int64_t n = p.tokens * top_k, per = n / experts;
-  p.few = per <= 20;
+  const int64_t n = p.tokens * top_k;
   // a band is whole, or the last one of an expert that has rows
-  p.max_bands = n / band_rows(p) + (n < experts ? n : experts);
+  p.max_bands = n / kBandRows + (n < experts ? n : experts);
   p.pad13 = hidden % 64 != 0;
   p.pad2 = inter % 64 != 0;
   size_t at = 0;
@@ -718,8 +541,6 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   BandList list{};
   list.bands = reinterpret_cast<ExpertBand*>(base + p.bands);
   list.count = reinterpret_cast<int*>(base + p.count);
-  list.rows = band_rows(p);
-  list.unit = p.few ? Stream::ROWS : Tiles::ROWS;
   list.scales = reinterpret_cast<const float*>(base + p.xs);
   list.row_weight = reinterpret_cast<float*>(base + p.row_weight);
   list.row_scale = reinterpret_cast<float*>(base + p.row_scale);
@@ -748,19 +569,22 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   if (p.pad13 && (st = pad_scales(w.c13, experts * 2 * inter, hidden, base + p.c13, s))) return st;
   if (p.pad2 && (st = pad_scales(w.c2, experts * hidden, inter, base + p.c2, s))) return st;
   a.x = reinterpret_cast<const uint16_t*>(base + p.x);
+  const auto grid = [&](int64_t runs) { return (unsigned)((p.max_bands + 7) / 8 * 8 * kBandTiles * runs); };
   for (int64_t t = 0; t < tokens; t += p.tokens) {
     const int64_t here = tokens - t < p.tokens ? tokens - t : p.tokens;
     a.x_bytes = (uint32_t)(here * hidden * 2);
-    half_rows_kernel<<<(unsigned)here, 256, 0, s>>>(x + t * ldx, ldx, here, (int)(hidden / 8),
-                                                    reinterpret_cast<uint16_t*>(base + p.x),
-                                                    reinterpret_cast<float*>(base + p.xs));
-    if ((st = launch_status("half_rows_kernel"))) return st;
+    if ((st = half_rows(x + t * ldx, ldx, here, hidden, reinterpret_cast<uint16_t*>(base + p.x),
+                        reinterpret_cast<float*>(base + p.xs), false, s)))
+      return st;
     list.weights = weights + t * top_k;
     if ((st = launch_moe_sort(ids + t * top_k, here * top_k, experts, order, place,
                               reinterpret_cast<int32_t*>(base + p.offsets), base + p.sort, list, s)))
       return st;
-    st = p.few ? run_stream(a, s) : run_tiles(a, p.max_bands, s);
-    if (st) return st;
+    moe_up_tile_kernel<<<grid((inter + Tiles::BN / 2 - 1) / (Tiles::BN / 2)), Tiles::THREADS, 0, s>>>(a);
+    if ((st = launch_status("moe_up_tile_kernel"))) return st;
+    if ((st = half_rows(a.h, inter, here * top_k, inter, a.h, list.row_weight, true, s))) return st;
+    moe_down_tile_kernel<<<grid((hidden + Tiles::BN - 1) / Tiles::BN), Tiles::THREADS, 0, s>>>(a);
+    if ((st = launch_status("moe_down_tile_kernel"))) return st;
     if ((st = launch_moe_combine_half(a.ys, a.ye, place, here, top_k, hidden, y + t * ldy, ldy, s))) return st;
   }
   return NVFP4_OK;

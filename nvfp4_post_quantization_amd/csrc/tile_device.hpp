@@ -203,9 +203,7 @@ __device__ __forceinline__ f32x16 mfma32_mx(uint4 a, uint32_t sa, uint4 b, uint3
 // with quarters, 706 without; MXFP4, which has scales of x too, 8192x12288x4096:
 // 252 and 247 us (without quarters the words of 32 rows lie in 16 of the 64 banks:
 // 36 of 99 LDS cycles of a wave and stage of the large tile are their conflicts).
-// PAIRED (with quarters): of 32 rows the first 16 and the others are as many rows
-// of two matrices, `pair` bytes apart.
-template <int RX, int RW, int NW, int AHEAD, bool QUARTERS, bool PAIRED = false>
+template <int RX, int RW, int NW, int AHEAD, bool QUARTERS>
 struct ScaleStages {
   static constexpr int CHUNKS = (RX + RW) / 64, LOADS = (CHUNKS + NW - 1) / NW, GROUP = (RX + RW) * 16;
   static constexpr int GROUPS = AHEAD <= 3 ? 2 : 4, BYTES = GROUPS * GROUP;
@@ -218,12 +216,11 @@ struct ScaleStages {
   int odd;                    // and how far from there in odd quarters
   int end[LOADS];             // the buffers' sizes
   int stride, first;          // bytes of a row; the first stage
-  int pair;
 
   // Rows past the last one read as zero: their results are not stored.
   __device__ __forceinline__ ScaleStages(const TileArgs& a, uint32_t lds, int t0, int rows_x, int o0, int rows_w, int s,
                                          int loader)
-      : stride(a.lds), first(s), pair(0) {
+      : stride(a.lds), first(s) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -237,27 +234,10 @@ struct ScaleStages {
     }
     odd = lane & 1 ? -4 : 4;
   }
-  // Rows of w only: `bytes` of them from `rows` on.
-  __device__ __forceinline__ ScaleStages(const uint8_t* rows, int bytes, int row_bytes, int pair_bytes, uint32_t lds, int s,
-                                         int loader)
-      : stride(row_bytes), first(s), pair(pair_bytes) {
-    static_assert(RX == 0 && QUARTERS, "weights of 16-bit activations");
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int c = (loader + i * NW) % CHUNKS;
-      end[i] = bytes;
-      b[i] = make_buffer(rows, (uint32_t)bytes);
-      dst[i] = lds + c * 1024;
-      at[i] = (uint32_t)(c * (PAIRED ? 32 : 64) + (lane >> 2)) * stride + (lane & 3) * 4;
-    }
-    odd = lane & 1 ? -4 : 4;
-  }
   // (words past a row's end: read, not used; a scalar offset is held to the
   // buffer's size, which keeps the bounds check right)
   __device__ __forceinline__ void load_quarter(int g, int q) const {
-    const int rows = PAIRED ? (q >> 1) * 16 * stride + (q & 1) * pair : q * 16 * stride;
-    const int base = (first + 4 * g) * 4 + rows;
+    const int base = (first + 4 * g) * 4 + q * 16 * stride;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
       load_lds4<0>(b[i], dst[i] + (g & (GROUPS - 1)) * GROUP + q * 256, at[i] + (q & 1 ? odd : 0), min(base, end[i]));
@@ -318,11 +298,11 @@ __device__ __forceinline__ f32x16 mfma32_16(uint4 a, uint4 b, f32x16 c) {
 
 // 16-bit activations x NVFP4 weights: WM x WN waves of 32 TM tokens x 32 TN
 // outputs, stages of 64 channels; NL waves that only load, AHEAD stages ahead.
-template <int TM, int TN, int WM, int WN, int NL, int AHEAD, bool PAIRED = false>
+template <int TM, int TN, int WM, int WN, int NL, int AHEAD>
 struct NvTile {
   static constexpr int NW = WM * WN, LW = NL ? NL : NW, BM = 32 * TM * WM, BN = 32 * TN * WN, NBUF = AHEAD + 1;
   static constexpr int XB = BM * 128, WB = BN * 32, STAGE = XB + WB;
-  using Scales = ScaleStages<0, BN, LW, AHEAD, true, PAIRED>;
+  using Scales = ScaleStages<0, BN, LW, AHEAD, true>;
   static constexpr int XL = BM / 8 / LW, WL = BN / 32 / LW, LOADS = XL + WL + Scales::STAGE_LOADS;
   static constexpr int LDS = NBUF * STAGE + Scales::BYTES, THREADS = 64 * (NW + NL);
   static_assert(BM % (8 * LW) == 0 && BN % (32 * LW) == 0 && LW % 2 == 0, "tile split");

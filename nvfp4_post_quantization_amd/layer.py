@@ -189,10 +189,11 @@ def moe_forward_sorted(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
                        workspace: torch.Tensor | None = None) -> torch.Tensor:
     """moe_forward for any number of tokens (the same arguments): beyond 64 the
     tokens are sorted by expert, silu(W1 x) * (W3 x) is rounded to bf16 and an
-    expert's row to fp16 with a power of two for every 32 columns; x enters as fp16
-    with a power of two for each token (exact but for values 2^29 and more below the
-    token's largest).  out: any row stride of 16-byte multiples; workspace: uint8, at
-    least moe_sorted_workspace_bytes(tokens, top_k, experts, hidden, inter) bytes."""
+    expert's row to fp16 with a power of two for every 32 columns; x and silu(..) *
+    (..) enter the products as fp16 with a power of two a row (exact but for values
+    2^29 and more below the row's largest).  out: any row stride of 16-byte multiples;
+    workspace: uint8, at least moe_sorted_workspace_bytes(tokens, top_k, experts,
+    hidden, inter) bytes."""
     _dev(x, _BF16, "x", 2)
     _dev(ids, torch.int32, "ids", 2)
     _dev(w13_packed, _U8, "w13_packed", 4)

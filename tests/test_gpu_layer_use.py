@@ -294,6 +294,33 @@ def test_values_far_below_their_token_s_largest(tokens):
     assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + off * (1 + HALF) + 2.0 ** -120)
 
 
+@pytest.mark.parametrize("tokens", [70, 700])
+def test_channels_far_below_their_row_s_largest(tokens):
+    """silu * up enters the second product like x the first: what is far below the row's
+    largest is off by 2^-39 of that, also in the columns that do not take the largest."""
+    note(f"layer, small channels, {tokens} tokens")
+    hidden, inter = 64, 96
+    c = experts_test.Case(10, tokens, hidden, inter, 4, 2)
+    rng = np.random.default_rng(11)
+    # gate and up rows of a channel: scales 2^-6 .. 2^8, and zero weights of the first
+    # 16 channels, the largest ones, in the upper half of the outputs
+    c.w[1][:] = (8 + 8 * rng.integers(0, 4, c.w[1].shape)).astype(np.uint8)
+    c.w[1][:, :, :16] = 0x78
+    c.w[4][:, :, hidden // 2:, 0] = 0
+    c.dev = [to_dev_f32(a) if a.dtype == np.float32 else torch.from_numpy(a).to(DEV) for a in c.w]
+    x, wt = F.bf16_bits_to_f64(c.x), c.wt.astype(np.float64)
+    w13, w2 = O.nvfp4_values(*c.w[:3]), O.nvfp4_values(*c.w[3:])[:, 0]
+    with np.errstate(over="ignore"):
+        ref, off = L.moe_forward_sorted(x, c.ids, wt, w13, w2, EPS, HALF + 32 * EPS, 2.0 ** -11)
+    for e in range(4):                                               # 2^-39 of the largest, in every channel
+        t, s = np.nonzero(c.ids == e)
+        with np.errstate(over="ignore"):
+            top = np.abs(silu(x[t] @ w13[e, 0].T) * (x[t] @ w13[e, 1].T)).max(1) * 1.01
+        np.add.at(off, t, (wt[t, s] * top * 2.0 ** -39)[:, None] * np.abs(w2[e]).sum(1))
+    got = _vals(c.run())
+    assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + off * (1 + HALF) + 2.0 ** -120)
+
+
 def test_no_tokens():
     note("no tokens")
     def none(*shape, dtype=torch.bfloat16):
