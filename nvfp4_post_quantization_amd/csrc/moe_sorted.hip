@@ -19,8 +19,8 @@
 // products as fp16 with a power of two a row, exact but for values far below a row's
 // largest.
 //
-// 8 of 128 experts of 7168 x 2048: 100 tokens 0.68 ms (weights and rows that cross
-// memory at 4.7 TB/s, which bounds it), 1023 tokens 1.19 ms (bound by neither memory
+// 8 of 128 experts of 7168 x 2048: 100 tokens 0.66 ms (weights and rows that cross
+// memory at 4.8 TB/s, which bounds it), 1023 tokens 1.17 ms (bound by neither memory
 // nor matrix units, which are 39% busy: half the experts have more than 64 rows and
 // are multiplied as 96), 8192 tokens 5.55 ms (1.04 PFLOP/s; the clocks fall to 1.7 GHz
 // under the matrix units' power).
@@ -129,18 +129,21 @@ __device__ __forceinline__ uint32_t beyond_if(bool cut, uint32_t offset) { retur
 // whose start and end nothing hides: 6.2 ms against 5.9 for 8192 tokens).
 //
 // A stage is 64 channels.  What bounds the tiles of few rows is how many pieces of
-// cache lines are asked for, and how many are on their way: weights come two stages at
-// a time, 64 bytes a row, and scales eight stages at a time, 32 bytes a row (a quarter
-// of the rows with each pair).  LDS keeps two stages of x, pairs of weights and groups
-// of scales, three of the first two in tiles of 32 rows: when something takes a place,
-// what was there has been read.  (256 tokens of 128 experts of 7168 x 2048 776 us, and
-// 1023 1190; one stage of each at a time, 32 and 16 bytes a row, 932 and 1350; a stage
-// of 256 channels, 128 bytes a row, one workgroup of 16 waves a CU, 878 and 1735.)
+// cache lines are asked for, how many are on their way, and how often a line of scales,
+// which serves 32 stages, leaves the L2 between two of them: weights come two stages at
+// a time, 64 bytes a row, and scales eight or sixteen, 32 or 64 bytes a row (parts of
+// the rows with each pair).  LDS keeps two pairs of weights, two groups of scales and
+// two stages of x, three where rows are few; when something takes a place, what was
+// there has been read.  (100, 256 and 1023 tokens of 128 experts of 7168 x 2048 in us:
+// 670, 765, 1165.  Groups of eight stages and three pairs for 32 rows: 690, 785, 1170.
+// A stage of each at a time, 32 and 16 bytes a row: 847, 932, 1350.  A stage of 256
+// channels, 128 bytes a row, one workgroup of 16 waves a CU: 692, 878, 1735.)
 struct Tiles {
   static constexpr int TN = 2, WAVES = 4, ROWS = 128, BN = 32 * TN * WAVES, THREADS = 64 * WAVES;
-  static constexpr int PAIR = BN * 64, GROUP = BN * 32;          // weights of two stages, scales of eight
+  static constexpr int PAIR = BN * 64;                           // weights of two stages
   static constexpr int WL = PAIR / 1024 / WAVES;                 // loads of a wave
-  static constexpr int kept(int tm) { return tm == 1 ? 3 : 2; }
+  static constexpr int x_kept(int tm) { return tm == 1 ? 3 : 2; }             // stages of x; of weights two pairs
+  static constexpr int group(int tm) { return tm <= 2 ? 16 : 8; }             // stages of a group of scales
   static constexpr int LDS = 80 * 1024;
 };
 static_assert(Tiles::WAVES * 32 * (64 * Tiles::TN + 16) <= Tiles::LDS && 2 * Tiles::LDS <= 160 * 1024,
@@ -158,8 +161,9 @@ template <bool PAIRED, int TM, typename XAt, typename WAt, typename Finish>
 __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XAt x_at, WAt w_at, int stride,
                                          uint32_t scale_bytes, int pair, uint8_t* lds, Finish finish) {
   constexpr int TN = Tiles::TN, WAVES = Tiles::WAVES, WL = Tiles::WL;
-  constexpr int KEPT = Tiles::kept(TM), XB = TM * 4096, W_AT = KEPT * XB, S_AT = W_AT + KEPT * Tiles::PAIR;
-  static_assert(S_AT + 2 * Tiles::GROUP <= Tiles::LDS, "stages");
+  constexpr int X = Tiles::x_kept(TM), XB = TM * 4096, W_AT = X * XB, S_AT = W_AT + 2 * Tiles::PAIR;
+  constexpr int G = Tiles::group(TM), GROUP = Tiles::BN * 4 * G, GR = 64 / G;  // GR: rows of scales a wave loads at a time
+  static_assert(S_AT + 2 * GROUP <= Tiles::LDS && (G == 8 || G == 16), "stages");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31, end = (k + 63) >> 6;
   const uint32_t lds_wave = lds_address(lds) + wave * 1024;
@@ -171,12 +175,10 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   for (int i = 0; i < TM; ++i) xo[i] = x_at((wave + i * WAVES) * 8 + (lane >> 3)) + xpiece * 16;
 #pragma unroll
   for (int i = 0; i < WL; ++i) wo[i] = w_at((wave + i * WAVES) * 16 + (lane >> 2)) + wpiece * 16;
-  // Of scales: 8 rows, block 4 e + wave of the tile's; word w of a row lies at place w ^
-  // (row >> 3 & 7), so that 32 rows' words lie in as many banks.
-  const int word = (lane & 7) ^ wave;
-  const uint32_t so = (uint32_t)((PAIRED ? (wave & 1) * 8 : wave * 8) + (lane >> 3)) * stride +
-                      (PAIRED ? (wave >> 1) * pair : 0) + word * 4;
-  const int odd = word & 4 ? -16 : 16;
+  // Of scales: GR rows, block e WAVES + wave of the tile's; word w of a row lies at place
+  // w ^ (row / GR % G), so that 32 rows' words lie in as many banks.
+  const int s_row = wave * GR + lane / G;            // of the first WAVES GR
+  const uint32_t so = (uint32_t)(s_row & (PAIRED ? 15 : 31)) * stride + (PAIRED ? (s_row >> 4) * pair : 0);
 
   const auto load_x = [&](int s, int buf, auto whole) {          // (past k: zeros)
     const bool cut = !whole && s * 64 + xpiece * 8 >= k;
@@ -190,10 +192,11 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   };
   // (words past a row's end: read, not used; a scalar offset is held to the buffer's
   // size, which keeps the bounds check right)
-  const auto load_scales = [&](int i) {                          // eighth i & 7 of group i >> 3
-    const int g = i >> 3, e = i & 7;
-    const uint32_t base = (uint32_t)(g * 32 + e * (PAIRED ? 16 : 32) * stride);
-    load_lds4<S_AT>(bs, lds_address(lds) + (g & 1) * Tiles::GROUP + (e * WAVES + wave) * 256, so + (e & 1 ? odd : 0),
+  const auto load_scales = [&](int i) {                          // part i % G of group i / G
+    const int g = i / G, e = i % G, row = e * WAVES * GR;
+    const uint32_t base = (uint32_t)(g * 4 * G + (PAIRED ? (row >> 5) * 16 * stride + (row >> 4 & 1) * pair : row * stride));
+    load_lds4<S_AT>(bs, lds_address(lds) + (g & 1) * GROUP + (e * WAVES + wave) * 256,
+                    so + (((lane ^ (e * WAVES + wave)) & (G - 1)) << 2),
                     (int)min(base, scale_bytes));
   };
 
@@ -207,11 +210,11 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   };
   const auto read_w = [&](int s, int buf) {
     const uint8_t* b = lds + W_AT + buf * Tiles::PAIR + w_row * 64 + (((2 * (s & 1) + half) ^ swizzle64(l32)) << 4);
-    const uint8_t* c = lds + S_AT + (s >> 3 & 1) * Tiles::GROUP + w_row * 32;
+    const uint8_t* c = lds + S_AT + (s / G & 1) * GROUP + w_row * 4 * G;
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
       wr_next[n] = *reinterpret_cast<const uint4*>(b + n * 2048);
-      wsr_next[n] = *reinterpret_cast<const uint32_t*>(c + n * 1024 + (((s & 7) ^ (4 * n) ^ (l32 >> 3)) << 2));
+      wsr_next[n] = *reinterpret_cast<const uint32_t*>(c + n * 128 * G + (((s % G) ^ (n * 32 / GR) ^ (l32 / GR)) << 2));
     }
   };
   static_assert(TN == 2, "a wave's rows start at a multiple of 64");
@@ -224,29 +227,26 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[n][m][e] = 0.0f;
 
-  // What goes on its way at the end of stage s: x of stage s + KEPT, and where s = 2 p + 1
-  // the eighths s + 9 and s + 10 of scales and pair p + KEPT.  A group's last eighths are
+  // What goes on its way at the end of stage s: x of stage s + X, and where s = 2 p + 1
+  // parts s + G + 1 and s + G + 2 of scales and pair p + 2.  A group's last parts are
   // there two stages on, before its first stage is read; its first are loaded when the
   // group in whose place they go has been read.
   const auto load_behind = [&](int s, int xbuf, int wbuf, auto whole) {
-    load_x(s + KEPT, xbuf, whole);
+    load_x(s + X, xbuf, whole);
     if (s & 1) {
-      load_scales(s + 9);
-      load_scales(s + 10);
-      load_w((s >> 1) + KEPT, wbuf);
+      load_scales(s + G + 1);
+      load_scales(s + G + 2);
+      load_w((s >> 1) + 2, wbuf);
     }
   };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_scales(i);
+  for (int i = 0; i < G; ++i) load_scales(i);
   load_w(0, 0);
   load_x(0, 0, std::false_type{});
-  if constexpr (KEPT == 3) {
-    load_w(1, 1);
-    load_x(1, 1, std::false_type{});
-  }
-  wait_loads<KEPT == 3 ? WL + TM : 0>();
+  if (X == 3) load_x(1, 1, std::false_type{});
+  wait_loads<(X - 2) * TM>();
   stage_barrier();
-  load_behind(-1, KEPT - 1, KEPT - 1, std::false_type{});
+  load_behind(-1, X - 1, 1, std::false_type{});
   int xbuf = 0, wbuf = 0;                            // stage s's
   read_w(0, 0);
   read_x(0, 0, 0);
@@ -263,12 +263,12 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
       } else if constexpr (!last) {
         // Stage s + 1 is to be there, what comes behind its x may be on its way, and all
         // that is read of stage s is in registers.
-        if (s & 1) wait_loads<KEPT == 3 ? WL + TM : 0>();
-        else wait_loads<(KEPT == 3 ? TM : 0) + 2 + WL>();
+        if (s & 1) wait_loads<(X - 2) * TM>();
+        else wait_loads<(X - 2) * TM + 2 + WL>();
         lds_barrier();
         load_behind(s, xbuf, wbuf, whole);
-        xbuf = xbuf == KEPT - 1 ? 0 : xbuf + 1;
-        if (s & 1) wbuf = wbuf == KEPT - 1 ? 0 : wbuf + 1;
+        xbuf = xbuf == X - 1 ? 0 : xbuf + 1;
+        if (s & 1) wbuf ^= 1;
         read_w(s + 1, wbuf);
         read_x(0, 0, xbuf);
       }
@@ -282,7 +282,7 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
     }
   };
   int s = 0;
-  for (; s + KEPT < k >> 6; ++s) step(s, std::true_type{}, std::false_type{});
+  for (; s + X < k >> 6; ++s) step(s, std::true_type{}, std::false_type{});
   for (; s + 1 < end; ++s) step(s, std::false_type{}, std::false_type{});
   step(s, std::false_type{}, std::true_type{});
   wait_loads<0>();                                               // what is still on its way to LDS
