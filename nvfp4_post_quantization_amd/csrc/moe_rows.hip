@@ -28,13 +28,14 @@ namespace {
 // and walks them 64 choices at a time; votes over the bits of the ids find the
 // lanes with the same expert, whose order gives the rows.  Counts are whole
 // numbers, so the result does not depend on who adds first.  One chunk needs no
-// first launch.
+// first launch.  Bound by latency, not by its bytes: 61 x 8 choices of 128 experts 4
+// us, 65536 x 8 12 us (of 6 MB, which cross memory in 1.3).
 constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
 // Choices of a workgroup, at least, where there are several: 1024, and 4 an expert, for
 // every workgroup adds up all counts (1023 x 8 of 128 experts 7.6 us, 10.0 with 4096;
 // 65536 x 8 of 1024 experts 22 us with 4096, 30 with 2048).
 constexpr int kSortChunk = 1024, kSortChunkPerExpert = 4;
-constexpr int kSortAlone = 4096;         // up to this many one workgroup does it
+constexpr int kSortAlone = 4096;         // up to this many one workgroup does it (4096 choices 7.2 us; 5600 in two launches 7.1)
 constexpr int kSortGroups = 256;
 
 struct SortArgs {
@@ -318,7 +319,7 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
 }
 
 // Sums in fp32, one rounding.  All rows of a token are on their way before the
-// first is added.
+// first is added.  Bound by memory: 8192 x 8 rows of 7168, 1.06 GB in 204 us.
 template <typename Rows, int K>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(Rows ys, Units u, int64_t pieces, const int32_t* place,
                                                               const float* weights, int64_t n, int top_k, uint16_t* y,
@@ -351,7 +352,9 @@ int with_places(int top_k, F f) {
   return f(std::integral_constant<int, 16>{});
 }
 
-// One token a workgroup (WAVES = 4) or a wave; K >= top_k sums of products.
+// One token a workgroup (WAVES = 4) or, of short rows, a wave; K >= top_k sums of
+// products, each a token's own, so that no two meet.  Bound by memory: 8192 x 8 rows
+// of 7168, 2.0 GB in 430 us.
 template <int K, int WAVES>
 __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* ys,
                                                                    int64_t ldys, const int32_t* place,

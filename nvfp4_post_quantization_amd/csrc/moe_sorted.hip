@@ -19,9 +19,9 @@
 // products as fp16 with a power of two a row, exact but for values far below a row's
 // largest.
 //
-// 8 of 128 experts of 7168 x 2048: 100 tokens 0.66 ms (weights and rows that cross
-// memory at 4.8 TB/s, which bounds it), 1023 tokens 1.17 ms (bound by neither memory
-// nor matrix units, which are 39% busy: half the experts have more than 64 rows and
+// 8 of 128 experts of 7168 x 2048: 100 tokens 0.62 to 0.67 ms (weights that cross
+// memory at 5 TB/s, which bounds it), 1023 tokens 1.17 ms (bound by neither memory
+// nor matrix units, which are 42% busy: half the experts have more than 64 rows and
 // are multiplied as 96), 8192 tokens 5.55 ms (1.04 PFLOP/s; the clocks fall to 1.7 GHz
 // under the matrix units' power).
 #include "layer.hpp"
@@ -102,8 +102,8 @@ struct TileAt { int expert, first, rows, n; };
 // a band, all output rows of the first come before those of the second.  What an XCD's
 // CUs work on at one time is then one or two experts, whose weights its L2 hands to
 // both row tiles (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product
-// fetches 10 GB, 19 where each row tile is on another XCD, and the layer takes 5.59 ms
-// and 5.80).  The list has the bands of most rows first, by 32: the XCDs have as much to
+// fetches 8 GB, and the layer takes 5.59 ms; 5.80 where each row tile is on another
+// XCD).  The list has the bands of most rows first, by 32: the XCDs have as much to
 // do, and what is left at the end is short (1023 tokens 1.25 ms by 128 rows, 1.20 so).
 constexpr int kBandTiles = 2;
 __device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, TileAt& t) {
