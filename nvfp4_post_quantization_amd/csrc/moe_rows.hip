@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     for (uint32_t i = 0; i < whole; ++i) a.list.bands[at + i] = ExpertBand{tid, (int)(first + i * most), (int)most, 0};
     at = count + __popcll(same & ((1ull << lane) - 1));
 #pragma unroll 1
-    for (int w = 0; w < kSortWaves; ++w)
+    for (int w = 0; w * 64 < E; ++w)                             // (a thread an expert)
 #pragma unroll
       for (uint32_t u = 1; u <= classes; ++u) {
         const uint32_t c = last[w][u - 1];

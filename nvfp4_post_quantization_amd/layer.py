@@ -36,6 +36,8 @@ _SIGS = {
 }
 
 _lib = None
+_I32, _F32 = torch.int32, torch.float32
+_device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def load() -> ctypes.CDLL:
@@ -58,29 +60,44 @@ def load() -> ctypes.CDLL:
 def _call(fn: str, device, *args) -> None:
     """fn(*args, the device's current stream), with the device made current."""
     index, lib = device.index, _lib or load()
-    if torch._C._cuda_getDevice() == index:
-        status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _device_now() == index:
+        status = getattr(lib, fn)(*args, _stream_now(index))
     else:
         with torch.cuda.device(device):
-            status = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = getattr(lib, fn)(*args, _stream_now(index))
     if status:
         _check(fn, status)
 
 
-def _place(place: torch.Tensor) -> tuple[int, int]:
-    """tokens and top_k of a contiguous int32 [tokens, top_k] tensor."""
-    _dev(place, torch.int32, "place", 2)
-    if not place.is_contiguous():
-        raise ValueError("place must be contiguous")
-    return place.shape[0], place.shape[1]
+# Small calls are the host's: each helper asks a good tensor as little as it can (a
+# tenth of such a call) and leaves it to the package's own to say what is wrong.
+
+def _choices(t: torch.Tensor, name: str) -> torch.Size:
+    """(tokens, top_k) of a contiguous int32 [tokens, top_k] tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.is_cuda and t.dim() == 2 and t.is_contiguous()):
+        _dev(t, _I32, name, 2)
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
 
 
-def _rows_in(t: torch.Tensor, rows: int, cols: int | None, name: str, device) -> int:
-    """Row stride of a bf16 [rows, cols] tensor with contiguous rows on `device`."""
-    _dev(t, _BF16, name, 2)
+def _matrix(t: torch.Tensor, dtype, name: str, rows: int, cols: int | None, device) -> tuple[int, int]:
+    """Columns and row stride of a [rows, cols] tensor with contiguous rows on `device`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 2 and t.device == device:
+        have, wide = t.shape
+        ld, one = t.stride()
+        if have == rows and one == 1 and (cols is None or wide == cols):
+            return wide, ld if rows > 1 else wide
+    _dev(t, dtype, name, 2)
     if t.shape[0] != rows or (cols is not None and t.shape[1] != cols) or t.device != device:
         raise ValueError(f"{name} must be [{rows}, {'cols' if cols is None else cols}] on {device}")
-    return _row_major(t, name)
+    return t.shape[1], _row_major(t, name)
+
+
+def _out(out: torch.Tensor | None, dtype, name: str, rows: int, cols: int, device) -> tuple[torch.Tensor, int]:
+    """The [rows, cols] output, made here or checked, and its row stride."""
+    if out is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device), cols
+    return out, _matrix(out, dtype, name, rows, cols, device)[1]
 
 
 def moe_sort_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:
@@ -95,18 +112,16 @@ def moe_sort(ids: torch.Tensor, experts: int, out=None, workspace: torch.Tensor 
     ids[token, s] names no expert), rows of expert e: offsets[e] .. offsets[e+1].
     Choices of an expert stay in their order.  out=(order, place, offsets) reuses
     buffers; workspace: uint8, at least moe_sort_workspace_bytes(...) bytes."""
-    _dev(ids, torch.int32, "ids", 2)
+    tokens, top_k = _choices(ids, "ids")
     dev = ids.device
-    tokens, top_k = ids.shape
-    _flat(ids, torch.int32, (tokens, top_k), "ids", dev)
     if out is None:
-        order = torch.empty(tokens * top_k, dtype=torch.int32, device=dev)
-        place = torch.empty(tokens, top_k, dtype=torch.int32, device=dev)
-        offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=dev)
+        order = torch.empty(tokens * top_k, dtype=_I32, device=dev)
+        place = torch.empty_like(ids)
+        offsets = torch.empty(max(experts, 0) + 1, dtype=_I32, device=dev)
     else:
-        order = _flat(out[0], torch.int32, (tokens * top_k,), "order", dev)
-        place = _flat(out[1], torch.int32, (tokens, top_k), "place", dev)
-        offsets = _flat(out[2], torch.int32, (experts + 1,), "offsets", dev)
+        order = _flat(out[0], _I32, (tokens * top_k,), "order", dev)
+        place = _flat(out[1], _I32, (tokens, top_k), "place", dev)
+        offsets = _flat(out[2], _I32, (experts + 1,), "offsets", dev)
     ws = _scratch(workspace, dev, moe_sort_workspace_bytes, tokens, top_k, experts)
     _call("nvfp4_moe_sort", dev, ids.data_ptr(), tokens, top_k, experts, order.data_ptr(), place.data_ptr(),
           offsets.data_ptr(), ws.data_ptr(), ws.numel())
@@ -118,21 +133,14 @@ def moe_dispatch(x: torch.Tensor, place: torch.Tensor, out: torch.Tensor | None 
     codes) to their sorted rows, [tokens * top_k, cols].  Rows to which no choice
     goes, those behind the last, are not written (without `out` they hold
     anything).  Rows contiguous, any row stride."""
-    tokens, top_k = _place(place)
+    tokens, top_k = _choices(place, "place")
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    _dev(x, x.dtype, "x", 2)
-    cols, size, dev = x.shape[1], x.element_size(), place.device
-    if x.shape[0] != tokens or x.device != dev:
-        raise ValueError(f"x must be [{tokens}, cols] on {dev}")
-    if out is None:
-        out = torch.empty(tokens * top_k, cols, dtype=x.dtype, device=dev)
-    else:
-        _dev(out, x.dtype, "out", 2)
-        if out.shape != (tokens * top_k, cols) or out.device != dev:
-            raise ValueError(f"out must be [{tokens * top_k}, {cols}] on {dev}")
-    _call("nvfp4_moe_dispatch", dev, x.data_ptr(), tokens, cols * size, _row_major(x, "x") * size, place.data_ptr(), top_k,
-          out.data_ptr(), _row_major(out, "out") * size)
+    dev, size, dtype = place.device, x.element_size(), x.dtype
+    cols, ldx = _matrix(x, dtype, "x", tokens, None, dev)
+    out, ldo = _out(out, dtype, "out", tokens * top_k, cols, dev)
+    _call("nvfp4_moe_dispatch", dev, x.data_ptr(), tokens, cols * size, ldx * size, place.data_ptr(), top_k,
+          out.data_ptr(), ldo * size)
     return out
 
 
@@ -142,12 +150,11 @@ def moe_combine(ys: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | N
     rounding), bf16 [tokens, cols] of bf16 ys [tokens * top_k, cols], cols a
     multiple of 8.  Places of -1 add nothing; weights (f32 [tokens, top_k]) None:
     all 1.  ys and out may have any row stride of 16-byte multiples."""
-    tokens, top_k = _place(place)
+    tokens, top_k = _choices(place, "place")
     dev = place.device
-    ld = _rows_in(ys, tokens * top_k, None, "ys", dev)
-    cols = ys.shape[1]
-    w = None if weights is None else _flat(weights, torch.float32, (tokens, top_k), "weights", dev).data_ptr()
-    y, ldy = _rows_out(out, tokens, cols, dev)
+    cols, ld = _matrix(ys, _BF16, "ys", tokens * top_k, None, dev)
+    w = None if weights is None else _flat(weights, _F32, (tokens, top_k), "weights", dev).data_ptr()
+    y, ldy = _out(out, _BF16, "out", tokens, cols, dev)
     _call("nvfp4_moe_combine", dev, ys.data_ptr(), ld, place.data_ptr(), w, tokens, top_k, cols, y.data_ptr(), ldy)
     return y
 
@@ -162,18 +169,17 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, place: torch.Tensor, we
     with dys[place[t, s]] = weights[t, s] * dy[t], dweights f32 [tokens, top_k] =
     <dy[t], ys[place[t, s]]>, 0 where the place is -1).  Rows of dys to which no
     choice goes are not written.  out=(dys, dweights) reuses buffers."""
-    tokens, top_k = _place(place)
+    tokens, top_k = _choices(place, "place")
     dev = place.device
-    lddy = _rows_in(dy, tokens, None, "dy", dev)
-    cols = dy.shape[1]
-    ldys = _rows_in(ys, tokens * top_k, cols, "ys", dev)
-    _flat(weights, torch.float32, (tokens, top_k), "weights", dev)
+    cols, lddy = _matrix(dy, _BF16, "dy", tokens, None, dev)
+    rows = tokens * top_k
+    _, ldys = _matrix(ys, _BF16, "ys", rows, cols, dev)
+    _flat(weights, _F32, (tokens, top_k), "weights", dev)
+    dys, lddys = _out(None if out is None else out[0], _BF16, "dys", rows, cols, dev)
     if out is None:
-        dys, lddys = _rows_out(None, tokens * top_k, cols, dev)
-        dw = torch.empty(tokens, top_k, dtype=torch.float32, device=dev)
+        dw = torch.empty_like(weights)
     else:
-        dys, lddys = _rows_out(out[0], tokens * top_k, cols, dev)
-        dw = _flat(out[1], torch.float32, (tokens, top_k), "dweights", dev)
+        dw = _flat(out[1], _F32, (tokens, top_k), "dweights", dev)
     _call("nvfp4_moe_combine_grad", dev, dy.data_ptr(), lddy, ys.data_ptr(), ldys, place.data_ptr(), weights.data_ptr(),
           tokens, top_k, cols, dys.data_ptr(), lddys, dw.data_ptr())
     return dys, dw
@@ -195,21 +201,21 @@ def moe_forward_sorted(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
     workspace: uint8, at least moe_sorted_workspace_bytes(tokens, top_k, experts,
     hidden, inter) bytes."""
     _dev(x, _BF16, "x", 2)
-    _dev(ids, torch.int32, "ids", 2)
+    _dev(ids, _I32, "ids", 2)
     _dev(w13_packed, _U8, "w13_packed", 4)
     dev = x.device
     tokens, hidden = x.shape
     top_k = ids.shape[1]
     e, _, inter, _ = w13_packed.shape
-    _flat(ids, torch.int32, (tokens, top_k), "ids", dev)
-    _flat(weights, torch.float32, (tokens, top_k), "weights", dev)
+    _flat(ids, _I32, (tokens, top_k), "ids", dev)
+    _flat(weights, _F32, (tokens, top_k), "weights", dev)
     _flat(w13_packed, _U8, (e, 2, inter, hidden // 2), "w13_packed", dev)
     _flat(w13_codes, _U8, (e, 2, inter, hidden // 16), "w13_codes", dev)
-    _flat(w13_scale2, torch.float32, (e,), "w13_scale2", dev)
+    _flat(w13_scale2, _F32, (e,), "w13_scale2", dev)
     mid = (1,) if w2_packed.dim() == 4 else ()
     _flat(w2_packed, _U8, (e, *mid, hidden, inter // 2), "w2_packed", dev)
     _flat(w2_codes, _U8, (e, *mid, hidden, inter // 16), "w2_codes", dev)
-    _flat(w2_scale2, torch.float32, (e,), "w2_scale2", dev)
+    _flat(w2_scale2, _F32, (e,), "w2_scale2", dev)
     y, ldy = _rows_out(out, tokens, hidden, dev)
     ws = _scratch(workspace, dev, moe_sorted_workspace_bytes, tokens, top_k, e, hidden, inter)
     _call("nvfp4_moe_forward_sorted", dev, x.data_ptr(), tokens, hidden, _row_major(x, "x"), ids.data_ptr(),
@@ -242,10 +248,10 @@ def matmul_w4a16_lora(x: torch.Tensor, w_packed: torch.Tensor, w_codes: torch.Te
     _flat(w_packed, _U8, (o, k // 2), "w_packed", dev)
     _flat(w_codes, _U8, (o, k // 16), "w_codes", dev)
     _scalar(w_scale2, "w_scale2", dev)
-    _flat(adapter_ids, torch.int32, (tokens,), "adapter_ids", dev)
+    _flat(adapter_ids, _I32, (tokens,), "adapter_ids", dev)
     _flat(lora_a, _BF16, (adapters, rank, k), "lora_a", dev)
     _flat(lora_b, _BF16, (adapters, o, rank), "lora_b", dev)
-    _flat(lora_scale, torch.float32, (adapters,), "lora_scale", dev)
+    _flat(lora_scale, _F32, (adapters,), "lora_scale", dev)
     y, ldy = _rows_out(out, tokens, o, dev)
     ws = _scratch(workspace, dev, matmul_lora_workspace_bytes, tokens, o, k, rank)
     _call("nvfp4_matmul_w4a16_lora", dev, x.data_ptr(), tokens, k, _row_major(x, "x"), w_packed.data_ptr(),
