@@ -67,13 +67,25 @@ __device__ __forceinline__ float finite_max(const uint4& v, float top) {
 // bf16, 550 so; h: 698 us of the layer with its own, 672 so, and no more at 8192).
 // Row t goes to y + t cols (which may be x itself); scale[t] gets the power, or is
 // multiplied by it.
+// The first 2048 HELD columns stay in registers: read once, all on their way at a time
+// (rows of 2048 columns, 1023 x 8 of them: 16 us with 1, 23 with 4).
+template <int HELD>
 __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64_t ldx, int64_t rows, int pieces,
                                                         uint16_t* y, float* scale, bool times) {
   __shared__ float part[4];
   for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
     const uint4* src = reinterpret_cast<const uint4*>(x + t * ldx);
+    f16x8* const dst = reinterpret_cast<f16x8*>(y + t * (int64_t)pieces * 8);
+    uint4 held[HELD];
+#pragma unroll
+    for (int z = 0; z < HELD; ++z) {
+      const int i = threadIdx.x + 256 * z;
+      held[z] = i < pieces ? src[i] : make_uint4(0, 0, 0, 0);
+    }
     float top = 0.f;
-    for (int i = threadIdx.x; i < pieces; i += 256) top = finite_max(src[i], top);
+#pragma unroll
+    for (int z = 0; z < HELD; ++z) top = finite_max(held[z], top);
+    for (int i = threadIdx.x + 256 * HELD; i < pieces; i += 256) top = finite_max(src[i], top);
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
@@ -81,17 +93,20 @@ __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64
     top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
     const int e = max((int)(__float_as_uint(top) >> 23), 15);
     const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);
-    for (int i = threadIdx.x; i < pieces; i += 256) {
-      const uint4 v = src[i];
+    const auto put = [&](int i, const uint4& v) {
       const uint32_t q[4] = {v.x, v.y, v.z, v.w};
       f16x8 h;
 #pragma unroll
       for (int z = 0; z < 8; ++z)
         h[z] = (_Float16)(__uint_as_float(z & 1 ? q[z >> 1] & 0xFFFF0000u : q[z >> 1] << 16) * f);
-      reinterpret_cast<f16x8*>(y + t * (int64_t)pieces * 8)[i] = h;
-    }
+      dst[i] = h;
+    };
+#pragma unroll
+    for (int z = 0; z < HELD; ++z)
+      if ((int)threadIdx.x + 256 * z < pieces) put(threadIdx.x + 256 * z, held[z]);
+    for (int i = threadIdx.x + 256 * HELD; i < pieces; i += 256) put(i, src[i]);
     if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(times ? scale[t] : 1.0f, e - kHalfBias);
-    __syncthreads();                                 // before the next token's maximum
+    __syncthreads();                                 // before the next row's maximum
   }
 }
 
@@ -464,7 +479,8 @@ __global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* src, int
 }
 
 int half_rows(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* y, float* scale, bool times, hipStream_t s) {
-  half_rows_kernel<<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
+  if (cols <= 2048) half_rows_kernel<1><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
+  else half_rows_kernel<4><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
   return launch_status("half_rows_kernel");
 }
 constexpr int64_t kPassRows = INT64_C(1) << 17;      // choices of one pass, at most

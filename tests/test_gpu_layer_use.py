@@ -321,6 +321,13 @@ def test_channels_far_below_their_row_s_largest(tokens):
     assert np.all(np.abs(got - ref) <= HALF * np.abs(ref) + off * (1 + HALF) + 2.0 ** -120)
 
 
+@pytest.mark.parametrize("tokens,hidden,inter", [(70, 8208, 48), (66, 9232, 32), (70, 48, 8224), (200, 10256, 16)])
+def test_rows_of_more_than_8192_columns(tokens, hidden, inter):
+    note(f"layer, {tokens} tokens, {hidden} -> {inter}")
+    c = experts_test.Case(hidden + inter, tokens, hidden, inter, 3, 2)
+    c.check(c.run())
+
+
 def test_no_tokens():
     note("no tokens")
     def none(*shape, dtype=torch.bfloat16):
