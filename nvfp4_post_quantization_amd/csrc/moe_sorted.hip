@@ -19,8 +19,8 @@
 // products as fp16 with a power of two a row, exact but for values far below a row's
 // largest.
 //
-// 8 of 128 experts of 7168 x 2048: 100 tokens 0.62 to 0.67 ms (weights that cross
-// memory at 5 TB/s, which bounds it), 1023 tokens 1.17 ms (bound by neither memory
+// 8 of 128 experts of 7168 x 2048: 100 tokens 0.62 to 0.63 ms (weights that cross
+// memory at 5 TB/s, which bounds it), 1023 tokens 1.13 ms (bound by neither memory
 // nor matrix units, which are 42% busy: half the experts have more than 64 rows and
 // are multiplied as 96), 8192 tokens 5.55 ms (1.04 PFLOP/s; the clocks fall to 1.7 GHz
 // under the matrix units' power).
