@@ -182,6 +182,7 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31, end = (k + 63) >> 6;
   const uint32_t lds_wave = lds_address(lds) + wave * 1024;
+  const int x_bytes = bx[2], w_bytes = bw[2];        // the buffers' sizes, below 2^31
   // loads of x: 8 rows each; of weights: 16 rows
   uint32_t xo[TM], wo[WL];
   const int xpiece = (lane & 7) ^ swizzle128(wave * 8 + (lane >> 3));
@@ -195,18 +196,23 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   const int s_row = wave * GR + lane / G;            // of the first WAVES GR
   const uint32_t so = (uint32_t)(s_row & (PAIRED ? 15 : 31)) * stride + (PAIRED ? (s_row >> 4) * pair : 0);
 
-  const auto load_x = [&](int s, int buf, auto whole) {          // (past k: zeros)
+  // Loads run ahead of the last stage: past k a lane's offset is beyond the buffer, which
+  // reads as zero, and the scalar offset is held to the buffer's size, without which the
+  // bounds check (lane's offset against size less scalar offset) could wrap: a tile of
+  // one row has 2 k bytes of x, and up to three stages of 128 are loaded past them.
+  const auto load_x = [&](int s, int buf, auto whole) {
     const bool cut = !whole && s * 64 + xpiece * 8 >= k;
     const uint32_t dst = lds_wave + buf * XB;
-    each<TM>([&](auto i) { load_lds16<i * WAVES * 1024>(bx, dst, beyond_if(cut, xo[i]), s * 128); });
+    const int base = min(s * 128, x_bytes);
+    each<TM>([&](auto i) { load_lds16<i * WAVES * 1024>(bx, dst, beyond_if(cut, xo[i]), base); });
   };
   const auto load_w = [&](int p, int buf) {
     const bool cut = p * 128 + wpiece * 32 >= k;
     const uint32_t dst = lds_wave + buf * Tiles::PAIR;
-    each<WL>([&](auto i) { load_lds16<W_AT + i * WAVES * 1024>(bw, dst, beyond_if(cut, wo[i]), p * 64); });
+    const int base = min(p * 64, w_bytes);
+    each<WL>([&](auto i) { load_lds16<W_AT + i * WAVES * 1024>(bw, dst, beyond_if(cut, wo[i]), base); });
   };
-  // (words past a row's end: read, not used; a scalar offset is held to the buffer's
-  // size, which keeps the bounds check right)
+  // (words past a row's end: read, not used)
   const auto load_scales = [&](int i) {                          // part i % G of group i / G
     const int g = i / G, e = i % G, row = e * WAVES * GR;
     const uint32_t base = (uint32_t)(g * 4 * G + (PAIRED ? (row >> 5) * 16 * stride + (row >> 4 & 1) * pair : row * stride));
