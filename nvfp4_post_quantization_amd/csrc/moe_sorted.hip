@@ -13,11 +13,10 @@
 // tiles is known on the device only; the grids are for the most there can be, and
 // workgroups past the last tile end at once.
 //
-// Rounded on the way: h to bf16, which halves what moves (an error the size of the
-// final rounding's); the rows to the 11 bits of fp16, with a power of two of their own
-// for every 32 columns, for a third error of that size would show.  x and h enter the
-// products as fp16 with a power of two a row, exact but for values far below a row's
-// largest.
+// Rounded on the way: h and the rows, both to the 11 bits of fp16 with a power of two of
+// their own for every 32 columns, which halves what moves; in bf16, of the same size,
+// either would be off by as much as y's own rounding.  x and h enter the products as
+// fp16 with a power of two a row, exact but for values far below a row's largest.
 //
 // 8 of 128 experts of 7168 x 2048: 100 tokens 0.62 to 0.63 ms (weights that cross
 // memory at 5 TB/s, which bounds it), 1023 tokens 1.13 ms (bound by neither memory
@@ -41,10 +40,11 @@ struct SortedArgs {
   const float* row_scale;          // the token's power of two: value = fp16 * scale
   const uint8_t *p13, *c13, *p2, *c2;
   const float *s13, *s2;
-  uint16_t* h;                     // [rows][inter], bf16, then fp16 (its powers of two go into row_weight)
+  uint16_t* h;                     // fp16 [rows][inter]
+  uint8_t* he;                     // its exponents, [rows][ldhe], until each row has one (which goes into row_weight)
   uint16_t* ys;                    // fp16 [rows][hidden]
   uint8_t* ye;                     // their exponents, [rows][lde]
-  int lde;
+  int ldhe, lde;
   int top_k, hidden, inter;
   int lds13, lds2;                 // bytes of a row of scales
 };
@@ -60,18 +60,16 @@ __device__ __forceinline__ float finite_max(const uint4& v, float top) {
   return top;
 }
 
-// bf16 rows in fp16 with a power of two each that puts the largest below 2^15: exact,
+// x: bf16 rows in fp16 with a power of two each that puts the largest below 2^15: exact,
 // but for values 2^29 and more below that, which are rounded to its 2^-39.  fp16
 // weights take half the work of bf16 ones to make, which is much of what a tile of few
-// rows has to do (x: 100 tokens of 128 experts of 7168 x 2048, first product 600 us in
-// bf16, 550 so; h: 698 us of the layer with its own, 672 so, and no more at 8192).
-// Row t goes to y + t cols (which may be x itself); scale[t] gets the power, or is
-// multiplied by it.
+// rows has to do (100 tokens of 128 experts of 7168 x 2048, first product 600 us in
+// bf16, 550 so).  Row t goes to y + t cols; scale[t] gets the power.
 // The first 2048 HELD columns stay in registers: read once, all on their way at a time
 // (rows of 2048 columns, 1023 x 8 of them: 16 us with 1, 23 with 4).
 template <int HELD>
 __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64_t ldx, int64_t rows, int pieces,
-                                                        uint16_t* y, float* scale, bool times) {
+                                                        uint16_t* y, float* scale) {
   __shared__ float part[4];
   for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
     const uint4* src = reinterpret_cast<const uint4*>(x + t * ldx);
@@ -105,9 +103,41 @@ __global__ __launch_bounds__(256) void half_rows_kernel(const uint16_t* x, int64
     for (int z = 0; z < HELD; ++z)
       if ((int)threadIdx.x + 256 * z < pieces) put(threadIdx.x + 256 * z, held[z]);
     for (int i = threadIdx.x + 256 * HELD; i < pieces; i += 256) put(i, src[i]);
-    if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(times ? scale[t] : 1.0f, e - kHalfBias);
+    if (threadIdx.x == 0) scale[t] = __builtin_amdgcn_ldexpf(1.0f, e - kHalfBias);
     __syncthreads();                                 // before the next row's maximum
   }
+}
+
+// h: from an exponent for every 32 columns to one a row, their largest, which weight[row]
+// is multiplied by; in place, and only the columns that change.  Exact, but for values
+// 2^29 and more below the row's largest: with h's own rounding they are off by 2^-38 of
+// that at most.  A workgroup a row; those behind the last are left alone.  (8192 x 8 rows
+// of 2048: 84 us, 108 with what is to change asked for when the exponents are there.)
+__global__ __launch_bounds__(256) void one_exponent_kernel(uint16_t* h, const uint8_t* exponents, int lde, int pieces,
+                                                           const int32_t* rows, float* weight) {
+  const int64_t t = blockIdx.x;
+  if ((int)t >= *rows) return;
+  const uint8_t* const of = exponents + t * lde;
+  f16x8* const row = reinterpret_cast<f16x8*>(h + t * (int64_t)pieces * 8);
+  int i = threadIdx.x, e = of[min(i, pieces - 1) >> 2];
+  f16x8 v = row[min(i, pieces - 1)];                 // on its way beside the exponents
+  int top = 0;
+  for (int z = threadIdx.x & 63; z < lde; z += 64) top = max(top, (int)of[z]);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) top = max(top, __shfl_xor(top, m));
+  while (i < pieces) {
+    if (e < top) {                                   // (64 powers below, a finite value is nothing; an infinity stays)
+      const float f = __builtin_amdgcn_ldexpf(1.0f, max(e - top, -64));
+#pragma unroll
+      for (int z = 0; z < 8; ++z) v[z] = (_Float16)((float)v[z] * f);
+      row[i] = v;
+    }
+    i += 256;
+    if (i >= pieces) break;
+    e = of[i >> 2];
+    v = row[i];
+  }
+  if (threadIdx.x == 0) weight[t] = __builtin_amdgcn_ldexpf(weight[t], top - kHalfBias);
 }
 
 // A row tile and run of output rows.
@@ -329,49 +359,13 @@ struct RowValues {
   }
 };
 
-// A wave's part of h: 16 TN channels from ch0 on of the tile's rows (s: what their sums
-// are to be multiplied by), through `mine` in LDS so that whole runs are stored.
-template <int TN, int TM>
-__device__ __forceinline__ void put_h(const SortedArgs& a, const TileAt& t, const f32x16 (&acc)[TN][TM],
-                                      const RowValues<TM>& s, int ch0, uint8_t* mine) {
-  constexpr int PITCH = 32 * TN + 16, LANES = 2 * TN, ROWS = 64 / LANES;
-  const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
-  const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + piece * 8;
-#pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    if (32 * m >= t.rows) break;
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float gate = acc[i][m][4 * g + e] * s.v[m], up = acc[i][m][8 + 4 * g + e] * s.v[m];
-          v[e] = to_bf16(gate / (1.0f + expf(-gate)) * up);
-        }
-        *reinterpret_cast<uint2*>(mine + l32 * PITCH + 32 * i + 16 * g + 2 * sub) =
-            make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-      }
-#pragma unroll
-    for (int r = 0; r < 32; r += ROWS) {
-      const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
-      const int at = 32 * m + r + row0;
-      if (at < t.rows && ch < a.inter) *reinterpret_cast<uint4*>(a.h + (int64_t)(t.first + at) * a.inter + ch) = v;
-    }
-  }
-}
-
-// v *= w; the biased exponent to store for the 32 columns of a token that this lane
-// and the one 32 on hold: that of the largest finite value, at least 14, so that
-// both powers of two are normal floats or, at the end of the range, exact ones.
-__device__ __forceinline__ int half_exponent(f32x16& v, float w) {
+// The biased exponent to store for the 32 columns of a token that this lane and the one
+// 32 on hold: that of the largest finite value, at least 14, so that both powers of
+// two are normal floats or, at the end of the range, exact ones.
+__device__ __forceinline__ int half_exponent(const f32x16& v) {
   float top = 0.f;
 #pragma unroll
-  for (int z = 0; z < 16; ++z) {
-    v[z] *= w;
-    top = fmaxf(top, __builtin_fabsf(v[z]));         // (a NaN is passed over)
-  }
+  for (int z = 0; z < 16; ++z) top = fmaxf(top, __builtin_fabsf(v[z]));       // (a NaN is passed over)
   if (top > 3.40282347e38f) {
     top = 0.f;
 #pragma unroll
@@ -381,6 +375,47 @@ __device__ __forceinline__ int half_exponent(f32x16& v, float w) {
   uint32_t p = __float_as_uint(top), q = p;
   swap32(p, q);
   return max((int)(max(p, q) >> 23), 14);
+}
+// What those columns are multiplied by: the largest comes below 2^15.
+__device__ __forceinline__ float half_factor(int e) { return __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23); }
+__device__ __forceinline__ uint32_t half_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+
+// A wave's part of h: 32 channels from ch0 on of the tile's rows (s: what their sums
+// are to be multiplied by), through `mine` in LDS so that whole runs are stored.
+// (Channels past the last: their up rows' scales are read as zero, so that they are
+// nothing or NaN and do not enter the exponent.)
+template <int TN, int TM>
+__device__ __forceinline__ void put_h(const SortedArgs& a, const TileAt& t, const f32x16 (&acc)[TN][TM],
+                                      const RowValues<TM>& s, int ch0, uint8_t* mine) {
+  static_assert(TN == 2, "one exponent's channels");
+  constexpr int PITCH = 32 * TN + 16, LANES = 2 * TN, ROWS = 64 / LANES;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
+  const int piece = lane % LANES, row0 = lane / LANES, ch = ch0 + piece * 8;
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    if (32 * m >= t.rows) break;
+    f32x16 h;
+#pragma unroll
+    for (int z = 0; z < 16; ++z) {
+      const int i = z >> 3, g = z >> 2 & 1, e = z & 3;
+      const float gate = acc[i][m][4 * g + e] * s.v[m], up = acc[i][m][8 + 4 * g + e] * s.v[m];
+      h[z] = gate / (1.0f + expf(-gate)) * up;
+    }
+    const int exponent = half_exponent(h);
+    const float f = half_factor(exponent);
+#pragma unroll
+    for (int z = 0; z < 16; z += 4)                  // channels 2 z + sub .. + 3
+      *reinterpret_cast<uint2*>(mine + l32 * PITCH + 4 * z + 2 * sub) =
+          make_uint2(half_bits(h[z] * f) | half_bits(h[z + 1] * f) << 16, half_bits(h[z + 2] * f) | half_bits(h[z + 3] * f) << 16);
+    if (sub == 0 && 32 * m + l32 < t.rows && ch0 < a.inter)
+      a.he[(int64_t)(t.first + 32 * m + l32) * a.ldhe + (ch0 >> 5)] = (uint8_t)exponent;
+#pragma unroll
+    for (int r = 0; r < 32; r += ROWS) {
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + (r + row0) * PITCH + piece * 16);
+      const int at = 32 * m + r + row0;
+      if (at < t.rows && ch < a.inter) *reinterpret_cast<uint4*>(a.h + (int64_t)(t.first + at) * a.inter + ch) = v;
+    }
+  }
 }
 
 // A wave's part of the rows: 32 TN outputs from o0 on (w as s).
@@ -396,13 +431,15 @@ __device__ __forceinline__ void put_rows(const SortedArgs& a, const TileAt& t, f
     const int at = t.first + min(32 * m + l32, t.rows - 1);
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
-      const int e = half_exponent(acc[i][m], w.v[m]);
-      const float f = __uint_as_float((uint32_t)(127 + kHalfBias - e) << 23);      // the block's largest below 2^15
+#pragma unroll
+      for (int z = 0; z < 16; ++z) acc[i][m][z] *= w.v[m];
+      const int e = half_exponent(acc[i][m]);
+      const float f = half_factor(e);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         uint32_t v[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) v[z] = __builtin_bit_cast(uint16_t, (_Float16)(acc[i][m][4 * g + z] * f));
+        for (int z = 0; z < 4; ++z) v[z] = half_bits(acc[i][m][4 * g + z] * f);
         *reinterpret_cast<uint2*>(mine + l32 * PITCH + 64 * i + 16 * g + 2 * sub) =
             make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
       }
@@ -484,9 +521,9 @@ __global__ __launch_bounds__(256) void pad_scales_kernel(const uint8_t* src, int
   }
 }
 
-int half_rows(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* y, float* scale, bool times, hipStream_t s) {
-  if (cols <= 2048) half_rows_kernel<1><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
-  else half_rows_kernel<4><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale, times);
+int half_rows(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* y, float* scale, hipStream_t s) {
+  if (cols <= 2048) half_rows_kernel<1><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale);
+  else half_rows_kernel<4><<<(unsigned)rows, 256, 0, s>>>(x, ldx, rows, (int)(cols / 8), y, scale);
   return launch_status("half_rows_kernel");
 }
 constexpr int64_t kPassRows = INT64_C(1) << 17;      // choices of one pass, at most
@@ -498,7 +535,7 @@ struct Plan {
   int64_t tokens;                                    // of a pass, at most
   int64_t max_bands;                                 // of a pass
   bool pad13, pad2;
-  size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, row_weight, row_scale, h, ys, ye, bytes;
+  size_t order, place, offsets, sort, bands, count, c13, c2, x, xs, row_weight, row_scale, h, he, ys, ye, bytes;
 };
 
 Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inter) {
@@ -532,6 +569,7 @@ Plan plan_layer(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, 
   p.row_weight = take(n * 4);
   p.row_scale = take(n * 4);
   p.h = take(n * inter * 2);
+  p.he = take(n * ((inter + 31) / 32));
   p.ys = take(n * hidden * 2);
   p.ye = take(n * ((hidden + 31) / 32));
   p.bytes = at;
@@ -560,6 +598,7 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   SortedArgs a{};
   int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
   int32_t* const place = reinterpret_cast<int32_t*>(base + p.place);
+  int32_t* const offsets = reinterpret_cast<int32_t*>(base + p.offsets);
   BandList list{};
   list.bands = reinterpret_cast<ExpertBand*>(base + p.bands);
   list.count = reinterpret_cast<int*>(base + p.count);
@@ -579,6 +618,8 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
   a.c13 = p.pad13 ? base + p.c13 : w.c13;
   a.c2 = p.pad2 ? base + p.c2 : w.c2;
   a.h = reinterpret_cast<uint16_t*>(base + p.h);
+  a.he = base + p.he;
+  a.ldhe = (int)((inter + 31) / 32);
   a.ys = reinterpret_cast<uint16_t*>(base + p.ys);
   a.ye = base + p.ye;
   a.lde = (int)((hidden + 31) / 32);
@@ -596,15 +637,16 @@ int launch_moe_sorted(const uint16_t* x, int64_t tokens, int64_t hidden, int64_t
     const int64_t here = tokens - t < p.tokens ? tokens - t : p.tokens;
     a.x_bytes = (uint32_t)(here * hidden * 2);
     if ((st = half_rows(x + t * ldx, ldx, here, hidden, reinterpret_cast<uint16_t*>(base + p.x),
-                        reinterpret_cast<float*>(base + p.xs), false, s)))
+                        reinterpret_cast<float*>(base + p.xs), s)))
       return st;
     list.weights = weights + t * top_k;
-    if ((st = launch_moe_sort(ids + t * top_k, here * top_k, experts, order, place,
-                              reinterpret_cast<int32_t*>(base + p.offsets), base + p.sort, list, s)))
+    if ((st = launch_moe_sort(ids + t * top_k, here * top_k, experts, order, place, offsets, base + p.sort, list, s)))
       return st;
     moe_up_tile_kernel<<<grid((inter + Tiles::BN / 2 - 1) / (Tiles::BN / 2)), Tiles::THREADS, 0, s>>>(a);
     if ((st = launch_status("moe_up_tile_kernel"))) return st;
-    if ((st = half_rows(a.h, inter, here * top_k, inter, a.h, list.row_weight, true, s))) return st;
+    one_exponent_kernel<<<(unsigned)(here * top_k), 256, 0, s>>>(a.h, a.he, a.ldhe, (int)(inter / 8), offsets + experts,
+                                                                list.row_weight);
+    if ((st = launch_status("one_exponent_kernel"))) return st;
     moe_down_tile_kernel<<<grid((hidden + Tiles::BN - 1) / Tiles::BN), Tiles::THREADS, 0, s>>>(a);
     if ((st = launch_status("moe_down_tile_kernel"))) return st;
     if ((st = launch_moe_combine_half(a.ys, a.ye, place, here, top_k, hidden, y + t * ldy, ldy, s))) return st;

@@ -96,13 +96,14 @@ NVFP4_CHECKED int nvfp4_moe_combine_grad(const uint16_t* dy, int64_t lddy, const
  * nvfp4_moe_forward for any number of tokens: the same layer and arguments,
  *   y[t] = RN_bf16( sum_s weights[t][s] W2_e ( silu(W1_e x[t]) * (W3_e x[t]) ) ).
  * Up to 64 tokens it is that function's streaming kernels; beyond, the tokens are
- * sorted by expert.  Sums are in fp32 (that over s ascending); before y,
- * silu(..)*(..) is rounded to bf16, and an expert's row, weight included, to fp16 with
- * a power of two for every 32 columns.  x and silu(..)*(..) enter the products as fp16
- * with a power of two for each token (and expert), which is exact but for values 2^29
- * and more below the largest of its row (off by 2^-39 of that at most).  An id outside
- * 0..experts-1 adds nothing; a token without any gets zeros; an expert that a token
- * names twice counts twice.
+ * sorted by expert.  Sums are in fp32 (that over s ascending); before y, silu(..)*(..)
+ * and an expert's row, weight included, are each rounded to fp16 with a power of two
+ * for every 32 columns (11 bits, where y has 8).  x and silu(..)*(..) enter the products
+ * as fp16 with a power of two for each token (and expert), which is exact but for
+ * values 2^29 and more below the largest of its row (x is off by 2^-39 of that at most,
+ * silu(..)*(..), which is rounded before, by 2^-38).  An id outside 0..experts-1 adds
+ * nothing; a token without any gets zeros; an expert that a token names twice counts
+ * twice.
  *
  * Arguments as nvfp4_moe_forward (rows of x and y 16-byte aligned); tokens * top_k
  * at most 2^30; hidden and inter multiples of 16, at most 2^17, their product below

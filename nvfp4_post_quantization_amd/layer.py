@@ -194,10 +194,10 @@ def moe_forward_sorted(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor
                        w2_codes: torch.Tensor, w2_scale2: torch.Tensor, out: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None) -> torch.Tensor:
     """moe_forward for any number of tokens (the same arguments): beyond 64 the
-    tokens are sorted by expert, silu(W1 x) * (W3 x) is rounded to bf16 and an
-    expert's row to fp16 with a power of two for every 32 columns; x and silu(..) *
-    (..) enter the products as fp16 with a power of two a row (exact but for values
-    2^29 and more below the row's largest).  out: any row stride of 16-byte multiples;
+    tokens are sorted by expert, and silu(W1 x) * (W3 x) and an expert's row are each
+    rounded to fp16 with a power of two for every 32 columns; x and silu(..) * (..)
+    enter the products as fp16 with a power of two a row (exact but for values 2^29
+    and more below the row's largest).  out: any row stride of 16-byte multiples;
     workspace: uint8, at least moe_sorted_workspace_bytes(tokens, top_k, experts,
     hidden, inter) bytes."""
     _dev(x, _BF16, "x", 2)
