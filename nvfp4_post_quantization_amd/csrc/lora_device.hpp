@@ -39,13 +39,37 @@ __device__ __forceinline__ bool all_finite(const i32x4& v) {
   return ok;
 }
 
+// Eight bf16 values with zeros for those that are (not) finite.
+template <bool FINITE>
+__device__ __forceinline__ i32x4 only(const i32x4& v) {
+  i32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = (uint32_t)v[e];
+    const bool hi = (x & 0x7F800000u) != 0x7F800000u, lo = (x & 0x7F80u) != 0x7F80u;
+    r[e] = (int)((hi == FINITE ? x & 0xFFFF0000u : 0) | (lo == FINITE ? x & 0xFFFFu : 0));
+  }
+  return r;
+}
+// -1, 0 or 1 by the signs of eight bf16 values.
+__device__ __forceinline__ i32x4 signs(const i32x4& v) {
+  i32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = (uint32_t)v[e];
+    r[e] = (int)((x & 0x80008000u) | (x & 0x7FFF0000u ? 0x3F800000u : 0) | (x & 0x7FFFu ? 0x3F80u : 0));
+  }
+  return r;
+}
+
 // acc (as store_tiles takes it) *= the tensor scale, and the term is added (all waves
 // of the workgroup call this).  The u of the tile's BM tokens go to LDS, 64 ranks at a
 // time, as the operands that they become.  A wave takes the (adapter, 16 ranks) pairs
 // of its tokens one after another, the next two pairs' rows of B on their way; where
 // the channels are split, each split takes its share of the pairs.  Tokens of other
-// adapters have zeros for u, or, where B holds an infinity or NaN, sums of their own
-// that leave them out.
+// adapters have zeros for u.  Infinities and NaN of B are kept out of that (zero times
+// one is NaN, and parts of u are zero, also its tokens' own); sums of their own with
+// the signs of u, which its first part has, are then added to those of their tokens.
 //
 // It runs once a tile, so that its instructions come from memory more often than not:
 // loops stay rolled up.  61 tokens of 64 adapters of 4096x12288, rank 16, take 46 us,
@@ -84,6 +108,11 @@ __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out,
     // pairs: adapter a (-1: no more), ranks from r on
     struct Pair { int a, r; i32x4 w[TN]; };
     int a = multiplies ? 0 : -1, r = ranks, count = -1;
+    // (past the last rank, and for no pair: some row, which is not used)
+    const auto load_b = [&](int a, int r, int n) {
+      return *reinterpret_cast<const i32x4*>(l.b + ((int64_t)a * out + min(o0 + 32 * n + l32, out - 1)) * l.rank +
+                                             min(c0 + r + 8 * half, l.rank - 8));
+    };
     const auto next_pair = [&]() {
       Pair p;
       if (a >= 0) {
@@ -103,12 +132,8 @@ __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out,
       }
       p.a = a;
       p.r = r;
-      // (past the last rank, and for no pair: some row, which is not used)
-      const int rank = min(c0 + r + 8 * half, l.rank - 8);
 #pragma unroll
-      for (int n = 0; n < TN; ++n)
-        p.w[n] = *reinterpret_cast<const i32x4*>(l.b + ((int64_t)max(a, 0) * out + min(o0 + 32 * n + l32, out - 1)) * l.rank +
-                                                 rank);
+      for (int n = 0; n < TN; ++n) p.w[n] = load_b(max(a, 0), r, n);
       return p;
     };
     Pair next = next_pair(), after = next_pair();
@@ -149,6 +174,9 @@ __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out,
         finite &= all_finite(b[n]);
       }
       finite = !__ballot(!finite);
+      if (__builtin_expect(!finite, 0))
+#pragma unroll
+        for (int n = 0; n < TN; ++n) b[n] = only<true>(b[n]);
       const uint8_t* u = lds + (row0 + l32) * PITCH + (now.r + 8 * half) * 2;
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
@@ -160,24 +188,28 @@ __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out,
           x[z] = *reinterpret_cast<const i32x4*>(u + z * PART + m * 32 * PITCH);
           x[z] = mine ? x[z] : i32x4{0, 0, 0, 0};
         }
-        if (__builtin_expect(finite || !__ballot(!mine && id[m] != -2), 1)) {
 #pragma unroll
-          for (int z = 0; z < 3; ++z)
+        for (int z = 0; z < 3; ++z)
 #pragma unroll
-            for (int n = 0; n < TN; ++n)
-              acc[n][m] = mfma32_16<false>(__builtin_bit_cast(uint4, b[n]), __builtin_bit_cast(uint4, x[z]), acc[n][m]);
-        } else {
+          for (int n = 0; n < TN; ++n)
+            acc[n][m] = mfma32_16<false>(__builtin_bit_cast(uint4, b[n]), __builtin_bit_cast(uint4, x[z]), acc[n][m]);
+      }
+      if (__builtin_expect(finite, 1)) continue;
 #pragma unroll
-          for (int n = 0; n < TN; ++n) {
-            f32x16 sum;
+      for (int n = 0; n < TN; ++n) {
+        // (its rows of B once more: kept from before, they cost every call registers)
+        const i32x4 w = only<false>(in ? load_b(now.a, now.r, n) : i32x4{0, 0, 0, 0});
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+        for (int m = 0; m < TM; ++m) {
+          const bool mine = id[m] == now.a;
+          if (!__ballot(mine)) continue;
+          const i32x4 x = signs(*reinterpret_cast<const i32x4*>(u + m * 32 * PITCH));
+          f32x16 sum;
 #pragma unroll
-            for (int z = 0; z < 3; ++z)
-              sum = mfma32_16<false>(__builtin_bit_cast(uint4, b[n]), __builtin_bit_cast(uint4, x[z]), sum);
+          for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+          sum = mfma32_16<false>(__builtin_bit_cast(uint4, w), __builtin_bit_cast(uint4, x), sum);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[n][m][e] += mine ? sum[e] : 0.f;
-          }
+          for (int e = 0; e < 16; ++e) acc[n][m][e] += mine ? sum[e] : 0.f;
         }
       }
     }

@@ -111,7 +111,9 @@ template <int TN, int TM>
 __device__ __forceinline__ void store_tiles(const TileArgs& a, const f32x16 (&acc)[TN][TM], int o0, int t0, int split,
                                             uint8_t* lds) {
   constexpr int PITCH = 64 * TN + 16, LANES = 4 * TN, ROWS = 64 / LANES;       // lanes per row, rows per store
-  const int lane = threadIdx.x & 63, l32 = lane & 31, sub = 4 * (lane >> 5);
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));                     // the places are worked out here, not kept in registers
+  const int l32 = lane & 31, sub = 4 * (lane >> 5);
   if (a.splits > 1) {
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
