@@ -157,6 +157,10 @@ InnerPlan plan_inner(int64_t tokens, int64_t k) {
   return p;
 }
 
+// Tokens of a launch: 512 threads for every 32 of them, of fewer than 2^32 (with more the
+// launch takes them modulo 2^32, without an error).
+constexpr int64_t kLaunchTokens = INT64_C(1) << 27;
+
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
@@ -172,17 +176,21 @@ int launch_w4a16_lora(const uint16_t* x, int64_t tokens, int64_t k, int64_t ldx,
   float* u = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                       align256(product_workspace_bytes(tokens, out, k, false)));
   const int64_t part = tokens * ad.rank;
-  const InnerArgs p{x, ldx, ad.ids, ad.a, ad.scale, u, part, (int)tokens, (int)k, ad.count, ad.rank, plan.splits};
-  const dim3 grid((unsigned)((tokens + plan.tokens - 1) / plan.tokens), plan.splits, plan.slots);
-  if (plan.tokens == 16) {
-    if (ad.rank <= 16) lora_inner_kernel<1, 1, 4, 8><<<grid, 512, 0, s>>>(p);
-    else lora_inner_kernel<1, 4, 4, 8><<<grid, 512, 0, s>>>(p);
-  } else {
-    if (ad.rank <= 16) lora_inner_kernel<2, 1, 4, 8><<<grid, 512, 0, s>>>(p);
-    else lora_inner_kernel<2, 4, 2, 8><<<grid, 512, 0, s>>>(p);
+  for (int64_t t = 0; t < tokens; t += kLaunchTokens) {
+    const int64_t here = tokens - t < kLaunchTokens ? tokens - t : kLaunchTokens;
+    const InnerArgs p{x + t * ldx, ldx, ad.ids + t, ad.a, ad.scale, u + t * ad.rank, part, (int)here, (int)k, ad.count, ad.rank,
+                      plan.splits};
+    const dim3 grid((unsigned)((here + plan.tokens - 1) / plan.tokens), plan.splits, plan.slots);
+    if (plan.tokens == 16) {
+      if (ad.rank <= 16) lora_inner_kernel<1, 1, 4, 8><<<grid, 512, 0, s>>>(p);
+      else lora_inner_kernel<1, 4, 4, 8><<<grid, 512, 0, s>>>(p);
+    } else {
+      if (ad.rank <= 16) lora_inner_kernel<2, 1, 4, 8><<<grid, 512, 0, s>>>(p);
+      else lora_inner_kernel<2, 4, 2, 8><<<grid, 512, 0, s>>>(p);
+    }
+    const int st = launch_status("lora_inner_kernel");
+    if (st) return st;
   }
-  const int st = launch_status("lora_inner_kernel");
-  if (st) return st;
   const LoraTerm l{ad.ids, u, ad.b, ws2, part, ad.count, ad.rank, plan.splits};
   return launch_matmul_w4a16(x, tokens, k, ldx, wp, wc, ws2, out, y, ldy, workspace, s, &l);
 }
