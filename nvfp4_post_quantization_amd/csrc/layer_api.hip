@@ -90,6 +90,10 @@ static int check_expert_sizes(int64_t hidden, int64_t inter) {
   if (hidden <= 0 || inter <= 0 || hidden % 16 || inter % 16 || hidden > most || inter > most) return NVFP4_ERR_BAD_SHAPE;
   return hidden * inter >= INT64_C(1) << 31 ? NVFP4_ERR_BAD_SHAPE : NVFP4_OK;
 }
+// Up to kMoeMaxTokens tokens it is nvfp4_moe_forward's kernels and its bits: they round
+// neither silu(..)*(..) nor an expert's row.  8 of 128 experts of 7168 x 2048, weights
+// cold, us, with them and sorted: 1 token 94 and 136, 4 tokens 234 and 249, 16 tokens
+// 505 and 520, 32 tokens 647 and 655, 48 tokens 735 and 701, 64 tokens 816 and 721.
 static size_t layer_workspace(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, int64_t inter) {
   return tokens <= kMoeMaxTokens ? moe_workspace_bytes(tokens, top_k, inter)
                                  : moe_sorted_workspace_bytes(tokens, top_k, experts, hidden, inter);

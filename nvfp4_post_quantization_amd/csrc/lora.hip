@@ -13,8 +13,8 @@
 // own adapter.  Where tokens follow in runs of a request that is one pass over x.
 // The waves of a workgroup add up their channels in LDS; what other
 // workgroups have of the same tokens are the splits that the product adds up.  Bound
-// by the wait for x and A: 8192 tokens of 4096 channels, rank 64, 31 us, 2.2 TB/s of
-// x (64 tokens and 4 waves a workgroup: 48 us).
+// by the wait for x and A: 8192 tokens of 4096 channels, rank 64, 35 us, 1.9 TB/s of
+// x (64 tokens and 4 waves a workgroup took half as long again).
 #include "layer.hpp"
 #include "lora_device.hpp"
 

@@ -72,10 +72,10 @@ __device__ __forceinline__ i32x4 signs(const i32x4& v) {
 // the signs of u, which its first part has, are then added to those of their tokens.
 //
 // It runs once a tile, so that its instructions come from memory more often than not:
-// loops stay rolled up.  61 tokens of 64 adapters of 4096x12288, rank 16, take 46 us,
-// 59 with four pairs at a time unrolled and the splits' shares of the channels alone;
-// 8192 tokens of 12288x4096, rank 64, 768 us, 682 of them without the adapters and 31
-// of them u.
+// loops stay rolled up.  61 tokens of 64 adapters of 4096x12288, rank 16, take 45 us (22
+// without adapters), 59 with four pairs at a time unrolled and the splits' shares of the
+// channels alone; 8192 tokens of 12288x4096, rank 64, in a graph of such calls 812 us
+// and 672 without adapters (on a slower card 856 and 735), 35 of them u.
 template <int TN, int TM, int BM, int LDS, int THREADS>
 __device__ __forceinline__ void add_lora(const LoraTerm& l, int tokens, int out, f32x16 (&acc)[TN][TM], bool multiplies,
                                          int o0, int tile0, int row0, int split_at, int splits, uint8_t* lds) {

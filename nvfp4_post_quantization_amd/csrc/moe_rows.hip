@@ -29,7 +29,8 @@ namespace {
 // lanes with the same expert, whose order gives the rows.  Counts are whole
 // numbers, so the result does not depend on who adds first.  One chunk needs no
 // first launch.  Bound by latency, not by its bytes: 61 x 8 choices of 128 experts 4
-// us, 65536 x 8 12 us (of 6 MB, which cross memory in 1.3).
+// us, 65536 x 8 12 us (of 6 MB, which cross memory in 1.2), of which a trace gives the
+// first launch 4 to 5 and the second 10.
 constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
 // Choices of a workgroup, at least, where there are several: 1024, and 4 an expert, for
 // every workgroup adds up all counts (1023 x 8 of 128 experts 7.6 us, 10.0 with 4096;
@@ -250,9 +251,11 @@ __device__ __forceinline__ void rows_of_token(const int32_t* place, int64_t t, i
   }
 }
 
-// Rows that are more than the 256 MB MALL can hand on are kept out of it: dispatch of
-// 8192x8x7168 (940 MB) 212 us, so 190, and combine 202 and 195; of 8192x8x2048 (268
-// MB) 51 and 54, and 51 and 58.
+// Rows that are more than the 256 MB MALL can hand on are kept out of it.  8192x8x7168
+// (940 MB), call after call: dispatch 216 us without that, 193 so, combine 205 and 197,
+// one after the other in turn 439 and 391.  (After 768 MB of other data were written:
+// dispatch 222 and 253, combine 259 and 212.)  8192x8x2048 (268 MB) took 51 and 54, and
+// 51 and 58.
 constexpr int64_t kPastMall = INT64_C(1) << 29;
 typedef uint32_t Word4 __attribute__((ext_vector_type(4)));
 
@@ -319,7 +322,7 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
 }
 
 // Sums in fp32, one rounding.  All rows of a token are on their way before the
-// first is added.  Bound by memory: 8192 x 8 rows of 7168, 1.06 GB in 204 us.
+// first is added.  Bound by memory: 8192 x 8 rows of 7168, 1.06 GB in 197 us.
 template <typename Rows, int K>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(Rows ys, Units u, int64_t pieces, const int32_t* place,
                                                               const float* weights, int64_t n, int top_k, uint16_t* y,

@@ -18,11 +18,13 @@
 // either would be off by as much as y's own rounding.  x and h enter the products as
 // fp16 with a power of two a row, exact but for values far below a row's largest.
 //
-// 8 of 128 experts of 7168 x 2048: 100 tokens 0.62 to 0.63 ms (weights that cross
-// memory at 5 TB/s, which bounds it), 1023 tokens 1.13 ms (bound by neither memory
-// nor matrix units, which are 42% busy: half the experts have more than 64 rows and
-// are multiplied as 96), 8192 tokens 5.55 ms (1.04 PFLOP/s; the clocks fall to 1.7 GHz
-// under the matrix units' power).
+// 8 of 128 experts of 7168 x 2048, by the card (a library's bf16 product of 8192^3 makes
+// 1.18 to 1.37 PFLOP/s on them): 100 tokens 0.62 to 0.65 ms (weights that cross memory
+// at 5 TB/s), 1023 tokens 1.13 to 1.20 ms (bound by neither memory nor matrix units,
+// which are 42% busy: half the experts have more than 64 rows and are multiplied as
+// 96), 8192 tokens 5.64 to 5.93 ms (0.97 to 1.02 PFLOP/s; the clocks fall to 1.7 GHz
+// under the matrix units' power).  Figures of one comparison below are of one card, and
+// of the form that the kernels had when it was made.
 #include "layer.hpp"
 #include "tile_device.hpp"
 
@@ -147,9 +149,9 @@ struct TileAt { int expert, first, rows, n; };
 // a band, all output rows of the first come before those of the second.  What an XCD's
 // CUs work on at one time is then one or two experts, whose weights its L2 hands to
 // both row tiles (8192 tokens, 8 of 128 experts of 7168 x 2048: the first product
-// fetches 8 GB, and the layer takes 5.59 ms; 5.80 where each row tile is on another
-// XCD).  The list has the bands of most rows first, by 32: the XCDs have as much to
-// do, and what is left at the end is short (1023 tokens 1.25 ms by 128 rows, 1.20 so).
+// fetches 8 GB; the layer took 5.80 ms with each row tile on another XCD, 5.59 so).  The
+// list has the bands of most rows first, by 32: the XCDs have as much to do, and what
+// is left at the end is short (1023 tokens 1.25 ms by 128 rows, 1.20 so).
 constexpr int kBandTiles = 2;
 __device__ __forceinline__ bool expert_tile(const SortedArgs& a, int tiles_n, TileAt& t) {
   constexpr int ROWS = 128;

@@ -310,8 +310,8 @@ struct NvTile {
   static_assert(BM % (8 * LW) == 0 && BN % (32 * LW) == 0 && LW % 2 == 0, "tile split");
 };
 
-// Which of the waves that load this one is (0 for one that only multiplies: its
-// places are worked out, and rows of theirs must be rows that there are).
+// Which of the waves that load this one is (0 for one that only multiplies: it works
+// out places of rows too, though it loads none).
 template <int NW, int NL>
 __device__ __forceinline__ int loader_of() {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -1,6 +1,8 @@
 """Binding of libnvfp4mi_layer.so (include/nvfp4mi_layer.h beside this file):
 tokens sorted by expert and back, the expert layer for any number of tokens, and
-low-rank adapters beside a W4A16 product.  Its functions are the package's.
+low-rank adapters beside a W4A16 product.  Its functions are the package's, and like
+those plain calls: autograd records none of them, and a gradient is the call that
+makes it (moe_dispatch_grad, moe_combine_grad).
 """
 from __future__ import annotations
 
