@@ -231,7 +231,7 @@ __device__ __forceinline__ void run_tile(i32x4 bx, i32x4 bw, i32x4 bs, int k, XA
   // Loads run ahead of the last stage: past k a lane's offset is beyond the buffer, which
   // reads as zero, and the scalar offset is held to the buffer's size, without which the
   // bounds check (lane's offset against size less scalar offset) could wrap: a tile of
-  // one row has 2 k bytes of x, and up to three stages of 128 are loaded past them.
+  // one row has 2 k bytes of x, and a stage that begins behind them is loaded all the same.
   const auto load_x = [&](int s, int buf, auto whole) {
     const bool cut = !whole && s * 64 + xpiece * 8 >= k;
     const uint32_t dst = lds_wave + buf * XB;
